@@ -1,4 +1,5 @@
-"""ctypes binding of ``libpdrsplat.so`` (the C ABI in ``include/pdr_splat.h``).
+"""ctypes binding of ``libpdrsplat.so`` (the C ABI in ``include/pdr_splat.h``
+and ``include/pdr_dense.h``).
 
 Argument marshalling only: every function here forwards to the entry point of
 the same name and turns a negative status into :class:`PdrError`.  Pointers
@@ -49,7 +50,84 @@ EXPORTED = (
     "pdr_splat_backward_algo",
 )
 
+EXPORTED_DENSE = (
+    "pdr_dense_kept_ld",
+    "pdr_linear_forward_workspace_bytes",
+    "pdr_linear_forward",
+    "pdr_linear_backward_workspace_bytes",
+    "pdr_linear_backward",
+    "pdr_gated_mlp_forward_workspace_bytes",
+    "pdr_gated_mlp_forward",
+    "pdr_gated_mlp_backward_workspace_bytes",
+    "pdr_gated_mlp_backward",
+    "pdr_orthogonalize_workspace_bytes",
+    "pdr_orthogonalize",
+)
+
 KERNEL_COUNT = 14
+
+
+def _struct(name, spec):
+    """A C struct from "type name" lines (the layouts of pdr_dense.h)."""
+    kinds = {"int": ctypes.c_int, "len": ctypes.c_longlong, "ptr": ctypes.c_void_p,
+             "float": ctypes.c_float}
+    fields = []
+    for line in spec.strip().splitlines():
+        kind, names = line.split(None, 1)
+        fields += [(n.strip(), kinds[kind]) for n in names.split(",")]
+    return type(name, (ctypes.Structure,), {"_fields_": fields})
+
+
+pdr_linear = _struct("pdr_linear", """
+    int fmt, out_fmt, activation
+    len M, N, K
+    ptr x
+    len ldx
+    ptr w
+    len ldw
+    ptr bias, res
+    len ldr
+    ptr y
+    len ldy
+    ptr slope, dy
+    len lddy
+    ptr dx
+    len lddx
+    ptr dw
+    len lddw
+    ptr dbias""")
+
+pdr_gated_mlp = _struct("pdr_gated_mlp", """
+    int fmt, activation
+    len M, D, F, O
+    ptr x
+    len ldx
+    ptr w_in
+    len ld_in
+    ptr w_out
+    len ld_out
+    ptr res
+    len ldr
+    ptr y
+    len ldy
+    ptr h, gu, dy
+    len lddy
+    ptr dx
+    len lddx
+    ptr dw_in
+    len ldd_in
+    ptr dw_out
+    len ldd_out""")
+
+pdr_orthogonalize_args = _struct("pdr_orthogonalize_args", """
+    int fmt
+    len batch, m, n
+    ptr g
+    len ldg, batch_g
+    ptr x
+    len ldx, batch_x
+    int steps
+    float a, b, c, eps""")
 
 
 class PdrError(RuntimeError):
@@ -133,6 +211,15 @@ def lib() -> ctypes.CDLL:
         L.pdr_splat_backward_fmt.restype = i
         L.pdr_splat_backward_algo.argtypes = [vp, vp, i, vp, i, i, i, i, i, f, vp, sz, i, i, vp]
         L.pdr_splat_backward_algo.restype = i
+        L.pdr_dense_kept_ld.argtypes = [ll]
+        L.pdr_dense_kept_ld.restype = ll
+        for name, args in (("pdr_linear_forward", pdr_linear), ("pdr_linear_backward", pdr_linear),
+                           ("pdr_gated_mlp_forward", pdr_gated_mlp),
+                           ("pdr_gated_mlp_backward", pdr_gated_mlp),
+                           ("pdr_orthogonalize", pdr_orthogonalize_args)):
+            size, call = getattr(L, name + "_workspace_bytes"), getattr(L, name)
+            size.argtypes, size.restype = [ctypes.POINTER(args)], ll
+            call.argtypes, call.restype = [ctypes.POINTER(args), vp, sz, vp], i
         _lib = L
     return _lib
 
@@ -302,3 +389,55 @@ def pdr_splat_backward_algo(params, grad_image, grad_format, grad_params, B, N, 
                                                 B, N, H, W, C, float(radius), workspace,
                                                 workspace_bytes, int(reuse_binning), int(algo),
                                                 stream), "pdr_splat_backward_algo")
+
+
+PDR_ACT_NONE, PDR_ACT_RELU, PDR_ACT_SILU, PDR_ACT_GELU = 0, 1, 2, 3
+
+
+def pdr_dense_kept_ld(n) -> int:
+    return _raise(lib().pdr_dense_kept_ld(int(n)), "pdr_dense_kept_ld")
+
+
+def pdr_linear_forward_workspace_bytes(args) -> int:
+    return _raise(lib().pdr_linear_forward_workspace_bytes(args), "pdr_linear_forward")
+
+
+def pdr_linear_forward(args, workspace, workspace_bytes, stream):
+    return _raise(lib().pdr_linear_forward(args, workspace, workspace_bytes, stream),
+                  "pdr_linear_forward")
+
+
+def pdr_linear_backward_workspace_bytes(args) -> int:
+    return _raise(lib().pdr_linear_backward_workspace_bytes(args), "pdr_linear_backward")
+
+
+def pdr_linear_backward(args, workspace, workspace_bytes, stream):
+    return _raise(lib().pdr_linear_backward(args, workspace, workspace_bytes, stream),
+                  "pdr_linear_backward")
+
+
+def pdr_gated_mlp_forward_workspace_bytes(args) -> int:
+    return _raise(lib().pdr_gated_mlp_forward_workspace_bytes(args), "pdr_gated_mlp_forward")
+
+
+def pdr_gated_mlp_forward(args, workspace, workspace_bytes, stream):
+    return _raise(lib().pdr_gated_mlp_forward(args, workspace, workspace_bytes, stream),
+                  "pdr_gated_mlp_forward")
+
+
+def pdr_gated_mlp_backward_workspace_bytes(args) -> int:
+    return _raise(lib().pdr_gated_mlp_backward_workspace_bytes(args), "pdr_gated_mlp_backward")
+
+
+def pdr_gated_mlp_backward(args, workspace, workspace_bytes, stream):
+    return _raise(lib().pdr_gated_mlp_backward(args, workspace, workspace_bytes, stream),
+                  "pdr_gated_mlp_backward")
+
+
+def pdr_orthogonalize_workspace_bytes(args) -> int:
+    return _raise(lib().pdr_orthogonalize_workspace_bytes(args), "pdr_orthogonalize")
+
+
+def pdr_orthogonalize(args, workspace, workspace_bytes, stream):
+    return _raise(lib().pdr_orthogonalize(args, workspace, workspace_bytes, stream),
+                  "pdr_orthogonalize")

@@ -9,12 +9,15 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = ["csrc/bin.hip", "csrc/raster.hip", "csrc/loss.hip", "csrc/adapter.hip", "csrc/span.hip",
            "csrc/abi.hip",
-           "csrc/timing.hip"]
+           "csrc/timing.hip", "csrc/dense.hip", "csrc/dense_gemm_bf16.hip",
+           "csrc/dense_gemm_f16.hip"]
 LIB = os.path.join(PKG, "libpdrsplat.so")
 
 HIPCC_FLAGS = [
@@ -32,16 +35,28 @@ def hipcc() -> str:
 
 def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"),
-           *[os.path.join(PKG, s) for s in SOURCES], "-o", tmp]
+    flags = [hipcc(), *HIPCC_FLAGS]
+    with tempfile.TemporaryDirectory() as objs:
+        def compile_one(src):
+            obj = os.path.join(objs, os.path.basename(src) + ".o")
+            _run([f for f in flags if f != "-shared"]
+                 + ["-I", os.path.join(ROOT, "include"), "-c", os.path.join(PKG, src), "-o", obj],
+                 verbose)
+            return obj
+        with ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+            built = list(ex.map(compile_one, SOURCES))
+        _run([*flags, *built, "-o", tmp], verbose)
+    os.replace(tmp, LIB)
+    return LIB
+
+
+def _run(cmd, verbose: bool):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError("hipcc failed building %s" % LIB)
-    os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

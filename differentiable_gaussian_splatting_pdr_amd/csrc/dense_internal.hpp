@@ -1,0 +1,24 @@
+// dense_internal.hpp -- what the dense operators' translation units share.
+#pragma once
+
+#include "dense_gemm.hpp"
+
+namespace pdr {
+namespace dense {
+
+// Launch one product (dense_gemm_*.hip: one file per operand format).  g's
+// tile counts and splits are chosen here; `ws` is scratch for split sums of
+// gemm_scratch_bytes() bytes.
+hipError_t launch_gemm_bf16(GemmArgs g, bool a_mc, bool b_mc, EpiKind kind, void *ws, hipStream_t st);
+hipError_t launch_gemm_f16(GemmArgs g, bool a_mc, bool b_mc, EpiKind kind, void *ws, hipStream_t st);
+size_t gemm_scratch_bytes(const GemmArgs &g, EpiKind kind);
+
+struct TilePlan {
+  int tiles_m, tiles_n, splits;
+};
+TilePlan plan_tiles(const GemmArgs &g, EpiKind kind);
+
+inline long long round8(long long n) { return (n + 7) & ~7LL; }
+
+}  // namespace dense
+}  // namespace pdr

@@ -1,0 +1,142 @@
+/*
+ * pdr_dense.h -- C ABI of the dense operators beside the splatting layer: the
+ * network that predicts the Gaussians' raw values, and the heavy part of the
+ * optimiser that trains it, on MI355X (gfx950).
+ *
+ *   linear         z = x w^T + bias,  y = act(z) + res
+ *   gated block    [g | u] = x w_in^T,  h = act(g) * u,  y = h w_out^T + res
+ *   orthogonalize  the Newton-Schulz products of the Muon optimiser
+ *
+ * Conventions, in addition to pdr_splat.h's (device pointers owned by the
+ * caller, no allocation, asynchronous on `stream`, arguments checked before
+ * anything is enqueued, workspaces 256-byte aligned):
+ *
+ *  - Operands are PDR_FMT_F32, PDR_FMT_F16 or PDR_FMT_BF16, all of one format
+ *    unless said otherwise.  Sums are held in fp32 and rounded once.  fp32
+ *    operands are split into two fp16 planes (22 bits under a power-of-two
+ *    scale per tensor; values below 2^-38 of the tensor's largest lose
+ *    relative accuracy) and multiplied as hi*hi + hi*lo + lo*hi; an infinity
+ *    in an fp32 operand makes the results it reaches not finite, as NaN or as
+ *    an infinity.
+ *  - Matrices are row-major; ld* is the distance between rows in elements
+ *    (>= the row's length, <= 2^22).  Rows that begin on 16 bytes (and, where
+ *    a row is summed along, hold a multiple of 8 values) are read in place;
+ *    others are copied into the workspace first.
+ *  - A length may be 0: sums over nothing are 0, and matrices without
+ *    elements may be NULL.  Every length is below 2^31.
+ *  - Results do not depend on the run: no atomics, one fixed order of sums
+ *    for given sizes and alignments.
+ *  - The *_workspace_bytes functions read the same struct as the call (sizes,
+ *    strides and the pointers' alignment) and return bytes or a negative
+ *    pdr_status.
+ */
+#ifndef PDR_DENSE_H
+#define PDR_DENSE_H
+
+#include <stddef.h>
+
+#include "pdr_splat.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* silu z sigmoid(z); gelu z Phi(z) with the error function. */
+typedef enum {
+    PDR_ACT_NONE = 0, PDR_ACT_RELU = 1, PDR_ACT_SILU = 2, PDR_ACT_GELU = 3
+} pdr_activation;
+
+/* Rows of the tensors a forward keeps for its gradient (slope, h, gu) are
+ * this many elements apart for a length of n. */
+long long pdr_dense_kept_ld(long long n);
+
+/* ------------------------------------------------------------------------ */
+/* Linear: x [M][K], w [N][K], bias [N] or NULL (format fmt); res [M][N] or
+ * NULL, y [M][N] (format out_fmt: fmt or PDR_FMT_F32).  slope, if not NULL,
+ * receives act'(z) for the backward: [M][kept_ld(N)], fp16 where fmt is bf16
+ * (11 bits of a value in (-0.2, 1.2): below bf16's own rounding), else fp32.
+ * Not used without an activation. */
+typedef struct {
+    int fmt, out_fmt, activation;
+    long long M, N, K;
+    const void *x; long long ldx;
+    const void *w; long long ldw;
+    const void *bias;
+    const void *res; long long ldr;
+    void *y; long long ldy;
+    void *slope;
+    /* backward only; a gradient that is NULL is not computed */
+    const void *dy; long long lddy;   /* format out_fmt */
+    void *dx; long long lddx;         /* [M][K], format fmt */
+    void *dw; long long lddw;         /* [N][K], format fmt */
+    void *dbias;                      /* [N], format fmt */
+} pdr_linear;
+
+long long pdr_linear_forward_workspace_bytes(const pdr_linear *p);
+int pdr_linear_forward(const pdr_linear *p, void *workspace, size_t workspace_bytes, void *stream);
+
+/* dz = dy act'(z) (rounded to fmt where it enters the products), dx = dz w,
+ * dw = dz^T x, dbias = sum of dz over rows.  The residual's gradient is dy. */
+long long pdr_linear_backward_workspace_bytes(const pdr_linear *p);
+int pdr_linear_backward(const pdr_linear *p, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Gated feed-forward block: x [M][D], w_in [2F][D] (gate rows, then up rows),
+ * w_out [O][F], res and y [M][O].  h [M][kept_ld(F)] (format fmt) receives the
+ * gated product; gu, if not NULL, the gate and up sums for the backward, fp32
+ * [M][2][kept_ld(F)]. */
+typedef struct {
+    int fmt, activation;
+    long long M, D, F, O;
+    const void *x; long long ldx;
+    const void *w_in; long long ld_in;
+    const void *w_out; long long ld_out;
+    const void *res; long long ldr;
+    void *y; long long ldy;
+    void *h;
+    void *gu;
+    /* backward only; h and gu as the forward left them; a gradient that is
+     * NULL is not computed */
+    const void *dy; long long lddy;
+    void *dx; long long lddx;         /* [M][D] */
+    void *dw_in; long long ldd_in;    /* [2F][D] */
+    void *dw_out; long long ldd_out;  /* [O][F] */
+} pdr_gated_mlp;
+
+long long pdr_gated_mlp_forward_workspace_bytes(const pdr_gated_mlp *p);
+int pdr_gated_mlp_forward(const pdr_gated_mlp *p, void *workspace, size_t workspace_bytes,
+                          void *stream);
+/* dh = dy w_out, dg = dh u act'(g), du = dh act(g), dx = [dg | du] w_in,
+ * dw_in = [dg | du]^T x, dw_out = dy^T h.  dg and du are rounded to fmt. */
+long long pdr_gated_mlp_backward_workspace_bytes(const pdr_gated_mlp *p);
+int pdr_gated_mlp_backward(const pdr_gated_mlp *p, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Newton-Schulz orthogonalisation of each [m][n] matrix of a batch:
+ *   X = G / (|G|_F + eps);  `steps` times: A = X X^T (X^T X where m > n),
+ *   X <- a X + (b A + c A^2) X
+ * The iterates are held in fp16 under a power-of-two scale (singular values
+ * stay near 1, so 11 bits serve a bf16 result where bf16's 8 would not), in
+ * two planes (22 bits) for fp16 and fp32 results.  The polynomial must keep
+ * the iterates' singular values below 8, as Muon's (3.4445, -4.775, 2.0315)
+ * does.  steps >= 0; with 0 the result is G / (|G|_F + eps). */
+typedef struct {
+    int fmt;                          /* of g and x */
+    long long batch, m, n;
+    const void *g; long long ldg, batch_g;
+    void *x; long long ldx, batch_x;  /* may not alias g */
+    int steps;
+    float a, b, c, eps;
+} pdr_orthogonalize_args;
+
+long long pdr_orthogonalize_workspace_bytes(const pdr_orthogonalize_args *p);
+int pdr_orthogonalize(const pdr_orthogonalize_args *p, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* PDR_DENSE_H */

@@ -1,0 +1,175 @@
+"""Host-side checks of the dense operators' C ABI (no GPU): names, struct
+layouts, workspace sizes, and refusals before anything is enqueued."""
+import ctypes
+import os
+import re
+import subprocess
+import sys
+
+import pytest
+
+from differentiable_gaussian_splatting_pdr_amd import _lib
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "pdr_dense.h")
+FAKE = 0x10000  # 256-byte aligned, never dereferenced on these paths
+
+
+def header():
+    return re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+
+
+def test_names():
+    declared = sorted(set(re.findall(r"\b(pdr_\w+)\s*\(", header())))
+    assert declared == sorted(_lib.EXPORTED_DENSE)
+    for f in declared:
+        assert hasattr(_lib.lib(), f)
+
+
+def test_struct_layouts_match_the_header(tmp_path):
+    lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "pdr_dense.h"', "int main(void) {"]
+    for name in ("pdr_linear", "pdr_gated_mlp", "pdr_orthogonalize_args"):
+        lines.append('printf("%s %%zu\\n", sizeof(%s));' % (name, name))
+        for f, _ in getattr(_lib, name)._fields_:
+            lines.append('printf("%s.%s %%zu\\n", offsetof(%s, %s));' % (name, f, name, f))
+    lines.append("return 0; }")
+    src, exe = tmp_path / "layout.c", tmp_path / "layout"
+    src.write_text("\n".join(lines))
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"), str(src), "-o",
+                    str(exe)], check=True)
+    said = dict(line.split() for line in subprocess.run([str(exe)], capture_output=True, text=True,
+                                                        check=True).stdout.splitlines())
+    for name in ("pdr_linear", "pdr_gated_mlp", "pdr_orthogonalize_args"):
+        cls = getattr(_lib, name)
+        assert int(said[name]) == ctypes.sizeof(cls)
+        for f, _ in cls._fields_:
+            assert int(said[name + "." + f]) == getattr(cls, f).offset, f
+
+
+def linear(**kw):
+    a = _lib.pdr_linear()
+    for k, v in dict(fmt=2, out_fmt=2, activation=0, M=64, N=32, K=128, x=FAKE, ldx=128, w=FAKE, ldw=128,
+                     y=FAKE, ldy=32, dy=FAKE, lddy=32).items():
+        setattr(a, k, v)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def gated(**kw):
+    a = _lib.pdr_gated_mlp()
+    for k, v in dict(fmt=2, activation=2, M=64, D=32, F=96, O=32, x=FAKE, ldx=32, w_in=FAKE, ld_in=32,
+                     w_out=FAKE, ld_out=96, y=FAKE, ldy=32, h=FAKE, gu=FAKE, dy=FAKE, lddy=32, dx=FAKE,
+                     lddx=32).items():
+        setattr(a, k, v)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def ortho(**kw):
+    a = _lib.pdr_orthogonalize_args()
+    for k, v in dict(fmt=0, batch=2, m=10, n=20, g=FAKE, ldg=20, batch_g=200, x=FAKE, ldx=20, batch_x=200,
+                     steps=5, a=3.4, b=-4.7, c=2.0, eps=1e-7).items():
+        setattr(a, k, v)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def refused(name, a, code=-1):
+    L = _lib.lib()
+    size = getattr(L, name + "_workspace_bytes")(ctypes.byref(a))
+    if code == -1:
+        assert size == -1
+    assert getattr(L, name)(ctypes.byref(a), None, 0, None) == code
+
+
+BIG = 1 << 23
+LINEAR_BAD = [dict(fmt=3), dict(fmt=-1), dict(out_fmt=1), dict(fmt=0, out_fmt=2, x=FAKE), dict(activation=4),
+              dict(activation=-1), dict(M=-1), dict(N=1 << 31), dict(K=-5), dict(x=None), dict(w=None),
+              dict(x=FAKE + 1), dict(ldx=127), dict(ldw=BIG), dict(slope=FAKE + 8)]
+
+
+@pytest.mark.parametrize("kw", LINEAR_BAD + [dict(y=None), dict(ldy=31), dict(y=FAKE + 1), dict(res=FAKE, ldr=3),
+                                             dict(res=FAKE + 1, ldr=32), dict(bias=FAKE + 1)])
+def test_linear_forward_refuses(kw):
+    refused("pdr_linear_forward", linear(**kw))
+
+
+@pytest.mark.parametrize("kw", LINEAR_BAD + [dict(dy=None), dict(lddy=31), dict(dx=FAKE, lddx=100),
+                                             dict(dw=FAKE, lddw=5), dict(dw=FAKE + 1, lddw=128),
+                                             dict(dbias=FAKE + 1), dict(activation=2)])
+def test_linear_backward_refuses(kw):
+    refused("pdr_linear_backward", linear(**kw))
+
+
+GATED_BAD = [dict(fmt=5), dict(activation=9), dict(M=-1), dict(D=-1), dict(F=-1), dict(O=-1), dict(x=None),
+             dict(w_in=None), dict(w_out=None), dict(ldx=31), dict(ld_in=31), dict(ld_out=95), dict(h=None),
+             dict(h=FAKE + 8), dict(gu=FAKE + 4), dict(F=1 << 22)]
+
+
+@pytest.mark.parametrize("kw", GATED_BAD + [dict(y=None), dict(ldy=31), dict(res=FAKE, ldr=31)])
+def test_gated_forward_refuses(kw):
+    refused("pdr_gated_mlp_forward", gated(**kw))
+
+
+@pytest.mark.parametrize("kw", GATED_BAD + [dict(dy=None), dict(lddy=3), dict(lddx=31), dict(gu=None),
+                                            dict(dw_in=FAKE, ldd_in=3), dict(dw_out=FAKE, ldd_out=95)])
+def test_gated_backward_refuses(kw):
+    refused("pdr_gated_mlp_backward", gated(**kw))
+
+
+@pytest.mark.parametrize("kw", [dict(fmt=7), dict(batch=-1), dict(batch=65536), dict(m=-1), dict(n=-1), dict(g=None),
+                                dict(x=None), dict(ldg=19), dict(ldx=19), dict(steps=-1), dict(a=float("inf")),
+                                dict(b=float("nan")), dict(eps=-1.0), dict(eps=float("nan")), dict(m=BIG),
+                                dict(g=FAKE + 2)])
+def test_orthogonalize_refuses(kw):
+    refused("pdr_orthogonalize", ortho(**kw))
+
+
+def test_null_structs_and_workspaces():
+    L = _lib.lib()
+    for name in ("pdr_linear_forward", "pdr_linear_backward", "pdr_gated_mlp_forward", "pdr_gated_mlp_backward",
+                 "pdr_orthogonalize"):
+        assert getattr(L, name + "_workspace_bytes")(None) == -1
+        assert getattr(L, name)(None, FAKE, 1 << 30, None) == -1
+    a = ortho()
+    need = L.pdr_orthogonalize_workspace_bytes(ctypes.byref(a))
+    assert need > 0
+    for ws, size in ((None, need), (FAKE, need - 1), (FAKE + 16, need)):
+        assert L.pdr_orthogonalize(ctypes.byref(a), ws, size, None) == _lib.PDR_ERR_WORKSPACE
+
+
+def test_workspace_bytes():
+    L = _lib.lib()
+    # in place: rows on 16 bytes, a multiple of 8 long, results enough to fill the card
+    a = linear(M=8192, N=2048, K=128, ldy=2048)
+    assert L.pdr_linear_forward_workspace_bytes(ctypes.byref(a)) == 0
+    # a row that is not a multiple of 8 long: both operands are copied to padded rows
+    b = linear(M=8192, N=2048, K=125, ldy=2048)
+    assert L.pdr_linear_forward_workspace_bytes(ctypes.byref(b)) == (8192 + 2048) * 128 * 2
+    assert _lib.pdr_dense_kept_ld(0) == 0 and _lib.pdr_dense_kept_ld(1) == 8 and _lib.pdr_dense_kept_ld(16) == 16
+    with pytest.raises(_lib.PdrError):
+        _lib.pdr_dense_kept_ld(-1)
+
+
+def test_cpu_tensors_are_refused():
+    code = r'''
+import torch
+from differentiable_gaussian_splatting_pdr_amd import dense
+x = torch.zeros(4, 8)
+for f in (lambda: dense.linear(x, x), lambda: dense.gated_mlp(x, x, x), lambda: dense.orthogonalize(x)):
+    try:
+        f()
+    except ValueError as e:
+        assert "ROCm device" in str(e)
+    else:
+        raise SystemExit("ran on the CPU")
+try:
+    dense.Muon([torch.zeros(3, requires_grad=True)])
+except ValueError:
+    print("refused")
+'''
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0 and "refused" in r.stdout, r.stdout + r.stderr
