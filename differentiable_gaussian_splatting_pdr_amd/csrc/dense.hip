@@ -338,7 +338,7 @@ void multiply(Walk &w, const GemmArgs &g, int fmt, bool a_mc, bool b_mc, EpiKind
 void set_out(Epi &e, void *y, int fmt, long long ldy) {
   e.y = y;
   e.fmt = fmt;
-  e.ldy = ldy;
+  e.ldy = (int)ldy;
   e.vec = aligned16(y) && (ldy & 7) == 0;
 }
 
@@ -378,12 +378,12 @@ void linear_forward(Walk &w, const pdr_linear &p) {
   g.epi.bias = p.bias;
   g.epi.bias_fmt = p.fmt;
   g.epi.res = p.res;
-  g.epi.ldr = p.ldr;
+  g.epi.ldr = (int)p.ldr;
   g.epi.vec = g.epi.vec && (!p.bias || aligned16(p.bias)) && (!p.res || (aligned16(p.res) && (p.ldr & 7) == 0));
   g.epi.act = p.activation;
   g.epi.slope = p.slope;
   g.epi.slope_fmt = slope_fmt(p.fmt);
-  g.epi.ld_slope = round8(p.N);
+  g.epi.ld_slope = (int)round8(p.N);
   multiply(w, g, p.fmt, false, false, kEpiLinear);
 }
 
@@ -478,7 +478,7 @@ void gated_forward(Walk &w, const pdr_gated_mlp &p) {
     g.epi.exp_b = wi.exp;
     g.epi.act = p.activation;
     g.epi.gu = (float *)p.gu;
-    g.epi.ld_gu = Fp;
+    g.epi.ld_gu = (int)Fp;
     multiply(w, g, p.fmt, false, false, kEpiGated);
     w.at = keep;
   }
@@ -490,7 +490,7 @@ void gated_forward(Walk &w, const pdr_gated_mlp &p) {
   g.epi.exp_a = h.exp;
   g.epi.exp_b = wo.exp;
   g.epi.res = p.res;
-  g.epi.ldr = p.ldr;
+  g.epi.ldr = (int)p.ldr;
   g.epi.vec = g.epi.vec && (!p.res || (aligned16(p.res) && (p.ldr & 7) == 0));
   multiply(w, g, p.fmt, false, false, kEpiLinear);
 }
@@ -520,12 +520,12 @@ void gated_backward(Walk &w, const pdr_gated_mlp &p) {
     add_product(g, dy, 0, wo, 0);
     set_out(g.epi, dgu, p.fmt, 2 * Fp);
     g.epi.store_n = (int)Fp;
-    g.epi.up_at = Fp;
+    g.epi.up_at = (int)Fp;
     g.epi.exp_a = dy.exp;
     g.epi.exp_b = wo.exp;
     g.epi.act = p.activation;
     g.epi.gu = (float *)p.gu;
-    g.epi.ld_gu = Fp;
+    g.epi.ld_gu = (int)Fp;
     multiply(w, g, p.fmt, false, true, kEpiGatedGrad);
     w.at = keep;
   }
@@ -621,7 +621,7 @@ void orthogonalize(Walk &w, const pdr_orthogonalize_args &p) {
     e.beta = beta;
     e.c = c.hi;
     e.c_lo = c.lo;
-    e.ldc = c.ld;
+    e.ldc = (int)c.ld;
     e.batch_c = batch;
   };
   for (int i = 0; i < p.steps; ++i) {
@@ -750,27 +750,64 @@ int pdr_orthogonalize(const pdr_orthogonalize_args *p, void *workspace, size_t w
 
 }  // extern "C"
 
-// How a product is cut into workgroups: 128x128 tiles, and where those are
-// too few for 256 compute units, the contraction in several parts, joined by
-// a second kernel.
+// How a product is cut into workgroups: 256x256 tiles, one workgroup on a
+// compute unit, or 128x128 tiles, two; and the contraction in one part or in
+// several, which a second kernel joins.  The choice is the least of an
+// estimate in microseconds whose constants are fits to measured products
+// (bf16, M x N x K, this card): a step is 64 contraction values of every
+// workgroup in flight.
+//   128: 2048x2048x2048 (256 workgroups) 22.9, 1024x1024x4096 (64) 34.2,
+//        4096x2048x2048 (512) 34.0, 8192x1024x2816 (512) 43.7
+//   256: 8192x1024x512 (128) 23.9, 16384x1024x1024 (256) 36.7,
+//        16384x2048x11264 (512, two rounds) 582; the same in 128 tiles: 687
+//   parts: 2048x2048x11264 in 256 tiles: one part 210, four 91.9;
+//        1024x1024x4096 in 128 tiles: one 34.2, four 21.6
 namespace pdr {
 namespace dense {
 
-TilePlan plan_tiles(const GemmArgs &g, EpiKind kind) {
-  TilePlan p;
-  const int bn = kind == kEpiGated ? 64 : 128;
-  p.tiles_m = (g.M + 127) / 128;
-  p.tiles_n = (int)(((long long)g.epi.store_n + bn - 1) / bn);
-  p.splits = 1;
-  const long long tiles = (long long)p.tiles_m * p.tiles_n * (g.batches > 0 ? g.batches : 1);
-  const int steps = (g.K + kBK - 1) / kBK * g.segs;
-  if (kind != kEpiGated && tiles > 0 && tiles < 256) {
-    long long most = 512 / tiles;
-    if (most > steps / 4) most = steps / 4;
-    if (most > 32) most = 32;
-    if (most > 1) p.splits = (int)most;
+namespace {
+
+double tiles_us(bool large, double workgroups, double steps) {
+  const double slots = large ? 256.0 : 512.0;
+  const double rounds = floor(workgroups / slots), rest = workgroups - rounds * slots;
+  const double full = large ? 1.5 * steps + 9.0 : 0.9 * steps + 5.0;
+  double last = 0.0;
+  if (rest > 0.0) {
+    if (large)
+      last = (rest > 128.0 ? 1.5 : 1.2) * steps + 9.0;
+    else
+      last = rest > 256.0 ? full : 0.46 * steps + 4.0;
   }
-  return p;
+  return rounds * full + last;
+}
+
+}  // namespace
+
+TilePlan plan_tiles(const GemmArgs &g, EpiKind kind) {
+  const int steps = (g.K + kBK - 1) / kBK * g.segs;
+  const double batches = g.batches > 0 ? g.batches : 1;
+  const double sums = batches * (double)g.M * (double)g.N;
+  const int most = kind == kEpiGated ? 1 : steps / 2 > 32 ? 32 : steps / 2 > 1 ? steps / 2 : 1;
+  TilePlan best = {};
+  double least = 0.0;
+  for (int large = 0; large < 2; ++large) {
+    const int bm = large ? 256 : 128, bn = kind == kEpiGated ? bm / 2 : bm;
+    TilePlan p;
+    p.large = large != 0;
+    p.tiles_m = (g.M + bm - 1) / bm;
+    p.tiles_n = (g.epi.store_n + bn - 1) / bn;
+    for (p.splits = 1; p.splits <= most; ++p.splits) {
+      double us = tiles_us(p.large, batches * p.tiles_m * p.tiles_n * p.splits,
+                           (double)((steps + p.splits - 1) / p.splits));
+      // the parts are written and read once, at 4.6 TB/s
+      if (p.splits > 1) us += 3.0 + 8.0 * sums * p.splits / 4.6e6;
+      if (least == 0.0 || us < least) {
+        least = us;
+        best = p;
+      }
+    }
+  }
+  return best;
 }
 
 size_t gemm_scratch_bytes(const GemmArgs &g, EpiKind kind) {

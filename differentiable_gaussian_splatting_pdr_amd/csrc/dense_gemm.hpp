@@ -29,15 +29,13 @@
 #include <stdint.h>
 
 #include "dense_epilogue.hpp"
+#include "pdr_common.hpp"
 
 namespace pdr {
 namespace dense {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) const char lds_char;
 
@@ -55,98 +53,125 @@ struct GemmArgs {
   long long lda, ldb;                  // elements between rows, multiples of 8
   long long up_at;                     // dual products: elements from the gate rows to the up rows
   long long batch_a, batch_b;          // elements between the operands of two batches
-  int tiles_m, tiles_n, splits, batches;
+  int tiles_m, tiles_n, batches;
+  int splits;                          // parts that the contraction is cut into
+  int steps, steps_more;               // kBK steps of a part; the first steps_more parts take one more
+  FastDiv band;                        // by kBand * tiles_n
   float *partial;                      // splits > 1: [split][batch][M][N] fp32
   Epi epi;
 };
 
+// c += a b on 16x16 tiles, 32 contraction values.  Written out so that the
+// sums stay in accumulation registers: with the builtin, the 256 sums a lane
+// holds are moved between register files at every turn of the loop.  The
+// instructions on one accumulator are far apart, and settle() stands between
+// them and any other use of the accumulators, before and after.
 template <int FMT>
-struct Mfma;
-template <>
-struct Mfma<kBf16> {
-  static __device__ __forceinline__ f32x4 go(s16x8 a, s16x8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  }
-};
-template <>
-struct Mfma<kF16> {
-  static __device__ __forceinline__ f32x4 go(s16x8 a, s16x8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
-                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-  }
-};
+__device__ __forceinline__ void mfma(f32x4 &c, s16x8 a, s16x8 b) {
+  if constexpr (FMT == kBf16)
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  else
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+// All but the wave's last LEFT loads to LDS have landed and its LDS reads are
+// done; then every wave's.
+template <int LEFT>
+__device__ __forceinline__ void landed() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+}
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 // LDS swizzles: 16-byte chunk c of tile row r is stored at chunk c ^ s(r), so
-// that the lanes of one read phase fall on different banks.
-//  kc, A: a read takes rows t = 0..15 of one chunk: s = t & 7.
-//  kc, B: a read takes rows 16 (t / 4) + t % 4 + const (see the accumulator
-//         layout below): s = t % 4 + 4 ((t / 4) & 1).
-//  mc, A: a read phase takes 4 rows k of 32 bytes: s moves pairs of chunks.
-//  mc, B: a read phase takes 4 rows k of 4 half chunks, 32 bytes apart.
-template <bool MC, bool SIDE_B>
+// that the lanes of one read phase fall on different banks (counted: no
+// conflicts).  A kc read takes rows 0..15 of one chunk: s = r & 7.  A mc read
+// takes 32 bytes of each of 4 rows per 16 lanes: s moves pairs of chunks.
+template <bool MC>
 __device__ __forceinline__ int swizzle(int r) {
-  if constexpr (!MC)
-    return SIDE_B ? (r & 3) | (((r >> 4) & 1) << 2) : r & 7;
-  else
-    return SIDE_B ? (r & 1) | (((r >> 1) & 1) << 3) : ((r & 3) << 1) | (((r >> 3) & 1) << 3);
+  return MC ? ((r & 3) << 1) | (((r >> 3) & 1) << 3) : r & 7;
+}
+
+// A value that is the same in every lane, told to the compiler.
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+  return lo | ((uint64_t)hi << 32);
 }
 
 // One operand's global-to-LDS copy: ROWS output rows by kBK contraction values
-// per tile, NW waves.
-template <int ROWS, bool MC, bool SIDE_B, int NW, bool DUAL>
+// per tile, NW waves.  It walks the tiles of its segments in order.  Stepping
+// from one whole tile to the next is a few scalar instructions (they stand
+// between matrix instructions); what is rare, a segment's last and partial
+// tile and a change of segment, is worked out in seek().
+template <int ROWS, bool MC, int NW, bool DUAL>
 struct Loader {
   static constexpr int kBytes = ROWS * kBK * 2;
   static constexpr int kIssues = kBytes / (NW * 1024);
+  const void *const *segs;  // where the segments begin,
+  long long off;            // and how many bytes further this batch's
+  long long ld;
+  int row0, rows, K, have;  // first output row, output rows, contraction values, those that a mc operand has
   uint32_t voff[kIssues];
-  const char *base;  // this tile's first byte in the segment
-  long long left;    // bytes from base to the operand's end
-  int chunk_k;       // kc: first contraction value of this lane's chunk
+  int chunk_k;              // kc: first contraction value of this lane's chunk
+  bool masked;              // chunks past a partial tile's end are turned away in voff
+  const char *base;         // this tile's first byte
+  uint32_t bytes;           // from there to the operand's end
+  uint32_t step, fewer;     // what a whole tile adds to base and takes from bytes
+  int seg, kin, plain;      // segment, and tile in it, after the next `plain` - 1 whole tiles
+  int more;                 // tiles to come, this one included
 
-  __device__ __forceinline__ void init(int wave, int lane, long long ld, int row0, int rows) {
+  __device__ __forceinline__ void place_lanes(int wave, int lane) {
+    masked = false;
 #pragma unroll
     for (int i = 0; i < kIssues; ++i) {
       const int blk = i * NW + wave;
       if constexpr (!MC) {
         const int r = blk * 8 + (lane >> 3);
-        const int c = (lane & 7) ^ swizzle<false, SIDE_B>(r);
-        chunk_k = c * 8;  // the same for every issue: s depends on r % 8 and bit 4 of r only
+        const int c = (lane & 7) ^ swizzle<false>(r);
+        chunk_k = c * 8;  // the same for every issue: r % 8 is
         if constexpr (DUAL) {
-          // LDS rows 16 q + 4 j + i of a wave's 64: gate column 8 q + 4 (j & 1) + i
-          // for j < 2, the up column of the same number for j >= 2
-          const int col = (r >> 6) * 32 + ((r >> 4) & 3) * 8 + (r & 7);
-          voff[i] = row0 + col < rows ? (uint32_t)((long long)col * ld * 2 + c * 16) : kOutside;
+          // LDS rows 16 j .. 16 j + 7 hold gate columns 8 j .. 8 j + 7, the 8 rows
+          // after them the same up columns (a wave loads only one kind)
+          const int col = (r >> 4) * 8 + (r & 7);
+          voff[i] = row0 + col < rows ? (uint32_t)col * (uint32_t)ld * 2u + c * 16 : kOutside;
         } else {
-          voff[i] = (uint32_t)((long long)r * ld * 2 + c * 16);
+          voff[i] = (uint32_t)r * (uint32_t)ld * 2u + c * 16;
         }
       } else {
         constexpr int kLanesPerRow = ROWS / 8;
         const int k = blk * (64 / kLanesPerRow) + lane / kLanesPerRow;
-        const int c = (lane % kLanesPerRow) ^ swizzle<true, SIDE_B>(k);
-        voff[i] = (uint32_t)((long long)k * ld * 2 + c * 16);
+        const int c = (lane % kLanesPerRow) ^ swizzle<true>(k);
+        voff[i] = (uint32_t)k * (uint32_t)ld * 2u + c * 16;
       }
     }
   }
-
-  // Point at contraction value k0 of rows row0.. of an operand.
-  __device__ __forceinline__ void seek(const void *p, long long ld, int row0, int rows, int K,
-                                       int k0) {
+  // Point at tile `kin` of segment `seg`.
+  __device__ __forceinline__ void seek(int wave, int lane) {
+    const char *first = (const char *)uniform((uint64_t)segs[seg]) + off;
+    const int k0 = kin * kBK, whole = K / kBK;
+    if (masked) place_lanes(wave, lane);
+    plain = kin < whole ? whole - kin : 1;
+    if (plain > more) plain = more;
+    long long left;
     if constexpr (!MC) {
-      const long long at = ((long long)row0 * ld + k0) * 2;
-      base = (const char *)p + at;
-      left = ((long long)(rows - 1) * ld + K) * 2 - at;
+      base = first + ((long long)row0 * ld + k0) * 2;
+      const int r = rows - row0 < ROWS ? rows - row0 : ROWS;
+      left = ((long long)(r - 1) * ld + K - k0) * 2;
+      step = fewer = kBK * 2;
+      if (kin >= whole && chunk_k >= K - k0) {
+        // a row goes on beyond K in memory
+#pragma unroll
+        for (int i = 0; i < kIssues; ++i) voff[i] = kOutside;
+      }
+      masked = kin >= whole;
     } else {
-      const long long at = ((long long)k0 * ld + row0) * 2;
-      base = (const char *)p + at;
-      left = ((long long)(K - 1) * ld + rows) * 2 - at;
+      base = first + ((long long)k0 * ld + row0) * 2;
+      left = ((long long)(have - k0 - 1) * ld + rows - row0) * 2;
+      // where more than kOutside bytes are left the bound need not follow
+      step = (uint32_t)ld * (kBK * 2u);
+      const long long after = left - (long long)plain * step;
+      fewer = after > (long long)kOutside ? 0u : step;
+      if (left > (long long)kOutside && fewer) plain = 1;
     }
-  }
-  __device__ __forceinline__ void advance(long long ld) {
-    const long long step = MC ? (long long)kBK * ld * 2 : kBK * 2;
-    base += step;
-    left -= step;
-  }
-  __device__ __forceinline__ void load(char *lds, int wave, int k_left) const {
     // The range check turns away whole 4-byte words.  An operand that ends in
     // the middle of one (an odd mc length) is bounded by the word's end: the
     // value beyond is in the same aligned word, so reading it cannot fault, and
@@ -154,37 +179,62 @@ struct Loader {
     const uint32_t n = left <= 0                       ? 0u
                        : left >= (long long)kOutside ? kOutside
                                                        : ((uint32_t)left + 3u) & ~3u;
+    bytes = (uint32_t)__builtin_amdgcn_readfirstlane((int)n);
+    kin += plain;
+    if (kin * kBK >= K) {
+      kin = 0;
+      ++seg;
+    }
+  }
+  __device__ __forceinline__ void next(int wave, int lane) {
+    --more;
+    if (--plain > 0) {
+      base += step;
+      bytes -= fewer;
+    } else if (more > 0) {
+      seek(wave, lane);
+    } else {
+      bytes = 0;  // zeros from here on
+    }
+    // both are the same in every lane; without this they move to vector registers
+    base = (const char *)uniform((uint64_t)base);
+    bytes = (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes);
+  }
+  __device__ __forceinline__ void load(int i, char *lds, int wave) const {
     const __amdgpu_buffer_rsrc_t rsrc =
-        __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)n, 0x00020000);
-    // a kc row goes on beyond K in memory: chunks past it are turned away here
-    const bool off = !MC && chunk_k >= k_left;
-#pragma unroll
-    for (int i = 0; i < kIssues; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(lds + (i * NW + wave) * 1024), 16,
-                                               off ? kOutside : voff[i], 0, 0, 0);
+        __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)bytes, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(lds + (i * NW + wave) * 1024), 16,
+                                             voff[i], 0, 0, 0);
   }
 };
 
+// ds_read_b64_tr_b16: of each 16 lanes' 4 rows of 16 values (a row is four
+// lanes' 8 bytes), lane t receives column t.  The restrict pointer matters: it
+// gives the read the alias information without which the compiler lets it wait
+// for every load to LDS in flight, whichever stage that goes to.
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+__device__ __forceinline__ s16x4 read_transposed(lds_s16x4 *__restrict p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+}
+
 // Register fragments of one operand from its LDS tile.
-template <int ROWS, bool MC, bool SIDE_B>
+template <int ROWS, bool MC>
 struct Reader {
-  static constexpr int kVar = MC ? (SIDE_B ? 2 : 8) : 2;
+  static constexpr int kVar = MC ? 8 : 2;
   uint32_t at[kVar];
   // row0: this wave's first output row in the tile
   __device__ __forceinline__ void init(int lane, int row0) {
     const int g = lane >> 4, t = lane & 15;
     if constexpr (!MC) {
-      const int r = row0 + (SIDE_B ? 16 * (t >> 2) + (t & 3) : t);
+      const int r = row0 + t;
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-        at[ks] = r * 128 + (((ks * 4 + g) ^ swizzle<false, SIDE_B>(r)) << 4);
+      for (int ks = 0; ks < 2; ++ks) at[ks] = r * 128 + (((ks * 4 + g) ^ swizzle<false>(r)) << 4);
     } else {
       const int k = 8 * g + (t >> 2), q = t & 3;
-      const int s = swizzle<true, SIDE_B>(k);
 #pragma unroll
       for (int v = 0; v < kVar; ++v) {
-        const int c = SIDE_B ? row0 / 8 + 2 * q + v : row0 / 8 + 2 * v + (q >> 1);
-        at[v] = k * (ROWS * 2) + ((c ^ s) << 4) + (SIDE_B ? 0 : (q & 1) * 8);
+        const int c = row0 / 8 + 2 * v + (q >> 1);
+        at[v] = k * (ROWS * 2) + ((c ^ swizzle<true>(k)) << 4) + (q & 1) * 8;
       }
     }
   }
@@ -192,12 +242,11 @@ struct Reader {
   __device__ __forceinline__ s16x8 get(const char *lds, int i, int ks) const {
     lds_char *p = (lds_char *)lds;
     if constexpr (!MC) {
-      return *(const __attribute__((address_space(3))) s16x8 *)(p + at[ks] + (SIDE_B ? i * 512 : i * 2048));
+      return *(const __attribute__((address_space(3))) s16x8 *)(p + at[ks] + i * 2048);
     } else {
-      lds_char *b = p + (SIDE_B ? at[i >> 1] + (i & 1) * 8 : at[i]) + ks * 32 * (ROWS * 2);
-      s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)b);
-      s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) s16x4 *)(b + 4 * ROWS * 2));
+      lds_char *b = p + at[i] + ks * 32 * (ROWS * 2);
+      const s16x4 lo = read_transposed((lds_s16x4 *)b);
+      const s16x4 hi = read_transposed((lds_s16x4 *)(b + 4 * ROWS * 2));
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
   }
@@ -208,127 +257,212 @@ struct Reader {
 // walk bands of kBand tile rows, so that the tiles in flight on one XCD share
 // operand rows.
 constexpr int kBand = 4;
-__device__ __forceinline__ void pick_tile(int id, int tiles_m, int tiles_n, int *tm, int *tn) {
-  const int total = tiles_m * tiles_n;
+__device__ __forceinline__ void pick_tile(const GemmArgs &g, int id, int *tm, int *tn) {
+  const int total = g.tiles_m * g.tiles_n;
   const int xcd = id & 7, at = id >> 3, each = total >> 3, extra = total & 7;
   const int t = xcd * each + (xcd < extra ? xcd : extra) + at;
-  const int band = t / (kBand * tiles_n), in = t - band * kBand * tiles_n;
-  const int rows = tiles_m - band * kBand < kBand ? tiles_m - band * kBand : kBand;
-  *tm = band * kBand + in % rows;
-  *tn = in / rows;
+  const int band = (int)fdiv((uint32_t)t, g.band), in = t - band * kBand * g.tiles_n;
+  const int rows = g.tiles_m - band * kBand;
+  if (rows >= kBand) {
+    *tm = band * kBand + in % kBand;
+    *tn = in / kBand;
+  } else {
+    *tm = band * kBand + in % rows;
+    *tn = in / rows;
+  }
 }
 
 // Accumulator layout.  The matrix instruction is given B as its row operand,
-// so a lane holds 4 consecutive rows n of one column m per instruction; B's
-// rows are dealt to the 4 instructions of a wave's 64 columns as
-// n = 16 q + 4 j + i (q: lane / 16, j: instruction, i: register), which makes
-// a lane's 16 values of one m consecutive in memory: 16-byte stores, 128
-// contiguous bytes per row and wave.
-template <int FMT, int BM, int BN, int WM, int WN, bool A_MC, bool B_MC, int EPI>
-__global__ __launch_bounds__(WM *WN * 64) void k_gemm(GemmArgs g) {
+// so a lane holds 4 consecutive columns n of one row m of the result.
+//
+// Schedule.  Tiles are TS x TS x 64, 4 waves.  A wave keeps the fragments of
+// two 32-value steps in registers: while the matrix cores work on one step,
+// the next step's fragments are read from LDS.  LDS holds five half tiles (A_t
+// or B_t) in a ring, all of the 160 KB with one workgroup of 256 x 256 or two
+// of 128 x 128 on a compute unit:
+//   step 0 of tile t: read step 1 of tile t; in small tiles, load A of t + 2
+//   wait for A and B of t + 1, barrier: the halves of t are free
+//   step 1 of tile t: read step 0 of tile t + 1, load B of t + 2; in large
+//     tiles, also A of t + 3
+// One barrier a tile, and no wait between a read or load and the next matrix
+// instruction.  Loads are spread out, one every 4 matrix instructions of each
+// wave: a load holds the address path for 16 clocks and a wave that meets it
+// busy stops issuing matrix instructions too.
+template <int FMT, int TS, bool A_MC, bool B_MC, int EPI>
+__global__ __launch_bounds__(256) void k_gemm(GemmArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the body is device builtins throughout
-  constexpr int NW = WM * WN;
-  constexpr int MT = BM / WM / 16;
+  constexpr int NW = 4, WN = 2, WS = TS / 2, MT = WS / 16, NT = WS / 16;
   constexpr bool DUAL = EPI == kEpiGated;
-  static_assert(BN / WN == 64, "a wave owns 64 columns");
-  using LA = Loader<BM, A_MC, false, NW, false>;
-  using LB = Loader<BN, B_MC, true, NW, DUAL>;
-  constexpr int kStage = LA::kBytes + LB::kBytes;
-  __shared__ __align__(1024) char smem[2 * kStage];
+  using LA = Loader<TS, A_MC, NW, false>;
+  using LB = Loader<TS, B_MC, NW, DUAL>;
+  constexpr int kHalf = LA::kBytes, kRing = 5;
+  __shared__ __align__(1024) char smem[kRing * kHalf];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
   int tm, tn;
-  pick_tile(blockIdx.x, g.tiles_m, g.tiles_n, &tm, &tn);
+  pick_tile(g, blockIdx.x, &tm, &tn);
   const int split = blockIdx.y, batch = blockIdx.z;
-  const int row0 = tm * BM, col0 = tn * (DUAL ? BN / 2 : BN);
+  const int row0 = tm * TS, col0 = tn * (DUAL ? TS / 2 : TS);
+  const int tiles = g.steps + (split < g.steps_more ? 1 : 0);
 
-  LA la;
-  LB lb;
-  la.init(wave, lane, g.lda, row0, g.M);
-  lb.init(wave, lane, g.ldb, col0, g.N);
-  Reader<BM, A_MC, false> ra;
-  Reader<BN, B_MC, true> rb;
-  ra.init(lane, wm * (BM / WM));
-  rb.init(lane, wn * 64);
-
-  const int kt_seg = (g.K + kBK - 1) / kBK, kt_all = kt_seg * g.segs;
-  const int each = kt_all / g.splits, extra = kt_all % g.splits;
-  int kt = split * each + (split < extra ? split : extra);
-  const int kt_end = kt + each + (split < extra ? 1 : 0);
-  int seg = kt / kt_seg, kin = kt - seg * kt_seg;
-  const long long oa = batch * g.batch_a * 2, ob = batch * g.batch_b * 2;
-  auto seek = [&]() {
-    la.seek((const char *)g.a[seg] + oa, g.lda, row0, g.M, A_MC ? g.ka : g.K, kin * kBK);
-    lb.seek((const char *)g.b[seg] + ob + (DUAL && (wave & 1) ? g.up_at * 2 : 0), g.ldb, col0, g.N,
-            B_MC ? g.kb : g.K, kin * kBK);
-  };
-  auto issue = [&](int buf) {
-    char *s = smem + buf * kStage;
-    la.load(s, wave, g.K - kin * kBK);
-    lb.load(s + LA::kBytes, wave, g.K - kin * kBK);
-    if (++kin == kt_seg) {
-      kin = 0;
-      if (++seg < g.segs) seek();
-    } else {
-      la.advance(g.lda);
-      lb.advance(g.ldb);
-    }
-  };
-
-  f32x4 acc[MT][4];
+  f32x4 acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  if (kt < kt_end) {
-    seek();
-    issue(0);
-  }
-  int buf = 0;
-  for (; kt < kt_end; ++kt) {
-    __syncthreads();  // tile kt has arrived, and every wave is done with the other buffer
-    if (kt + 1 < kt_end) issue(buf ^ 1);
-    const char *s = smem + buf * kStage;
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      s16x8 fb[4], fa[MT];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) fb[j] = rb.get(s + LA::kBytes, j, ks);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) fa[i] = ra.get(s, i, ks);
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = Mfma<FMT>::go(fb[j], fa[i], acc[i][j]);
+  if (tiles > 0) {
+    LA la;
+    LB lb;
+    la.segs = g.a;
+    lb.segs = g.b;
+    la.off = batch * g.batch_a * 2;
+    lb.off = batch * g.batch_b * 2 + (DUAL && (wave & 1) ? g.up_at * 2 : 0);
+    la.ld = g.lda;
+    lb.ld = g.ldb;
+    la.row0 = row0;
+    lb.row0 = col0;
+    la.rows = g.M;
+    lb.rows = g.N;
+    la.K = lb.K = g.K;
+    la.have = g.ka;
+    lb.have = g.kb;
+    la.more = lb.more = tiles;
+    la.seg = la.kin = 0;
+    if (split > 0) {
+      const int per = (g.K + kBK - 1) / kBK;
+      const int kt = split * g.steps + (split < g.steps_more ? split : g.steps_more);
+      la.seg = kt / per;
+      la.kin = kt - la.seg * per;
     }
-    buf ^= 1;
-  }
+    lb.seg = la.seg;
+    lb.kin = la.kin;
+    la.place_lanes(wave, lane);
+    lb.place_lanes(wave, lane);
+    la.seek(wave, lane);
+    lb.seek(wave, lane);
+    auto load_a = [&](char *s) {
+#pragma unroll
+      for (int i = 0; i < LA::kIssues; ++i) la.load(i, s, wave);
+    };
+    auto load_b = [&](char *s) {
+#pragma unroll
+      for (int i = 0; i < LB::kIssues; ++i) lb.load(i, s, wave);
+    };
+    load_a(smem);
+    load_b(smem + kHalf);
+    la.next(wave, lane);
+    lb.next(wave, lane);
+    load_a(smem + 2 * kHalf);
+    load_b(smem + 3 * kHalf);
+    la.next(wave, lane);
+    lb.next(wave, lane);
+    constexpr int kMfma = MT * NT, kReads = MT + NT, kLoads = LA::kIssues + LB::kIssues;
+    constexpr int kPer = kMfma / 2 / kReads;  // matrix instructions between reads
+    // one load every 4 matrix instructions: all in step 1, or those of A in step 0
+    constexpr bool kLate = kLoads > kMfma / 4;
+    static_assert(kPer >= 1 && LB::kIssues <= kMfma / 4 && LA::kIssues <= kMfma / 4, "the loads fit");
+    if constexpr (!kLate) {
+      load_a(smem + 4 * kHalf);
+      la.next(wave, lane);
+    }
 
-  const int q = lane >> 4;
+    s16x8 fa[2][MT], fb[2][NT];
+    Reader<TS, A_MC> ra;
+    Reader<TS, B_MC> rb;
+    ra.init(lane, wm * WS);
+    rb.init(lane, wn * WS);
+    landed<(kLate ? 1 : 2) * LA::kIssues + LB::kIssues>();
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int m = row0 + wm * (BM / WM) + i * 16 + (lane & 15);
-    if (m >= g.M) continue;
-    float v[16];
+    for (int j = 0; j < NT; ++j) fb[0][j] = rb.get(smem + kHalf, j, 0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int i = 0; i < MT; ++i) fa[0][i] = ra.get(smem, i, 0);
+
+    int slot = 0;                // of A_t; B_t in the next one
+    char *sa = smem, *sb = smem + kHalf;
+    char *to = smem + 4 * kHalf, *free_b = smem;  // where the next A and B go
+    settle();
+    for (int t = 0; t < tiles; ++t) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[j * 4 + e] = acc[i][j][e];
-    if constexpr (DUAL) {
-      epi_gated(g.epi, m, col0 + wn * 32 + q * 8, v, v + 8);
-    } else {
-      const int n = col0 + wn * 64 + q * 16;
-      if (g.splits > 1) {
-        float *p = g.partial + ((long long)split * g.batches + batch) * g.M * g.N;
-        store_partial(p, m, n, g.N, v);
-        store_partial(p, m, n + 8, g.N, v + 8);
-      } else {
-        epi_apply<EPI>(g.epi, batch, m, n, g.N, v);
-        epi_apply<EPI>(g.epi, batch, m, n + 8, g.N, v + 8);
+      for (int x = 0; x < kMfma; ++x) {
+        if (x % kPer == 0 && x / kPer < kReads) {
+          const int r = x / kPer;
+          if (r < NT)
+            fb[1][r] = rb.get(sb, r, 1);
+          else
+            fa[1][r - NT] = ra.get(sa, r - NT, 1);
+        }
+        if (kLate && x % 4 == 2 && x / 4 < LA::kIssues) la.load(x / 4, to, wave);
+        if (x == kMfma - 2) {
+          slot = slot >= 3 ? slot - 3 : slot + 2;
+          free_b = sa;  // B of t + 2 goes where A of t was, the next A where B was
+          to = sb;
+          sa = smem + slot * kHalf;
+          sb = smem + (slot == 4 ? 0 : slot + 1) * kHalf;
+          if (kLate) la.next(wave, lane);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        mfma<FMT>(acc[x / NT][x % NT], fb[0][x % NT], fa[0][x / NT]);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      // all that may be in flight is A of t + 2
+      landed<LA::kIssues>();
+#pragma unroll
+      for (int x = 0; x < kMfma; ++x) {
+        if (x % kPer == 0 && x / kPer < kReads) {
+          const int r = x / kPer;
+          if (r < NT)
+            fb[0][r] = rb.get(sb, r, 0);
+          else
+            fa[0][r - NT] = ra.get(sa, r - NT, 0);
+        }
+        if (x % 4 == 2) {
+          if (x / 4 < LB::kIssues)
+            lb.load(x / 4, free_b, wave);
+          else if (!kLate && x / 4 < kLoads)
+            la.load(x / 4 - LB::kIssues, to, wave);
+        }
+        if (x == kMfma - 1) {
+          lb.next(wave, lane);
+          if (!kLate) la.next(wave, lane);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        mfma<FMT>(acc[x / NT][x % NT], fb[1][x % NT], fa[1][x / NT]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  settle();
+  landed<0>();
+
+  // Sums go through LDS, 64 rows of a wave at a time, so that what follows
+  // reads and writes whole rows, and its code is small: it runs once, and
+  // instructions that run once are paid for in fetches.  16-byte chunk c of
+  // row m lies at chunk c ^ (m & 15).
+  char *const mine = smem + wave * 64 * (WS * 4);
+  const int first = row0 + wm * WS, n0 = col0 + wn * (DUAL ? WS / 2 : WS);
+#pragma unroll 1
+  for (int h = 0; h < MT / 4; ++h) {
+    const int m_in = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int hh = 0; hh < MT / 4; ++hh)
+      if (h == hh) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            *(f32x4 *)(mine + (i * 16 + m_in) * (WS * 4) + (((j * 4 + q) ^ m_in) << 4)) =
+                acc[hh * 4 + i][j];
+      }
+    const int m0 = first + h * 64, rows = g.M - m0;
+    if (g.splits > 1) {
+      if constexpr (!DUAL)
+        store_staged<WS>(mine, lane, g.partial + ((long long)split * g.batches + batch) * g.M * g.N,
+                         m0, rows, n0, g.M, g.N);
+    } else {
+      finish_staged<EPI, WS>(g.epi, mine, lane, batch, m0, rows, n0, g.N);
     }
   }
 #endif

@@ -6,43 +6,63 @@
 namespace pdr {
 namespace dense {
 
-// Sums the splits of one product and applies its epilogue: one thread per 8
-// columns.
-template <int EPI>
-__global__ __launch_bounds__(256) void k_join_splits(GemmArgs g, int groups) {
-  const long long at = (long long)blockIdx.x * 256 + threadIdx.x;
+// Sums the parts of one product and applies its epilogue: one thread per W
+// columns of a row.
+template <int EPI, int W>
+__global__ __launch_bounds__(256) void k_join_splits(GemmArgs g, FastDiv groups) {
+  const uint32_t at = blockIdx.x * 256u + threadIdx.x;
   const int batch = blockIdx.z;
-  const long long m = at / groups;
-  if (m >= g.M) return;
-  const int n = (int)(at - m * groups) * 8;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < g.splits; ++s) {
-    float w[8];
-    load8(g.partial + ((long long)s * g.batches + batch) * g.M * g.N, kF32, m * g.N + n, g.N - n,
-          (g.N & 3) == 0, w);
+  const uint32_t m = fdiv(at, groups);
+  if (m >= (uint32_t)g.M) return;
+  const int n = (int)(at - m * groups.d) * W;
+  const long long each = (long long)g.M * g.N;
+  const float *p = g.partial + batch * each + (long long)m * g.N + n;
+  const Columns<EPI, W, kAsked> cols(g.epi, batch, n, g.N);
+  typename Columns<EPI, W, kAsked>::Row row;
+  cols.fetch(g.epi, (int)m, row);
+  float v[W];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += w[i];
+  for (int i = 0; i < W; ++i) v[i] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < g.splits; ++s) {
+    float w[W];
+    if constexpr (W == 1)
+      w[0] = n < g.N ? p[s * g.batches * each] : 0.f;
+    else
+      load8(p + s * g.batches * each, kF32, 0, g.N - n, (g.N & 3) == 0, w);
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] += w[i];
   }
-  epi_apply<EPI>(g.epi, batch, (int)m, n, g.N, v);
+  cols.finish(g.epi, (int)m, v, row);
 }
 
 template <int FMT, bool A_MC, bool B_MC, int EPI>
 hipError_t launch_one(GemmArgs g, void *ws, hipStream_t st) {
+  if (g.M <= 0 || g.epi.store_n <= 0 || g.batches <= 0) return hipSuccess;
   const TilePlan p = plan_tiles(g, (EpiKind)EPI);
   g.tiles_m = p.tiles_m;
   g.tiles_n = p.tiles_n;
   g.splits = p.splits;
+  const int steps = (g.K + kBK - 1) / kBK * g.segs;
+  g.steps = steps / p.splits;
+  g.steps_more = steps % p.splits;
+  g.band = make_fastdiv((uint32_t)(kBand * p.tiles_n));
   g.partial = (float *)ws;
-  if (g.M <= 0 || g.epi.store_n <= 0 || g.batches <= 0) return hipSuccess;
+  g.epi.vec = g.epi.vec && (g.epi.store_n & 7) == 0;
   const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)p.splits, (unsigned)g.batches);
-  hipLaunchKernelGGL((k_gemm<FMT, 128, 128, 2, 2, A_MC, B_MC, EPI>), grid, dim3(256), 0, st, g);
-  if (p.splits > 1) {
-    if constexpr (EPI != kEpiGated) {
-      const int groups = (g.epi.store_n + 7) / 8;
-      const long long threads = (long long)groups * g.M;
-      hipLaunchKernelGGL((k_join_splits<EPI>),
-                         dim3((unsigned)((threads + 255) / 256), 1, (unsigned)g.batches), dim3(256),
-                         0, st, g, groups);
+  if (p.large)
+    hipLaunchKernelGGL((k_gemm<FMT, 256, A_MC, B_MC, EPI>), grid, dim3(256), 0, st, g);
+  else
+    hipLaunchKernelGGL((k_gemm<FMT, 128, A_MC, B_MC, EPI>), grid, dim3(256), 0, st, g);
+  if constexpr (EPI != kEpiGated) {
+    if (p.splits > 1) {
+      const int w = g.epi.vec ? 8 : 1;
+      const unsigned groups = (unsigned)((g.epi.store_n + w - 1) / w);
+      const dim3 blocks((unsigned)(((long long)groups * g.M + 255) / 256), 1, (unsigned)g.batches);
+      if (w == 8)
+        hipLaunchKernelGGL((k_join_splits<EPI, 8>), blocks, dim3(256), 0, st, g, make_fastdiv(groups));
+      else
+        hipLaunchKernelGGL((k_join_splits<EPI, 1>), blocks, dim3(256), 0, st, g, make_fastdiv(groups));
     }
   }
   return hipGetLastError();
