@@ -17,7 +17,7 @@ ROOT = os.path.dirname(PKG)
 SOURCES = ["csrc/bin.hip", "csrc/raster.hip", "csrc/loss.hip", "csrc/adapter.hip", "csrc/span.hip",
            "csrc/abi.hip",
            "csrc/timing.hip", "csrc/dense.hip", "csrc/dense_gemm_bf16.hip",
-           "csrc/dense_gemm_f16.hip"]
+           "csrc/dense_gemm_f16.hip", "csrc/dense_skinny.hip"]
 LIB = os.path.join(PKG, "libpdrsplat.so")
 
 HIPCC_FLAGS = [

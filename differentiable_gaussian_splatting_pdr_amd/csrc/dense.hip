@@ -5,216 +5,251 @@
 #include <stdint.h>
 
 #include "dense_internal.hpp"
+#include "pdr_common.hpp"
 #include "pdr_dense.h"
 
+using namespace pdr;
 using namespace pdr::dense;
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAmaxBlocks = 256;
+constexpr int kParts = 1024;  // workgroups of a pass that reduces, at most
 
 // ------------------------------------------------------------------ kernels
+//
+// The passes around the products are bound by memory (4.6 TB/s for a copy on
+// this card): 8 values to a thread in 16-byte accesses where rows allow, a few
+// rows in flight to a thread, and enough workgroups (about a thousand) to
+// cover the latency.
 
-// Copy a 16-bit matrix to rows of ldd elements (a multiple of 8), zeros after
-// each row's end.  One thread per 8 values.
-__global__ __launch_bounds__(kThreads) void k_repack(const uint16_t *__restrict__ src, long long ld,
-                                                     long long rows, int cols,
-                                                     uint16_t *__restrict__ dst, int ldd) {
-  const int groups = ldd / 8;
-  const long long at = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const long long r = at / groups;
-  if (r >= rows) return;
-  const int c = (int)(at - r * groups) * 8;
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c + i < cols) w[i >> 1] |= (uint32_t)src[r * ld + c + i] << ((i & 1) * 16);
-  *(uint4 *)(dst + r * ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Largest finite magnitude of an fp32 matrix, one value per workgroup.
-__global__ __launch_bounds__(kThreads) void k_amax(const float *__restrict__ src, long long ld,
-                                                   long long rows, int cols,
-                                                   float *__restrict__ part) {
-  const int groups = (cols + 7) / 8;
-  const long long total = rows * groups;
-  float best = 0.f;
-  for (long long at = (long long)blockIdx.x * kThreads + threadIdx.x; at < total;
-       at += (long long)gridDim.x * kThreads) {
-    const long long r = at / groups;
-    const int c = (int)(at - r * groups) * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < cols) {
-        const float a = fabsf(src[r * ld + c + i]);
-        if (a < INFINITY) best = fmaxf(best, a);
-      }
-  }
+// The largest of a workgroup's values, in every thread.
+__device__ __forceinline__ float block_max(float v) {
   __shared__ float red[kThreads];
-  red[threadIdx.x] = best;
+  red[threadIdx.x] = v;
   __syncthreads();
   for (int s = kThreads / 2; s > 0; s >>= 1) {
     if (threadIdx.x < s) red[threadIdx.x] = fmaxf(red[threadIdx.x], red[threadIdx.x + s]);
     __syncthreads();
   }
-  if (threadIdx.x == 0) part[blockIdx.x] = red[0];
+  return red[0];
+}
+__device__ __forceinline__ double block_sum(double v) {
+  __shared__ double red[kThreads];
+  red[threadIdx.x] = v;
+  __syncthreads();
+  for (int s = kThreads / 2; s > 0; s >>= 1) {
+    if (threadIdx.x < s) red[threadIdx.x] += red[threadIdx.x + s];
+    __syncthreads();
+  }
+  return red[0];
+}
+__device__ __forceinline__ float finite_abs(float v) {
+  const float a = fabsf(v);
+  return a < INFINITY ? a : 0.f;
+}
+
+// Copy a 16-bit matrix to rows of ldd elements (a multiple of 8), zeros after
+// each row's end.  One thread per 8 values.
+__global__ __launch_bounds__(kThreads) void k_repack(const uint16_t *__restrict__ src, long long ld,
+                                                     int rows, int cols, uint16_t *__restrict__ dst,
+                                                     int ldd, FastDiv groups) {
+  const uint32_t at = blockIdx.x * kThreads + threadIdx.x;
+  const uint32_t r = fdiv(at, groups);
+  if (r >= (uint32_t)rows) return;
+  const int c = (int)(at - r * groups.d) * 8;
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < cols) w[i >> 1] |= (uint32_t)src[r * ld + c + i] << ((i & 1) * 16);
+  *(uint4 *)(dst + (long long)r * ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Largest finite magnitude of an fp32 matrix, one value per workgroup.
+__global__ __launch_bounds__(kThreads) void k_amax(const float *__restrict__ src, long long ld,
+                                                   int rows, int cols, int vec, FastDiv groups,
+                                                   float *__restrict__ part) {
+  const uint32_t total = (uint32_t)rows * groups.d;
+  float best = 0.f;
+#pragma unroll 4
+  for (uint32_t at = blockIdx.x * kThreads + threadIdx.x; at < total; at += gridDim.x * kThreads) {
+    const uint32_t r = fdiv(at, groups);
+    const int c = (int)(at - r * groups.d) * 8;
+    float v[8];
+    load8(src, kF32, r * ld + c, cols - c, vec, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) best = fmaxf(best, finite_abs(v[i]));
+  }
+  best = block_max(best);
+  if (threadIdx.x == 0) part[blockIdx.x] = best;
 }
 
 // Split an fp32 matrix into fp16 planes hi + lo under the scale 2^e that
 // brings its largest value to [2^14, 2^15); e goes to *exp.
 __global__ __launch_bounds__(kThreads) void k_split(const float *__restrict__ src, long long ld,
-                                                    long long rows, int cols,
-                                                    const float *__restrict__ part,
+                                                    int rows, int cols, int vec, FastDiv groups,
+                                                    const float *__restrict__ part, int parts,
                                                     uint16_t *__restrict__ hi,
                                                     uint16_t *__restrict__ lo, int ldd,
                                                     int *__restrict__ exp) {
-  __shared__ float red[kThreads];
-  red[threadIdx.x] = part[threadIdx.x];
-  __syncthreads();
-  for (int s = kThreads / 2; s > 0; s >>= 1) {
-    if (threadIdx.x < s) red[threadIdx.x] = fmaxf(red[threadIdx.x], red[threadIdx.x + s]);
-    __syncthreads();
-  }
-  const float amax = red[0];
+  const uint32_t at = blockIdx.x * kThreads + threadIdx.x;
+  const uint32_t r = fdiv(at, groups);
+  const int c = (int)(at - r * groups.d) * 8;
+  const bool mine = r < (uint32_t)rows;
+  float v[8];
+  if (mine) load8(src, kF32, r * ld + c, cols - c, vec, v);
+  float amax = 0.f;
+  for (int i = threadIdx.x; i < parts; i += kThreads) amax = fmaxf(amax, part[i]);
+  amax = block_max(amax);
   const int e = amax > 0.f ? 14 - ilogbf(amax) : 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) *exp = e;
-  const int groups = ldd / 8;
-  const long long at = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const long long r = at / groups;
-  if (r >= rows) return;
-  const int c = (int)(at - r * groups) * 8;
+  if (!mine) return;
   float h[8], l[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float v = c + i < cols ? ldexpf(src[r * ld + c + i], e) : 0.f;
-    h[i] = f16_to_f(f_to_f16(v));
-    l[i] = fabsf(v) < INFINITY ? v - h[i] : 0.f;
+    const float s = ldexpf(v[i], e);
+    h[i] = f16_to_f(f_to_f16(s));
+    l[i] = fabsf(s) < INFINITY ? s - h[i] : 0.f;
   }
-  store8(hi, kF16, r * ldd + c, 8, 1, h);
-  store8(lo, kF16, r * ldd + c, 8, 1, l);
+  store_w<8>(hi, kF16, (long long)r * ldd + c, h);
+  store_w<8>(lo, kF16, (long long)r * ldd + c, l);
 }
 
-// dz = dy * slope (slope null: dz = dy), rounded to the products' format, and
-// the sums of dz over this workgroup's rows.  A workgroup takes kDzRows rows
-// and 256 columns (32 threads of 8 columns, 8 rows at a time).
-constexpr int kDzRows = 256;
-__global__ __launch_bounds__(kThreads) void k_dz(const void *__restrict__ dy, int dy_fmt,
-                                                 long long lddy, const void *__restrict__ slope,
-                                                 int slope_fmt, long long ld_slope, long long M,
-                                                 int N, void *__restrict__ dz, int dz_fmt,
-                                                 long long ld_dz, float *__restrict__ colsum,
-                                                 int vec) {
-  const int n = (blockIdx.y * 32 + (threadIdx.x & 31)) * 8;
-  const int ty = threadIdx.x >> 5;
-  const long long m0 = (long long)blockIdx.x * kDzRows;
-  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (n < N) {
-    for (int i = ty; i < kDzRows && m0 + i < M; i += 8) {
-      const long long m = m0 + i;
-      float v[8], s[8];
-      load8(dy, dy_fmt, m * lddy + n, N - n, vec, v);
-      if (slope) {
-        load8(slope, slope_fmt, m * ld_slope + n, N - n, 1, s);
+// dz = dy * slope (no slope: dz = dy), rounded to the products' format, and
+// over this workgroup's rows the sums of dz and its largest finite magnitude.
+// A workgroup takes `rows` rows and TX * 8 columns.
+struct DzArgs {
+  const void *dy, *slope;
+  void *dz;       // null: only the sums
+  float *colsum;  // [row block][N], or null
+  float *amax;    // [workgroup], or null
+  long long lddy, ld_slope, ld_dz;
+  int dy_fmt, slope_fmt, dz_fmt;
+  int M, N, rows, vec;
+};
+template <int TX, bool SLOPE>
+__global__ __launch_bounds__(kThreads) void k_dz(DzArgs a) {
+  constexpr int TY = kThreads / TX, kAtOnce = 4;
+  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
+  const int n = (blockIdx.y * TX + tx) * 8;
+  const int m0 = blockIdx.x * a.rows, m1 = m0 + a.rows < a.M ? m0 + a.rows : a.M;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, best = 0.f;
+  if (n < a.N) {
+    for (int m = m0 + ty; m < m1; m += TY * kAtOnce) {
+      float v[kAtOnce][8], s[kAtOnce][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= s[j];
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int r = m + u * TY < m1 ? m + u * TY : m;
+        load8(a.dy, a.dy_fmt, r * a.lddy + n, a.N - n, a.vec, v[u]);
+        if constexpr (SLOPE) load_w<8>(a.slope, a.slope_fmt, r * a.ld_slope + n, s[u]);
       }
-      if (dz) store8(dz, dz_fmt, m * ld_dz + n, 8, 1, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += v[j];
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (m + u * TY >= m1) break;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          // past N the slope's rows hold nothing that was written
+          if constexpr (SLOPE) v[u][j] = n + j < a.N ? v[u][j] * s[u][j] : 0.f;
+          sum[j] += v[u][j];
+          best = fmaxf(best, finite_abs(v[u][j]));
+        }
+        if (a.dz) store_w<8>(a.dz, a.dz_fmt, (m + u * TY) * a.ld_dz + n, v[u]);
+      }
     }
   }
-  if (!colsum) return;
-  __shared__ float red[8][256];
+  if (a.amax) {
+    best = block_max(best);
+    if (threadIdx.x == 0) a.amax[blockIdx.y * gridDim.x + blockIdx.x] = best;
+  }
+  if (!a.colsum) return;
+  __shared__ float red[TY][TX * 8 + 1];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) red[ty][(threadIdx.x & 31) * 8 + j] = sum[j];
+  for (int j = 0; j < 8; ++j) red[ty][tx * 8 + j] = sum[j];
   __syncthreads();
-  const int c = blockIdx.y * 256 + threadIdx.x;
-  if (c < N) {
+  for (int c = threadIdx.x; c < TX * 8; c += kThreads) {
+    if (blockIdx.y * TX * 8 + c >= a.N) break;
     float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t += red[i][threadIdx.x];
-    colsum[(long long)blockIdx.x * N + c] = t;
+    for (int i = 0; i < TY; ++i) t += red[i][c];
+    a.colsum[(long long)blockIdx.x * a.N + blockIdx.y * TX * 8 + c] = t;
   }
 }
 
-// dbias[n] = sum of the row blocks' sums.
+// dbias[n] = sum of the row blocks' sums; 8 columns to a workgroup.
 __global__ __launch_bounds__(kThreads) void k_colsum(const float *__restrict__ part, int blocks,
                                                      int N, void *__restrict__ out, int fmt) {
-  const int n = blockIdx.x * 32 + (threadIdx.x & 31), ty = threadIdx.x >> 5;
+  const int n = blockIdx.x * 8 + (threadIdx.x & 7), ty = threadIdx.x >> 3;
   float s = 0.f;
-  if (n < N)
-    for (int b = ty; b < blocks; b += 8) s += part[(long long)b * N + n];
-  __shared__ float red[8][32];
-  red[ty][threadIdx.x & 31] = s;
+  if (n < N) {
+#pragma unroll 8
+    for (int b = ty; b < blocks; b += 32) s += part[(long long)b * N + n];
+  }
+  __shared__ float red[32][8];
+  red[ty][threadIdx.x & 7] = s;
   __syncthreads();
   if (ty == 0 && n < N) {
     float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t += red[i][threadIdx.x];
+    for (int i = 0; i < 32; ++i) t += red[i][threadIdx.x];
     store1(out, fmt, n, t);
   }
 }
 
 // Sums of squares of a batch's matrices (fp64: the square of any fp32 value is
-// in range), kNormBlocks partial sums per matrix.
-constexpr int kNormBlocks = 128;
+// in range), gridDim.x partial sums per matrix.
 __global__ __launch_bounds__(kThreads) void k_squares(const void *__restrict__ g, int fmt,
-                                                      long long ld, long long batch_g, long long m,
-                                                      int n, int vec, double *__restrict__ part) {
-  const int groups = (n + 7) / 8;
-  const long long total = m * groups;
+                                                      long long ld, long long batch_g, int m, int n,
+                                                      int vec, FastDiv groups,
+                                                      double *__restrict__ part) {
+  const uint32_t total = (uint32_t)m * groups.d;
   double s = 0.0;
-  for (long long at = (long long)blockIdx.x * kThreads + threadIdx.x; at < total;
-       at += (long long)kNormBlocks * kThreads) {
-    const long long r = at / groups;
-    const int c = (int)(at - r * groups) * 8;
+#pragma unroll 4
+  for (uint32_t at = blockIdx.x * kThreads + threadIdx.x; at < total; at += gridDim.x * kThreads) {
+    const uint32_t r = fdiv(at, groups);
+    const int c = (int)(at - r * groups.d) * 8;
     float v[8];
     load8(g, fmt, blockIdx.y * batch_g + r * ld + c, n - c, vec, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) s += (double)v[i] * (double)v[i];
   }
-  __shared__ double red[kThreads];
-  red[threadIdx.x] = s;
-  __syncthreads();
-  for (int h = kThreads / 2; h > 0; h >>= 1) {
-    if (threadIdx.x < h) red[threadIdx.x] += red[threadIdx.x + h];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) part[blockIdx.y * kNormBlocks + blockIdx.x] = red[0];
+  s = block_sum(s);
+  if (threadIdx.x == 0) part[blockIdx.y * gridDim.x + blockIdx.x] = s;
 }
 
 // x = g / (|g| + eps) 2^shift in fp16 planes (lo null: one), or in format
 // `fmt_out` with no planes; rows of ldx elements, zeros after each row's end.
-__global__ __launch_bounds__(kThreads) void k_normalise(
-    const void *__restrict__ g, int fmt, long long ld, long long batch_g, long long m, int n, int vec,
-    const double *__restrict__ part, float eps, int shift, void *__restrict__ x,
-    void *__restrict__ x_lo, int fmt_out, long long ldx, long long batch_x, int cols_out, int vec_out) {
-  __shared__ double red[kNormBlocks];
-  if (threadIdx.x < kNormBlocks) red[threadIdx.x] = part[blockIdx.y * kNormBlocks + threadIdx.x];
-  __syncthreads();
-  for (int h = kNormBlocks / 2; h > 0; h >>= 1) {
-    if (threadIdx.x < h) red[threadIdx.x] += red[threadIdx.x + h];
-    __syncthreads();
-  }
-  const double scale = ldexp(1.0 / (sqrt(red[0]) + (double)eps), shift);
-  const int groups = (cols_out + 7) / 8;
-  const long long at = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const long long r = at / groups;
-  if (r >= m) return;
-  const int c = (int)(at - r * groups) * 8;
+struct NormaliseArgs {
+  const void *g;
+  const double *part;
+  void *x, *x_lo;
+  long long ld, batch_g, ldx, batch_x;
+  int fmt, fmt_out, parts, m, n, cols_out, vec, vec_out, shift;
+  float eps;
+  FastDiv groups;
+};
+__global__ __launch_bounds__(kThreads) void k_normalise(NormaliseArgs a) {
+  const uint32_t at = blockIdx.x * kThreads + threadIdx.x;
+  const uint32_t r = fdiv(at, a.groups);
+  const int c = (int)(at - r * a.groups.d) * 8;
+  const bool mine = r < (uint32_t)a.m;
   float v[8], lo[8];
-  load8(g, fmt, blockIdx.y * batch_g + r * ld + c, n - c, vec, v);
+  if (mine) load8(a.g, a.fmt, blockIdx.y * a.batch_g + r * a.ld + c, a.n - c, a.vec, v);
+  double s = 0.0;
+  for (int i = threadIdx.x; i < a.parts; i += kThreads) s += a.part[blockIdx.y * a.parts + i];
+  s = block_sum(s);
+  if (!mine) return;
+  // 1 / (|g| + eps) as a value in [1/2, 1) and a power of two: no fp32 input
+  // makes the product with either leave fp32's range on the way
+  int e;
+  const float f = (float)frexp(1.0 / (sqrt(s) + (double)a.eps), &e);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     // a zero matrix with eps = 0 stays zero rather than 0 * inf
-    const float t = v[i] == 0.f ? 0.f : (float)((double)v[i] * scale);
+    const float t = v[i] == 0.f ? 0.f : ldexpf(v[i] * f, e + a.shift);
     v[i] = t;
     lo[i] = t - f16_to_f(f_to_f16(t));
   }
-  const long long to = blockIdx.y * batch_x + r * ldx + c;
-  store8(x, fmt_out, to, cols_out - c, vec_out, v);
-  if (x_lo) store8(x_lo, kF16, to, cols_out - c, vec_out, lo);
+  const long long to = blockIdx.y * a.batch_x + r * a.ldx + c;
+  store8(a.x, a.fmt_out, to, a.cols_out - c, a.vec_out, v);
+  if (a.x_lo) store8(a.x_lo, kF16, to, a.cols_out - c, a.vec_out, lo);
 }
 
 // ------------------------------------------------------------------- set-up
@@ -224,6 +259,8 @@ bool good_len(long long n) { return n >= 0 && n <= 0x7fffffffLL - 256; }
 // A matrix of this many rows and columns: its pointer and row distance.
 bool good_mat(const void *p, long long ld, long long rows, long long cols, int fmt) {
   if (rows == 0 || cols == 0) return true;
+  // passes index a matrix by 8 values in 31 bits
+  if (rows * ((cols + 7) / 8) > 0x7fffffffLL - kThreads) return false;
   if (!p || ((uintptr_t)p & (uintptr_t)(fmt_bytes(fmt) - 1))) return false;
   return ld >= cols && ld <= kMaxLd;
 }
@@ -259,8 +296,15 @@ struct Planes {
 
 int product_fmt(int fmt) { return fmt == kBf16 ? kBf16 : kF16; }
 
+unsigned blocks_for(long long threads) { return (unsigned)((threads + kThreads - 1) / kThreads); }
+unsigned parts_for(long long threads) {
+  const long long b = (threads + kThreads - 1) / kThreads;
+  return (unsigned)(b < 1 ? 1 : b < kParts ? b : kParts);
+}
+
+// `amax`, if given: `parts` values whose largest is p's largest magnitude.
 Planes lay_out(Walk &w, const void *p, int fmt, long long ld, long long rows, long long cols,
-               bool summed_along_row) {
+               bool summed_along_row, const float *amax = nullptr, int parts = 0) {
   Planes r;
   if (rows == 0 || cols == 0) {
     r.ld = round8(cols > 0 ? cols : 1);
@@ -271,29 +315,34 @@ Planes lay_out(Walk &w, const void *p, int fmt, long long ld, long long rows, lo
     r.ld = ld;
     return r;
   }
-  const long long ldd = round8(cols);
-  const unsigned blocks = (unsigned)((rows * (ldd / 8) + kThreads - 1) / kThreads);
+  const long long ldd = round8(cols), threads = rows * (ldd / 8);
+  const FastDiv groups = make_fastdiv((uint32_t)(ldd / 8));
   uint16_t *hi = (uint16_t *)w.take((size_t)(rows * ldd) * 2);
   r.hi = hi;
   r.ld = ldd;
   if (fmt != kF32) {
     if (w.go()) {
-      hipLaunchKernelGGL(k_repack, dim3(blocks), dim3(kThreads), 0, w.st, (const uint16_t *)p, ld,
-                         rows, (int)cols, hi, (int)ldd);
+      hipLaunchKernelGGL(k_repack, dim3(blocks_for(threads)), dim3(kThreads), 0, w.st,
+                         (const uint16_t *)p, ld, (int)rows, (int)cols, hi, (int)ldd, groups);
       w.done(hipGetLastError());
     }
     return r;
   }
   uint16_t *lo = (uint16_t *)w.take((size_t)(rows * ldd) * 2);
-  float *part = (float *)w.take(kAmaxBlocks * sizeof(float));
+  float *part = amax ? nullptr : (float *)w.take(kParts * sizeof(float));
   int *exp = (int *)w.take(sizeof(int));
   r.lo = lo;
   r.exp = exp;
   if (w.go()) {
-    hipLaunchKernelGGL(k_amax, dim3(kAmaxBlocks), dim3(kThreads), 0, w.st, (const float *)p, ld, rows,
-                       (int)cols, part);
-    hipLaunchKernelGGL(k_split, dim3(blocks), dim3(kThreads), 0, w.st, (const float *)p, ld, rows,
-                       (int)cols, part, hi, lo, (int)ldd, exp);
+    const int vec = aligned16(p) && (ld & 7) == 0;
+    if (!amax) {
+      parts = (int)parts_for(threads);
+      hipLaunchKernelGGL(k_amax, dim3((unsigned)parts), dim3(kThreads), 0, w.st, (const float *)p, ld,
+                         (int)rows, (int)cols, vec, groups, part);
+      amax = part;
+    }
+    hipLaunchKernelGGL(k_split, dim3(blocks_for(threads)), dim3(kThreads), 0, w.st, (const float *)p,
+                       ld, (int)rows, (int)cols, vec, groups, amax, parts, hi, lo, (int)ldd, exp);
     w.done(hipGetLastError());
   }
   return r;
@@ -367,23 +416,37 @@ int check_linear(const pdr_linear *p, bool backward) {
 
 int slope_fmt(int fmt) { return fmt == kBf16 ? kF16 : kF32; }
 
+// Few rows: the kernel for them, which lays nothing out.
+void multiply_few(Walk &w, const void *x, long long ldx, const void *wt, long long ldw,
+                  long long up_at, long long M, long long N, long long K, const Epi &epi, int fmt,
+                  bool gated) {
+  if (!w.go()) return;
+  SkinnyArgs a = {x, wt, ldx, ldw, up_at, (int)M, (int)N, (int)K, epi};
+  w.done(launch_skinny(a, fmt, gated, w.st));
+}
+
 void linear_forward(Walk &w, const pdr_linear &p) {
+  Epi e = {};
+  e.store_n = (int)p.N;
+  set_out(e, p.y, p.out_fmt, p.ldy);
+  e.bias = p.bias;
+  e.bias_fmt = p.fmt;
+  e.res = p.res;
+  e.ldr = (int)p.ldr;
+  e.vec = e.vec && (!p.bias || aligned16(p.bias)) && (!p.res || (aligned16(p.res) && (p.ldr & 7) == 0));
+  e.act = p.activation;
+  e.slope = p.activation != PDR_ACT_NONE ? p.slope : nullptr;
+  e.slope_fmt = slope_fmt(p.fmt);
+  e.ld_slope = (int)round8(p.N);
+  if (p.M <= kSkinnyRows)
+    return multiply_few(w, p.x, p.ldx, p.w, p.ldw, 0, p.M, p.N, p.K, e, p.fmt, false);
   const Planes x = lay_out(w, p.x, p.fmt, p.ldx, p.M, p.K, true);
   const Planes wt = lay_out(w, p.w, p.fmt, p.ldw, p.N, p.K, true);
   GemmArgs g = product(p.M, p.N, round8(p.K));
   add_product(g, x, 0, wt, 0);
-  set_out(g.epi, p.y, p.out_fmt, p.ldy);
+  g.epi = e;
   g.epi.exp_a = x.exp;
   g.epi.exp_b = wt.exp;
-  g.epi.bias = p.bias;
-  g.epi.bias_fmt = p.fmt;
-  g.epi.res = p.res;
-  g.epi.ldr = (int)p.ldr;
-  g.epi.vec = g.epi.vec && (!p.bias || aligned16(p.bias)) && (!p.res || (aligned16(p.res) && (p.ldr & 7) == 0));
-  g.epi.act = p.activation;
-  g.epi.slope = p.slope;
-  g.epi.slope_fmt = slope_fmt(p.fmt);
-  g.epi.ld_slope = (int)round8(p.N);
   multiply(w, g, p.fmt, false, false, kEpiLinear);
 }
 
@@ -399,21 +462,55 @@ void linear_backward(Walk &w, const pdr_linear &p) {
     ld_dz = round8(p.N);
     dz = buf = w.take((size_t)(p.M * ld_dz) * fmt_bytes(p.fmt));
   }
-  const int row_blocks = (int)((p.M + kDzRows - 1) / kDzRows);
-  float *part = p.dbias ? (float *)w.take((size_t)row_blocks * p.N * sizeof(float)) : nullptr;
+  // threads across a row's 8s, and rows to a workgroup for about kParts of them
+  const int tx = p.N <= 8 ? 1 : p.N <= 64 ? 8 : 32, ty = kThreads / tx;
+  const long long col_blocks = (p.N + tx * 8 - 1) / (tx * 8);
+  long long rows = (p.M * col_blocks + kParts - 1) / kParts;
+  rows = rows < ty ? ty : (rows + ty - 1) / ty * ty;
+  const long long row_blocks = p.M ? (p.M + rows - 1) / rows : 0;
+  const bool split = write && p.fmt == kF32;
+  float *part = p.dbias ? (float *)w.take((size_t)(row_blocks * p.N) * sizeof(float)) : nullptr;
+  float *amax = split ? (float *)w.take((size_t)(row_blocks * col_blocks) * sizeof(float)) : nullptr;
   if ((write || p.dbias) && p.N && w.go()) {
-    if (row_blocks)
-      hipLaunchKernelGGL(k_dz, dim3((unsigned)row_blocks, (unsigned)((p.N + 255) / 256)),
-                         dim3(kThreads), 0, w.st, p.dy, p.out_fmt, p.lddy, act ? p.slope : nullptr,
-                         slope_fmt(p.fmt), round8(p.N), p.M, (int)p.N, buf, p.fmt, ld_dz, part,
-                         aligned16(p.dy) && (p.lddy & 7) == 0);
+    DzArgs a = {};
+    a.dy = p.dy;
+    a.slope = act ? p.slope : nullptr;
+    a.dz = buf;
+    a.colsum = part;
+    a.amax = amax;
+    a.lddy = p.lddy;
+    a.ld_slope = round8(p.N);
+    a.ld_dz = ld_dz;
+    a.dy_fmt = p.out_fmt;
+    a.slope_fmt = slope_fmt(p.fmt);
+    a.dz_fmt = p.fmt;
+    a.M = (int)p.M;
+    a.N = (int)p.N;
+    a.rows = (int)rows;
+    a.vec = aligned16(p.dy) && (p.lddy & 7) == 0;
+    const dim3 grid((unsigned)row_blocks, (unsigned)col_blocks);
+    auto run = [&](auto with_slope, auto without) {
+      if (a.slope)
+        hipLaunchKernelGGL(with_slope, grid, dim3(kThreads), 0, w.st, a);
+      else
+        hipLaunchKernelGGL(without, grid, dim3(kThreads), 0, w.st, a);
+    };
+    if (row_blocks) {
+      if (tx == 1)
+        run(k_dz<1, true>, k_dz<1, false>);
+      else if (tx == 8)
+        run(k_dz<8, true>, k_dz<8, false>);
+      else
+        run(k_dz<32, true>, k_dz<32, false>);
+    }
     if (p.dbias)
-      hipLaunchKernelGGL(k_colsum, dim3((unsigned)((p.N + 31) / 32)), dim3(kThreads), 0, w.st, part,
-                         row_blocks, (int)p.N, p.dbias, p.fmt);
+      hipLaunchKernelGGL(k_colsum, dim3((unsigned)((p.N + 7) / 8)), dim3(kThreads), 0, w.st, part,
+                         (int)row_blocks, (int)p.N, p.dbias, p.fmt);
     w.done(hipGetLastError());
   }
   if (!products) return;
-  const Planes z = lay_out(w, dz, p.fmt, ld_dz, p.M, write ? round8(p.N) : p.N, p.dx != nullptr);
+  const Planes z = lay_out(w, dz, p.fmt, ld_dz, p.M, write ? round8(p.N) : p.N, p.dx != nullptr, amax,
+                           (int)(row_blocks * col_blocks));
   if (p.dx) {
     const size_t keep = w.at;
     const Planes wt = lay_out(w, p.w, p.fmt, p.ldw, p.N, p.K, false);
@@ -465,6 +562,21 @@ int check_gated(const pdr_gated_mlp *p, bool backward) {
 
 void gated_forward(Walk &w, const pdr_gated_mlp &p) {
   const long long Fp = round8(p.F);
+  Epi in = {}, out = {};
+  in.store_n = (int)Fp;
+  set_out(in, p.h, p.fmt, Fp);
+  in.act = p.activation;
+  in.gu = (float *)p.gu;
+  in.ld_gu = (int)Fp;
+  out.store_n = (int)p.O;
+  set_out(out, p.y, p.fmt, p.ldy);
+  out.res = p.res;
+  out.ldr = (int)p.ldr;
+  out.vec = out.vec && (!p.res || (aligned16(p.res) && (p.ldr & 7) == 0));
+  if (p.M <= kSkinnyRows) {
+    multiply_few(w, p.x, p.ldx, p.w_in, p.ld_in, p.F * p.ld_in, p.M, p.F, p.D, in, p.fmt, true);
+    return multiply_few(w, p.h, Fp, p.w_out, p.ld_out, 0, p.M, p.O, p.F, out, p.fmt, false);
+  }
   {
     const size_t keep = w.at;
     const Planes x = lay_out(w, p.x, p.fmt, p.ldx, p.M, p.D, true);
@@ -472,13 +584,9 @@ void gated_forward(Walk &w, const pdr_gated_mlp &p) {
     GemmArgs g = product(p.M, p.F, round8(p.D));
     add_product(g, x, 0, wi, 0);
     g.up_at = p.F * wi.ld;
-    set_out(g.epi, p.h, p.fmt, Fp);
-    g.epi.store_n = (int)Fp;
+    g.epi = in;
     g.epi.exp_a = x.exp;
     g.epi.exp_b = wi.exp;
-    g.epi.act = p.activation;
-    g.epi.gu = (float *)p.gu;
-    g.epi.ld_gu = (int)Fp;
     multiply(w, g, p.fmt, false, false, kEpiGated);
     w.at = keep;
   }
@@ -486,12 +594,9 @@ void gated_forward(Walk &w, const pdr_gated_mlp &p) {
   const Planes wo = lay_out(w, p.w_out, p.fmt, p.ld_out, p.O, p.F, true);
   GemmArgs g = product(p.M, p.O, Fp);
   add_product(g, h, 0, wo, 0);
-  set_out(g.epi, p.y, p.fmt, p.ldy);
+  g.epi = out;
   g.epi.exp_a = h.exp;
   g.epi.exp_b = wo.exp;
-  g.epi.res = p.res;
-  g.epi.ldr = (int)p.ldr;
-  g.epi.vec = g.epi.vec && (!p.res || (aligned16(p.res) && (p.ldr & 7) == 0));
   multiply(w, g, p.fmt, false, false, kEpiLinear);
 }
 
@@ -581,20 +686,39 @@ void orthogonalize(Walk &w, const pdr_orthogonalize_args &p) {
   const bool two = p.fmt != kBf16, tall = p.m > p.n;
   const long long s = tall ? p.n : p.m, sp = round8(s), np = round8(p.n);
   const size_t x_bytes = (size_t)(p.batch * p.m * np) * 2, a_bytes = (size_t)(p.batch * s * sp) * 2;
-  double *part = (double *)w.take((size_t)p.batch * kNormBlocks * sizeof(double));
+  const int parts = (int)parts_for(p.m * ((p.n + 7) / 8) / 4);
+  double *part = (double *)w.take((size_t)p.batch * kParts * sizeof(double));
   if (p.batch == 0 || p.m == 0 || p.n == 0) return;
   const int vec_g = aligned16(p.g) && (p.ldg & 7) == 0 && (p.batch_g & 7) == 0;
   const int vec_x = aligned16(p.x) && (p.ldx & 7) == 0 && (p.batch_x & 7) == 0;
   auto normalise = [&](void *x, void *lo, int shift, int fmt, long long ldx, long long batch_x,
                        long long cols, int vec) {
-    const long long threads = p.m * ((cols + 7) / 8);
     if (!w.go()) return;
-    hipLaunchKernelGGL(k_squares, dim3(kNormBlocks, (unsigned)p.batch), dim3(kThreads), 0, w.st, p.g,
-                       p.fmt, p.ldg, p.batch_g, p.m, (int)p.n, vec_g, part);
-    hipLaunchKernelGGL(k_normalise,
-                       dim3((unsigned)((threads + kThreads - 1) / kThreads), (unsigned)p.batch),
-                       dim3(kThreads), 0, w.st, p.g, p.fmt, p.ldg, p.batch_g, p.m, (int)p.n, vec_g,
-                       part, p.eps, shift, x, lo, fmt, ldx, batch_x, (int)cols, vec);
+    hipLaunchKernelGGL(k_squares, dim3((unsigned)parts, (unsigned)p.batch), dim3(kThreads), 0, w.st,
+                       p.g, p.fmt, p.ldg, p.batch_g, (int)p.m, (int)p.n, vec_g,
+                       make_fastdiv((uint32_t)((p.n + 7) / 8)), part);
+    NormaliseArgs a = {};
+    a.g = p.g;
+    a.part = part;
+    a.x = x;
+    a.x_lo = lo;
+    a.ld = p.ldg;
+    a.batch_g = p.batch_g;
+    a.ldx = ldx;
+    a.batch_x = batch_x;
+    a.fmt = p.fmt;
+    a.fmt_out = fmt;
+    a.parts = parts;
+    a.m = (int)p.m;
+    a.n = (int)p.n;
+    a.cols_out = (int)cols;
+    a.vec = vec_g;
+    a.vec_out = vec;
+    a.shift = shift;
+    a.eps = p.eps;
+    a.groups = make_fastdiv((uint32_t)((cols + 7) / 8));
+    hipLaunchKernelGGL(k_normalise, dim3(blocks_for(p.m * ((cols + 7) / 8)), (unsigned)p.batch),
+                       dim3(kThreads), 0, w.st, a);
     w.done(hipGetLastError());
   };
   if (p.steps == 0) {

@@ -399,7 +399,7 @@ __device__ __forceinline__ void finish_rows(const Epi &e, const char *mine, int 
   constexpr bool DUAL = KIND == kEpiGated;
   constexpr int kOut = DUAL ? COLS / 2 : COLS;  // columns of the result
   constexpr int kLanes = kOut / W < 64 ? kOut / W : 64;
-  constexpr int kRows = 64 / kLanes, kAtOnce = W == 1 ? 1 : 2;
+  constexpr int kRows = 64 / kLanes, kAtOnce = W == 1 ? 4 : 2;
 #pragma unroll 1
   for (int c = (lane % kLanes) * W; c < kOut; c += kLanes * W) {
     if (n0 + c >= e.store_n) continue;
@@ -446,14 +446,12 @@ __device__ __forceinline__ void finish_rows(const Epi &e, const char *mine, int 
   }
 }
 
-template <int KIND, int COLS>
-__device__ __forceinline__ void finish_staged(const Epi &e, const char *mine, int lane, int batch,
-                                              int m0, int rows, int n0, int N) {
-  if (rows <= 0) return;
-  if (!e.vec) return finish_rows<KIND, COLS, 1, kAsked>(e, mine, lane, batch, m0, rows, n0, N);
+template <int KIND, int COLS, int W>
+__device__ __forceinline__ void finish_flags(const Epi &e, const char *mine, int lane, int batch,
+                                             int m0, int rows, int n0, int N) {
   const int f = epi_flags(KIND, e);
   auto with = [&](auto flags) {
-    finish_rows<KIND, COLS, 8, decltype(flags)::value>(e, mine, lane, batch, m0, rows, n0, N);
+    finish_rows<KIND, COLS, W, decltype(flags)::value>(e, mine, lane, batch, m0, rows, n0, N);
   };
   if constexpr (KIND == kEpiGatedGrad) {
     (f & kWide) ? with(Flags<kWide>()) : with(Flags<0>());
@@ -474,6 +472,16 @@ __device__ __forceinline__ void finish_staged(const Epi &e, const char *mine, in
       default: return with(Flags<7>());
     }
   }
+}
+
+template <int KIND, int COLS>
+__device__ __forceinline__ void finish_staged(const Epi &e, const char *mine, int lane, int batch,
+                                              int m0, int rows, int n0, int N) {
+  if (rows <= 0) return;
+  if (e.vec)
+    finish_flags<KIND, COLS, 8>(e, mine, lane, batch, m0, rows, n0, N);
+  else if constexpr (KIND == kEpiLinear || KIND == kEpiPoly)  // the others write rows of their own
+    finish_flags<KIND, COLS, 1>(e, mine, lane, batch, m0, rows, n0, N);
 }
 
 // The sums themselves, as one part of a contraction that is cut.

@@ -19,6 +19,17 @@ struct TilePlan {
 };
 TilePlan plan_tiles(const GemmArgs &g, EpiKind kind);
 
+// Products of at most kSkinnyRows rows, read where they lie (dense_skinny.hip):
+// x [M][K], w [N][K]; a gated product's up rows begin up_at elements further.
+constexpr int kSkinnyRows = 64;
+struct SkinnyArgs {
+  const void *x, *w;
+  long long ldx, ldw, up_at;
+  int M, N, K;
+  Epi epi;
+};
+hipError_t launch_skinny(const SkinnyArgs &a, int fmt, bool gated, hipStream_t st);
+
 inline long long round8(long long n) { return (n + 7) & ~7LL; }
 
 }  // namespace dense

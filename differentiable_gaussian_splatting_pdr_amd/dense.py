@@ -13,12 +13,13 @@ strided; the last dimension is packed (anything else is copied first).
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from . import _lib
-from .splat import _FMT, _stream
+from .splat import _FMT
+
+# the current stream's handle, without the stream object around it
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 _ACTS = {"none": _lib.PDR_ACT_NONE, "relu": _lib.PDR_ACT_RELU, "silu": _lib.PDR_ACT_SILU,
          "gelu": _lib.PDR_ACT_GELU}
@@ -53,24 +54,62 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
 
 
 def _ld(t: torch.Tensor) -> int:
-    return max(t.stride(0), t.shape[1], 1) if t.shape[0] > 1 else max(t.shape[1], 1)
+    rows, cols = t.shape
+    return (t.stride(0) if rows > 1 else cols) or 1
+
+
+def _kept_ld(n: int) -> int:
+    """pdr_dense_kept_ld."""
+    return (n + 7) // 8 * 8
+
+
+_CALLS = {}
 
 
 def _call(name: str, args, device):
-    with torch.cuda.device(device):
-        size = getattr(_lib, name + "_workspace_bytes")(ctypes.byref(args))
-        ws = torch.empty(size, dtype=torch.uint8, device=device) if size else None
-        getattr(_lib, name)(ctypes.byref(args), ws.data_ptr() if size else None, size, _stream(device))
+    """Run an entry point in a workspace of its size, on the current stream."""
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call(name, args, device)
+    if name not in _CALLS:
+        _CALLS[name] = (getattr(_lib, name + "_workspace_bytes"), getattr(_lib, name))
+    size_of, run = _CALLS[name]
+    size = size_of(args)
+    if size:
+        ws = torch.empty(size, dtype=torch.uint8, device=device)
+        run(args, ws.data_ptr(), size, _raw_stream(device.index))
+    else:
+        run(args, None, 0, _raw_stream(device.index))
+
+
+def _wants_grad(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
 # ------------------------------------------------------------------- linear
 
 def _linear_args(x, w, activation, out_dtype):
-    a = _lib.pdr_linear()
-    a.fmt, a.out_fmt, a.activation = _FMT[x.dtype], _FMT[out_dtype], activation
-    a.M, a.N, a.K = x.shape[0], w.shape[0], x.shape[1]
-    a.x, a.ldx, a.w, a.ldw = x.data_ptr(), _ld(x), w.data_ptr(), _ld(w)
-    return a
+    """pdr_linear of the operands; the results' fields follow."""
+    return _lib.pdr_linear(_FMT[x.dtype], _FMT[out_dtype], activation, x.shape[0], w.shape[0],
+                           x.shape[1], x.data_ptr(), _ld(x), w.data_ptr(), _ld(w))
+
+
+def _linear_forward(x, w, bias, residual, activation, out_dtype, keep):
+    """(y, slope); slope only with `keep`."""
+    a = _linear_args(x, w, activation, out_dtype)
+    y = torch.empty((x.shape[0], w.shape[0]), dtype=out_dtype, device=x.device)
+    a.y, a.ldy = y.data_ptr(), w.shape[0] or 1
+    if bias is not None:
+        a.bias = bias.data_ptr()
+    if residual is not None:
+        a.res, a.ldr = residual.data_ptr(), _ld(residual)
+    slope = None
+    if keep and activation != _lib.PDR_ACT_NONE:
+        kind = torch.float16 if x.dtype == torch.bfloat16 else torch.float32
+        slope = torch.empty((x.shape[0], _kept_ld(w.shape[0])), dtype=kind, device=x.device)
+        a.slope = slope.data_ptr()
+    _call("pdr_linear_forward", a, x.device)
+    return y, slope
 
 
 class Linear(torch.autograd.Function):
@@ -78,19 +117,8 @@ class Linear(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w, bias, residual, activation, out_dtype):
-        a = _linear_args(x, w, activation, out_dtype)
-        y = torch.empty((a.M, a.N), dtype=out_dtype, device=x.device)
-        a.y, a.ldy = y.data_ptr(), max(a.N, 1)
-        if bias is not None:
-            a.bias = bias.data_ptr()
-        if residual is not None:
-            a.res, a.ldr = residual.data_ptr(), _ld(residual)
-        slope = None
-        if activation != _lib.PDR_ACT_NONE and any(ctx.needs_input_grad[:3]):
-            kind = torch.float16 if x.dtype == torch.bfloat16 else torch.float32
-            slope = torch.empty((a.M, _lib.pdr_dense_kept_ld(a.N)), dtype=kind, device=x.device)
-            a.slope = slope.data_ptr()
-        _call("pdr_linear_forward", a, x.device)
+        y, slope = _linear_forward(x, w, bias, residual, activation, out_dtype,
+                                   any(ctx.needs_input_grad[:3]))
         ctx.save_for_backward(x, w, slope)
         ctx.meta = (activation, out_dtype, bias is not None)
         return y
@@ -148,19 +176,40 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
         if residual.shape != shape:
             raise ValueError("residual must be %s" % (shape,))
         residual = _rows(residual)
-    y = Linear.apply(_rows(x), _rows(weight), bias, residual, _activation(activation), out_dtype)
-    return y.view(shape)
+    args = (_rows(x), _rows(weight), bias, residual, _activation(activation), out_dtype)
+    if _wants_grad(x, weight, bias, residual):
+        y = Linear.apply(*args)
+    else:
+        y, _ = _linear_forward(*args, False)
+    return y if x.dim() == 2 else y.view(shape)
 
 
 # -------------------------------------------------------------- gated block
 
 def _gated_args(x, w_in, w_out, activation):
-    a = _lib.pdr_gated_mlp()
-    a.fmt, a.activation = _FMT[x.dtype], activation
-    a.M, a.D, a.F, a.O = x.shape[0], x.shape[1], w_out.shape[1], w_out.shape[0]
-    a.x, a.ldx = x.data_ptr(), _ld(x)
-    a.w_in, a.ld_in, a.w_out, a.ld_out = w_in.data_ptr(), _ld(w_in), w_out.data_ptr(), _ld(w_out)
-    return a
+    """pdr_gated_mlp of the operands; the results' fields follow."""
+    return _lib.pdr_gated_mlp(_FMT[x.dtype], activation, x.shape[0], x.shape[1], w_out.shape[1],
+                              w_out.shape[0], x.data_ptr(), _ld(x), w_in.data_ptr(), _ld(w_in),
+                              w_out.data_ptr(), _ld(w_out))
+
+
+def _gated_forward(x, w_in, w_out, residual, activation, keep):
+    """(y, h, gu); gu only with `keep`."""
+    a = _gated_args(x, w_in, w_out, activation)
+    rows, cols = x.shape[0], w_out.shape[0]
+    y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    a.y, a.ldy = y.data_ptr(), cols or 1
+    if residual is not None:
+        a.res, a.ldr = residual.data_ptr(), _ld(residual)
+    ld = _kept_ld(w_out.shape[1])
+    h = torch.empty((rows, ld), dtype=x.dtype, device=x.device)
+    a.h = h.data_ptr()
+    gu = None
+    if keep:
+        gu = torch.empty((rows, 2, ld), dtype=torch.float32, device=x.device)
+        a.gu = gu.data_ptr()
+    _call("pdr_gated_mlp_forward", a, x.device)
+    return y, h, gu
 
 
 class GatedMLP(torch.autograd.Function):
@@ -169,19 +218,8 @@ class GatedMLP(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w_in, w_out, residual, activation):
-        a = _gated_args(x, w_in, w_out, activation)
-        y = torch.empty((a.M, a.O), dtype=x.dtype, device=x.device)
-        a.y, a.ldy = y.data_ptr(), max(a.O, 1)
-        if residual is not None:
-            a.res, a.ldr = residual.data_ptr(), _ld(residual)
-        ld = _lib.pdr_dense_kept_ld(a.F)
-        h = torch.empty((a.M, ld), dtype=x.dtype, device=x.device)
-        a.h = h.data_ptr()
-        gu = None
-        if any(ctx.needs_input_grad[:2]):
-            gu = torch.empty((a.M, 2, ld), dtype=torch.float32, device=x.device)
-            a.gu = gu.data_ptr()
-        _call("pdr_gated_mlp_forward", a, x.device)
+        y, h, gu = _gated_forward(x, w_in, w_out, residual, activation,
+                                  any(ctx.needs_input_grad[:2]))
         ctx.save_for_backward(x, w_in, w_out, h, gu)
         ctx.activation = activation
         return y
@@ -230,8 +268,12 @@ def gated_mlp(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor,
         if residual.shape != shape:
             raise ValueError("residual must be %s" % (shape,))
         residual = _rows(residual)
-    y = GatedMLP.apply(_rows(x), _rows(w_in), _rows(w_out), residual, _activation(activation))
-    return y.view(shape)
+    args = (_rows(x), _rows(w_in), _rows(w_out), residual, _activation(activation))
+    if _wants_grad(x, w_in, w_out, residual):
+        y = GatedMLP.apply(*args)
+    else:
+        y = _gated_forward(*args, False)[0]
+    return y if x.dim() == 2 else y.view(shape)
 
 
 # ------------------------------------------------------------ orthogonalize

@@ -154,6 +154,26 @@ def test_workspace_bytes():
         _lib.pdr_dense_kept_ld(-1)
 
 
+@pytest.mark.parametrize("which", ["M", "N", "K", "D", "F", "O", "m", "n", "batch"])
+def test_empty_lengths_need_no_pointers(which):
+    """Lengths of 0 are sized like any other (no matrix is looked at)."""
+    L = _lib.lib()
+    for fmt in (0, 1, 2):
+        if which in "MNK":
+            for act in (0, 3):
+                a = linear(fmt=fmt, out_fmt=fmt, activation=act, slope=FAKE, dx=FAKE, lddx=128, dw=FAKE, lddw=128,
+                           dbias=FAKE, **{which: 0})
+                assert L.pdr_linear_forward_workspace_bytes(ctypes.byref(a)) >= 0
+                assert L.pdr_linear_backward_workspace_bytes(ctypes.byref(a)) >= 0
+        if which in "MDFO":
+            a = gated(fmt=fmt, dw_in=FAKE, ldd_in=32, dw_out=FAKE, ldd_out=96, **{which: 0})
+            assert L.pdr_gated_mlp_forward_workspace_bytes(ctypes.byref(a)) >= 0
+            assert L.pdr_gated_mlp_backward_workspace_bytes(ctypes.byref(a)) >= 0
+        if which in ("m", "n", "batch"):
+            a = ortho(fmt=fmt, **{which: 0})
+            assert L.pdr_orthogonalize_workspace_bytes(ctypes.byref(a)) >= 0
+
+
 def test_cpu_tensors_are_refused():
     code = r'''
 import torch
