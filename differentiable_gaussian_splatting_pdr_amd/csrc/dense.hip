@@ -875,34 +875,36 @@ int pdr_orthogonalize(const pdr_orthogonalize_args *p, void *workspace, size_t w
 }  // extern "C"
 
 // How a product is cut into workgroups: 256x256 tiles, one workgroup on a
-// compute unit, or 128x128 tiles, two; and the contraction in one part or in
-// several, which a second kernel joins.  The choice is the least of an
+// compute unit, 128x128 or 64x64 tiles, two; and the contraction in one part or
+// in several, which a second kernel joins.  The choice is the least of an
 // estimate in microseconds whose constants are fits to measured products
 // (bf16, M x N x K, this card): a step is 64 contraction values of every
 // workgroup in flight.
-//   128: 2048x2048x2048 (256 workgroups) 22.9, 1024x1024x4096 (64) 34.2,
-//        4096x2048x2048 (512) 34.0, 8192x1024x2816 (512) 43.7
-//   256: 8192x1024x512 (128) 23.9, 16384x1024x1024 (256) 36.7,
-//        16384x2048x11264 (512, two rounds) 582; the same in 128 tiles: 687
-//   parts: 2048x2048x11264 in 256 tiles: one part 210, four 91.9;
-//        1024x1024x4096 in 128 tiles: one 34.2, four 21.6
+//   64:  512x512x512 (64 workgroups) 6.1, 1024x1024x1024 (256) 8.1,
+//        2048x1024x1024 (512) 10.8; in 128 tiles: 8.7, 12.2, 12.7
+//   128: 2048x2048x2048 (256) 22.8, 1024x1024x4096 (64) 33.6, 4096x2048x2048
+//        (512) 36.8, 8192x1024x2816 (512) 45.7; in 64 tiles: 32.3, 20.6, 59.9, 76.8
+//   256: 8192x1024x512 (128) 24.7, 16384x1024x1024 (256) 37.6,
+//        16384x2048x11264 (512, two rounds) 582; in 128 tiles: 15.1, 38.8, 687
+//   parts: 2048x2048x11264 in 256 tiles: one part 214, four 91.9;
+//        512x512x4096 in 64 tiles: one 18.5, four 12.7
 namespace pdr {
 namespace dense {
 
 namespace {
 
-double tiles_us(bool large, double workgroups, double steps) {
-  const double slots = large ? 256.0 : 512.0;
+double tiles_us(int tile, double workgroups, double steps) {
+  const double slots = tile == 256 ? 256.0 : 512.0;
+  const double fixed = tile == 256 ? 9.0 : tile == 128 ? 5.0 : 3.0;
+  // a round with every slot taken, with half of them, with fewer
+  const double full = tile == 256 ? 1.5 : tile == 128 ? 0.9 : 0.43;
+  const double half = tile == 256 ? 1.2 : tile == 128 ? 0.57 : 0.28;
+  const double few = tile == 256 ? 1.2 : tile == 128 ? 0.45 : 0.25;
   const double rounds = floor(workgroups / slots), rest = workgroups - rounds * slots;
-  const double full = large ? 1.5 * steps + 9.0 : 0.9 * steps + 5.0;
-  double last = 0.0;
-  if (rest > 0.0) {
-    if (large)
-      last = (rest > 128.0 ? 1.5 : 1.2) * steps + 9.0;
-    else
-      last = rest > 256.0 ? full : 0.46 * steps + 4.0;
-  }
-  return rounds * full + last;
+  double us = rounds * (full * steps + fixed);
+  if (rest > 0.0)
+    us += (rest > slots / 2 ? full : rest > slots / 4 ? half : few) * steps + fixed;
+  return us;
 }
 
 }  // namespace
@@ -914,14 +916,14 @@ TilePlan plan_tiles(const GemmArgs &g, EpiKind kind) {
   const int most = kind == kEpiGated ? 1 : steps / 2 > 32 ? 32 : steps / 2 > 1 ? steps / 2 : 1;
   TilePlan best = {};
   double least = 0.0;
-  for (int large = 0; large < 2; ++large) {
-    const int bm = large ? 256 : 128, bn = kind == kEpiGated ? bm / 2 : bm;
+  for (int bm = 64; bm <= 256; bm *= 2) {
+    const int bn = kind == kEpiGated ? bm / 2 : bm;
     TilePlan p;
-    p.large = large != 0;
+    p.tile = bm;
     p.tiles_m = (g.M + bm - 1) / bm;
     p.tiles_n = (g.epi.store_n + bn - 1) / bn;
     for (p.splits = 1; p.splits <= most; ++p.splits) {
-      double us = tiles_us(p.large, batches * p.tiles_m * p.tiles_n * p.splits,
+      double us = tiles_us(bm, batches * p.tiles_m * p.tiles_n * p.splits,
                            (double)((steps + p.splits - 1) / p.splits));
       // the parts are written and read once, at 4.6 TB/s
       if (p.splits > 1) us += 3.0 + 8.0 * sums * p.splits / 4.6e6;

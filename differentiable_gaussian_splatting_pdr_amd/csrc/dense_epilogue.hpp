@@ -383,13 +383,14 @@ struct Columns<kEpiGated, W, FLAGS> {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// Column c of row r of a wave's 64 staged rows of COLS sums.
+// Column c of row r of a wave's staged rows of COLS sums: 16-byte chunks are
+// moved by the row, so that rows of one chunk fall on different banks.
 template <int COLS>
 __device__ __forceinline__ const char *staged(const char *mine, int r, int c) {
-  return mine + r * (COLS * 4) + ((((c >> 2) ^ (r & 15))) << 4) + (c & 3) * 4;
+  return mine + r * (COLS * 4) + ((((c >> 2) ^ (r & (COLS >= 64 ? 15 : 7)))) << 4) + (c & 3) * 4;
 }
 
-// The epilogue of `rows` (1 to 64) staged rows m0.. and their columns n0..,
+// The epilogue of `rows` staged rows m0.. and their columns n0..,
 // W columns of a row to a lane at a time.  A gated product's staged columns
 // are 8 gate sums, the 8 up sums of the same columns, and so on.  The next
 // rows are fetched before the present ones are stored.
@@ -416,13 +417,14 @@ __device__ __forceinline__ void finish_rows(const Epi &e, const char *mine, int 
     // what the columns need is there, so that nothing in the loop waits for it
     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
 #pragma unroll 1
-    for (int r0 = lane / kLanes; r0 < 64 && r0 < rows; r0 += kRows * kAtOnce) {
+    for (int r0 = lane / kLanes; r0 < rows; r0 += kRows * kAtOnce) {
       float v[kAtOnce][DUAL ? 2 * W : W];
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u) row[u] = next[u];
       fetch(r0 + kRows * kAtOnce);
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u) {
+        // a row past the last is read (the staged rows go on) and not used
         const int r = r0 + u * kRows;
 #pragma unroll
         for (int k = 0; k < (DUAL ? 2 : 1); ++k) {
@@ -494,7 +496,7 @@ __device__ __forceinline__ void store_staged(const char *mine, int lane, float *
   const int left = N - n0 - c;
   if (left <= 0) return;
 #pragma unroll 2
-  for (int r = lane / kLanes; r < 64 && r < rows; r += kRows) {
+  for (int r = lane / kLanes; r < rows; r += kRows) {
     const f32x4 w = *(const f32x4 *)staged<COLS>(mine, r, c);
     float *to = part + (long long)(m0 + r) * N + n0 + c;
     if ((N & 3) == 0) {

@@ -84,10 +84,11 @@ __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" :
 // LDS swizzles: 16-byte chunk c of tile row r is stored at chunk c ^ s(r), so
 // that the lanes of one read phase fall on different banks (counted: no
 // conflicts).  A kc read takes rows 0..15 of one chunk: s = r & 7.  A mc read
-// takes 32 bytes of each of 4 rows per 16 lanes: s moves pairs of chunks.
-template <bool MC>
+// takes 32 bytes of each of 4 rows per 16 lanes: s moves pairs of chunks (of
+// the 8 that a row of 64 values has, or within 16).
+template <bool MC, int ROWS>
 __device__ __forceinline__ int swizzle(int r) {
-  return MC ? ((r & 3) << 1) | (((r >> 3) & 1) << 3) : r & 7;
+  return MC ? ((r & 3) << 1) | (ROWS > 64 ? ((r >> 3) & 1) << 3 : 0) : r & 7;
 }
 
 // A value that is the same in every lane, told to the compiler.
@@ -126,7 +127,7 @@ struct Loader {
       const int blk = i * NW + wave;
       if constexpr (!MC) {
         const int r = blk * 8 + (lane >> 3);
-        const int c = (lane & 7) ^ swizzle<false>(r);
+        const int c = (lane & 7) ^ swizzle<false, ROWS>(r);
         chunk_k = c * 8;  // the same for every issue: r % 8 is
         if constexpr (DUAL) {
           // LDS rows 16 j .. 16 j + 7 hold gate columns 8 j .. 8 j + 7, the 8 rows
@@ -139,7 +140,7 @@ struct Loader {
       } else {
         constexpr int kLanesPerRow = ROWS / 8;
         const int k = blk * (64 / kLanesPerRow) + lane / kLanesPerRow;
-        const int c = (lane % kLanesPerRow) ^ swizzle<true>(k);
+        const int c = (lane % kLanesPerRow) ^ swizzle<true, ROWS>(k);
         voff[i] = (uint32_t)k * (uint32_t)ld * 2u + c * 16;
       }
     }
@@ -228,13 +229,13 @@ struct Reader {
     if constexpr (!MC) {
       const int r = row0 + t;
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) at[ks] = r * 128 + (((ks * 4 + g) ^ swizzle<false>(r)) << 4);
+      for (int ks = 0; ks < 2; ++ks) at[ks] = r * 128 + (((ks * 4 + g) ^ swizzle<false, ROWS>(r)) << 4);
     } else {
       const int k = 8 * g + (t >> 2), q = t & 3;
 #pragma unroll
       for (int v = 0; v < kVar; ++v) {
         const int c = row0 / 8 + 2 * v + (q >> 1);
-        at[v] = k * (ROWS * 2) + ((c ^ swizzle<true>(k)) << 4) + (q & 1) * 8;
+        at[v] = k * (ROWS * 2) + ((c ^ swizzle<true, ROWS>(k)) << 4) + (q & 1) * 8;
       }
     }
   }
@@ -277,17 +278,17 @@ __device__ __forceinline__ void pick_tile(const GemmArgs &g, int id, int *tm, in
 //
 // Schedule.  Tiles are TS x TS x 64, 4 waves.  A wave keeps the fragments of
 // two 32-value steps in registers: while the matrix cores work on one step,
-// the next step's fragments are read from LDS.  LDS holds five half tiles (A_t
-// or B_t) in a ring, all of the 160 KB with one workgroup of 256 x 256 or two
-// of 128 x 128 on a compute unit:
-//   step 0 of tile t: read step 1 of tile t; in small tiles, load A of t + 2
+// the next step's fragments are read from LDS.  LDS holds 2 d + 1 half tiles
+// (A_t or B_t) in a ring, d tiles ahead: d = 2 for 256 x 256 (all of the 160 KB)
+// and 128 x 128 (two workgroups on a compute unit), 4 for 64 x 64 (two):
+//   step 0 of tile t: read step 1 of tile t; below 256, load A of t + d
 //   wait for A and B of t + 1, barrier: the halves of t are free
-//   step 1 of tile t: read step 0 of tile t + 1, load B of t + 2; in large
-//     tiles, also A of t + 3
+//   step 1 of tile t: read step 0 of tile t + 1, load B of t + d; at 256, also
+//     A of t + d + 1
 // One barrier a tile, and no wait between a read or load and the next matrix
-// instruction.  Loads are spread out, one every 4 matrix instructions of each
-// wave: a load holds the address path for 16 clocks and a wave that meets it
-// busy stops issuing matrix instructions too.
+// instruction.  Loads are spread out between the matrix instructions: a load
+// holds the address path for 16 clocks and a wave that meets it busy stops
+// issuing matrix instructions too.
 template <int FMT, int TS, bool A_MC, bool B_MC, int EPI>
 __global__ __launch_bounds__(256) void k_gemm(GemmArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the body is device builtins throughout
@@ -295,7 +296,7 @@ __global__ __launch_bounds__(256) void k_gemm(GemmArgs g) {
   constexpr bool DUAL = EPI == kEpiGated;
   using LA = Loader<TS, A_MC, NW, false>;
   using LB = Loader<TS, B_MC, NW, DUAL>;
-  constexpr int kHalf = LA::kBytes, kRing = 5;
+  constexpr int kHalf = LA::kBytes, kRing = TS == 64 ? 9 : 5, kAhead = kRing / 2;
   __shared__ __align__(1024) char smem[kRing * kHalf];
 
   const int lane = threadIdx.x & 63;
@@ -351,21 +352,22 @@ __global__ __launch_bounds__(256) void k_gemm(GemmArgs g) {
 #pragma unroll
       for (int i = 0; i < LB::kIssues; ++i) lb.load(i, s, wave);
     };
-    load_a(smem);
-    load_b(smem + kHalf);
-    la.next(wave, lane);
-    lb.next(wave, lane);
-    load_a(smem + 2 * kHalf);
-    load_b(smem + 3 * kHalf);
-    la.next(wave, lane);
-    lb.next(wave, lane);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      load_a(smem + 2 * i * kHalf);
+      load_b(smem + (2 * i + 1) * kHalf);
+      la.next(wave, lane);
+      lb.next(wave, lane);
+    }
     constexpr int kMfma = MT * NT, kReads = MT + NT, kLoads = LA::kIssues + LB::kIssues;
-    constexpr int kPer = kMfma / 2 / kReads;  // matrix instructions between reads
-    // one load every 4 matrix instructions: all in step 1, or those of A in step 0
-    constexpr bool kLate = kLoads > kMfma / 4;
-    static_assert(kPer >= 1 && LB::kIssues <= kMfma / 4 && LA::kIssues <= kMfma / 4, "the loads fit");
+    constexpr int kPer = kMfma / 2 > kReads ? kMfma / 2 / kReads : 1;  // matrix instructions between reads
+    constexpr int kGap = kMfma > 4 ? 4 : 2;                            // and between loads:
+    // all in step 1, or those of A in step 0
+    constexpr bool kLate = kLoads > kMfma / kGap;
+    static_assert(kReads * kPer <= kMfma && LB::kIssues <= kMfma / kGap && LA::kIssues <= kMfma / kGap,
+                  "reads and loads fit");
     if constexpr (!kLate) {
-      load_a(smem + 4 * kHalf);
+      load_a(smem + 2 * kAhead * kHalf);
       la.next(wave, lane);
     }
 
@@ -374,7 +376,7 @@ __global__ __launch_bounds__(256) void k_gemm(GemmArgs g) {
     Reader<TS, B_MC> rb;
     ra.init(lane, wm * WS);
     rb.init(lane, wn * WS);
-    landed<(kLate ? 1 : 2) * LA::kIssues + LB::kIssues>();
+    landed<(kLate ? kAhead - 1 : kAhead) * LA::kIssues + (kAhead - 1) * LB::kIssues>();
 #pragma unroll
     for (int j = 0; j < NT; ++j) fb[0][j] = rb.get(smem + kHalf, j, 0);
 #pragma unroll
@@ -382,7 +384,7 @@ __global__ __launch_bounds__(256) void k_gemm(GemmArgs g) {
 
     int slot = 0;                // of A_t; B_t in the next one
     char *sa = smem, *sb = smem + kHalf;
-    char *to = smem + 4 * kHalf, *free_b = smem;  // where the next A and B go
+    char *to = smem + 2 * kAhead * kHalf, *free_b = smem;  // where the next A and B go
     settle();
     for (int t = 0; t < tiles; ++t) {
 #pragma unroll
@@ -394,21 +396,21 @@ __global__ __launch_bounds__(256) void k_gemm(GemmArgs g) {
           else
             fa[1][r - NT] = ra.get(sa, r - NT, 1);
         }
-        if (kLate && x % 4 == 2 && x / 4 < LA::kIssues) la.load(x / 4, to, wave);
-        if (x == kMfma - 2) {
-          slot = slot >= 3 ? slot - 3 : slot + 2;
-          free_b = sa;  // B of t + 2 goes where A of t was, the next A where B was
+        if (kLate && x % kGap == kGap / 2 && x / kGap < LA::kIssues) la.load(x / kGap, to, wave);
+        if (x == kMfma - 1) {
+          slot = slot >= kRing - 2 ? slot - (kRing - 2) : slot + 2;
+          free_b = sa;  // the next B goes where A of t was, the next A where B was
           to = sb;
           sa = smem + slot * kHalf;
-          sb = smem + (slot == 4 ? 0 : slot + 1) * kHalf;
+          sb = smem + (slot == kRing - 1 ? 0 : slot + 1) * kHalf;
           if (kLate) la.next(wave, lane);
         }
         __builtin_amdgcn_sched_barrier(0);
         mfma<FMT>(acc[x / NT][x % NT], fb[0][x % NT], fa[0][x / NT]);
         __builtin_amdgcn_sched_barrier(0);
       }
-      // all that may be in flight is A of t + 2
-      landed<LA::kIssues>();
+      // what was loaded after B of t + 1 may be in flight
+      landed<(kAhead - 1) * LA::kIssues + (kAhead - 2) * LB::kIssues>();
 #pragma unroll
       for (int x = 0; x < kMfma; ++x) {
         if (x % kPer == 0 && x / kPer < kReads) {
@@ -418,11 +420,11 @@ __global__ __launch_bounds__(256) void k_gemm(GemmArgs g) {
           else
             fa[0][r - NT] = ra.get(sa, r - NT, 0);
         }
-        if (x % 4 == 2) {
-          if (x / 4 < LB::kIssues)
-            lb.load(x / 4, free_b, wave);
-          else if (!kLate && x / 4 < kLoads)
-            la.load(x / 4 - LB::kIssues, to, wave);
+        if (x % kGap == kGap / 2) {
+          if (x / kGap < LB::kIssues)
+            lb.load(x / kGap, free_b, wave);
+          else if (!kLate && x / kGap < kLoads)
+            la.load(x / kGap - LB::kIssues, to, wave);
         }
         if (x == kMfma - 1) {
           lb.next(wave, lane);
@@ -437,26 +439,26 @@ __global__ __launch_bounds__(256) void k_gemm(GemmArgs g) {
   settle();
   landed<0>();
 
-  // Sums go through LDS, 64 rows of a wave at a time, so that what follows
+  // Sums go through LDS, up to 64 rows of a wave at a time, so that what follows
   // reads and writes whole rows, and its code is small: it runs once, and
-  // instructions that run once are paid for in fetches.  16-byte chunk c of
-  // row m lies at chunk c ^ (m & 15).
-  char *const mine = smem + wave * 64 * (WS * 4);
+  // instructions that run once are paid for in fetches.
+  constexpr int kStaged = WS < 64 ? WS : 64, kTiles = kStaged / 16;
+  char *const mine = smem + wave * kStaged * (WS * 4);
   const int first = row0 + wm * WS, n0 = col0 + wn * (DUAL ? WS / 2 : WS);
 #pragma unroll 1
-  for (int h = 0; h < MT / 4; ++h) {
+  for (int h = 0; h < MT / kTiles; ++h) {
     const int m_in = lane & 15, q = lane >> 4;
 #pragma unroll
-    for (int hh = 0; hh < MT / 4; ++hh)
+    for (int hh = 0; hh < MT / kTiles; ++hh)
       if (h == hh) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kTiles; ++i)
 #pragma unroll
           for (int j = 0; j < NT; ++j)
-            *(f32x4 *)(mine + (i * 16 + m_in) * (WS * 4) + (((j * 4 + q) ^ m_in) << 4)) =
-                acc[hh * 4 + i][j];
+            *(f32x4 *)const_cast<char *>(staged<WS>(mine, i * 16 + m_in, j * 16 + q * 4)) =
+                acc[hh * kTiles + i][j];
       }
-    const int m0 = first + h * 64, rows = g.M - m0;
+    const int m0 = first + h * kStaged, rows = g.M - m0 < kStaged ? g.M - m0 : kStaged;
     if (g.splits > 1) {
       if constexpr (!DUAL)
         store_staged<WS>(mine, lane, g.partial + ((long long)split * g.batches + batch) * g.M * g.N,

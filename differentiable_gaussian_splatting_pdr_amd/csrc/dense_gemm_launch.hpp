@@ -50,10 +50,12 @@ hipError_t launch_one(GemmArgs g, void *ws, hipStream_t st) {
   g.partial = (float *)ws;
   g.epi.vec = g.epi.vec && (g.epi.store_n & 7) == 0;
   const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)p.splits, (unsigned)g.batches);
-  if (p.large)
+  if (p.tile == 256)
     hipLaunchKernelGGL((k_gemm<FMT, 256, A_MC, B_MC, EPI>), grid, dim3(256), 0, st, g);
-  else
+  else if (p.tile == 128)
     hipLaunchKernelGGL((k_gemm<FMT, 128, A_MC, B_MC, EPI>), grid, dim3(256), 0, st, g);
+  else
+    hipLaunchKernelGGL((k_gemm<FMT, 64, A_MC, B_MC, EPI>), grid, dim3(256), 0, st, g);
   if constexpr (EPI != kEpiGated) {
     if (p.splits > 1) {
       const int w = g.epi.vec ? 8 : 1;

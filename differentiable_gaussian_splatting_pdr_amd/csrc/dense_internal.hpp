@@ -15,7 +15,7 @@ size_t gemm_scratch_bytes(const GemmArgs &g, EpiKind kind);
 
 struct TilePlan {
   int tiles_m, tiles_n, splits;
-  bool large;  // 256x256 tiles, else 128x128
+  int tile;  // rows and columns: 256, 128 or 64
 };
 TilePlan plan_tiles(const GemmArgs &g, EpiKind kind);
 
