@@ -49,60 +49,81 @@ __device__ __forceinline__ float finite_abs(float v) {
   return a < INFINITY ? a : 0.f;
 }
 
-// Copy a 16-bit matrix to rows of ldd elements (a multiple of 8), zeros after
-// each row's end.  One thread per 8 values.
-__global__ __launch_bounds__(kThreads) void k_repack(const uint16_t *__restrict__ src, long long ld,
-                                                     int rows, int cols, uint16_t *__restrict__ dst,
-                                                     int ldd, FastDiv groups) {
-  const uint32_t at = blockIdx.x * kThreads + threadIdx.x;
-  const uint32_t r = fdiv(at, groups);
-  if (r >= (uint32_t)rows) return;
-  const int c = (int)(at - r * groups.d) * 8;
+// Matrices to lay out for the products, several to a launch: workgroups
+// [first, first of the next) of a pass work on one matrix.
+constexpr int kMaxPrep = 6;
+struct Prep {
+  const void *src;
+  long long ld;
+  int rows, cols, vec;
+  FastDiv groups;     // by the groups of 8 of a row
+  uint16_t *hi, *lo;  // rows of ldd elements (a multiple of 8), zeros after each row's end
+  int ldd;
+  float *part;        // largest magnitudes of an fp32 matrix, `parts` of them
+  int parts;
+  int *exp;           // the exponent of its scale
+  unsigned first, first_part;
+};
+struct PrepBatch {
+  Prep item[kMaxPrep];
+  int count;
+};
+__device__ __forceinline__ int prep_of(const PrepBatch &b, unsigned block) {
+  int i = 0;
+  while (i + 1 < b.count && block >= b.item[i + 1].first) ++i;
+  return i;
+}
+
+// Copy 16-bit matrices.  One thread per 8 values.
+__global__ __launch_bounds__(kThreads) void k_repack(PrepBatch b) {
+  const Prep &p = b.item[prep_of(b, blockIdx.x)];
+  const uint32_t at = (blockIdx.x - p.first) * kThreads + threadIdx.x;
+  const uint32_t r = fdiv(at, p.groups);
+  if (r >= (uint32_t)p.rows) return;
+  const int c = (int)(at - r * p.groups.d) * 8;
+  const uint16_t *src = (const uint16_t *)p.src + r * p.ld + c;
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (c + i < cols) w[i >> 1] |= (uint32_t)src[r * ld + c + i] << ((i & 1) * 16);
-  *(uint4 *)(dst + (long long)r * ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (c + i < p.cols) w[i >> 1] |= (uint32_t)src[i] << ((i & 1) * 16);
+  *(uint4 *)(p.hi + (long long)r * p.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Largest finite magnitude of an fp32 matrix, one value per workgroup.
-__global__ __launch_bounds__(kThreads) void k_amax(const float *__restrict__ src, long long ld,
-                                                   int rows, int cols, int vec, FastDiv groups,
-                                                   float *__restrict__ part) {
-  const uint32_t total = (uint32_t)rows * groups.d;
+// Largest finite magnitudes of fp32 matrices, one value per workgroup.
+__global__ __launch_bounds__(kThreads) void k_amax(PrepBatch b) {
+  int i = 0;
+  while (i + 1 < b.count && blockIdx.x >= b.item[i + 1].first_part) ++i;
+  const Prep &p = b.item[i];
+  const uint32_t total = (uint32_t)p.rows * p.groups.d, block = blockIdx.x - p.first_part;
   float best = 0.f;
 #pragma unroll 4
-  for (uint32_t at = blockIdx.x * kThreads + threadIdx.x; at < total; at += gridDim.x * kThreads) {
-    const uint32_t r = fdiv(at, groups);
-    const int c = (int)(at - r * groups.d) * 8;
+  for (uint32_t at = block * kThreads + threadIdx.x; at < total; at += p.parts * kThreads) {
+    const uint32_t r = fdiv(at, p.groups);
+    const int c = (int)(at - r * p.groups.d) * 8;
     float v[8];
-    load8(src, kF32, r * ld + c, cols - c, vec, v);
+    load8(p.src, kF32, r * p.ld + c, p.cols - c, p.vec, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) best = fmaxf(best, finite_abs(v[i]));
+    for (int j = 0; j < 8; ++j) best = fmaxf(best, finite_abs(v[j]));
   }
   best = block_max(best);
-  if (threadIdx.x == 0) part[blockIdx.x] = best;
+  if (threadIdx.x == 0) p.part[block] = best;
 }
 
-// Split an fp32 matrix into fp16 planes hi + lo under the scale 2^e that
-// brings its largest value to [2^14, 2^15); e goes to *exp.
-__global__ __launch_bounds__(kThreads) void k_split(const float *__restrict__ src, long long ld,
-                                                    int rows, int cols, int vec, FastDiv groups,
-                                                    const float *__restrict__ part, int parts,
-                                                    uint16_t *__restrict__ hi,
-                                                    uint16_t *__restrict__ lo, int ldd,
-                                                    int *__restrict__ exp) {
-  const uint32_t at = blockIdx.x * kThreads + threadIdx.x;
-  const uint32_t r = fdiv(at, groups);
-  const int c = (int)(at - r * groups.d) * 8;
-  const bool mine = r < (uint32_t)rows;
+// Split fp32 matrices into fp16 planes hi + lo under the scale 2^e that brings
+// a matrix's largest value to [2^14, 2^15); e goes to *exp.
+__global__ __launch_bounds__(kThreads) void k_split(PrepBatch b) {
+  const Prep &p = b.item[prep_of(b, blockIdx.x)];
+  const uint32_t block = blockIdx.x - p.first, at = block * kThreads + threadIdx.x;
+  const uint32_t r = fdiv(at, p.groups);
+  const int c = (int)(at - r * p.groups.d) * 8;
+  const bool mine = r < (uint32_t)p.rows;
   float v[8];
-  if (mine) load8(src, kF32, r * ld + c, cols - c, vec, v);
+  if (mine) load8(p.src, kF32, r * p.ld + c, p.cols - c, p.vec, v);
   float amax = 0.f;
-  for (int i = threadIdx.x; i < parts; i += kThreads) amax = fmaxf(amax, part[i]);
+  for (int i = threadIdx.x; i < p.parts; i += kThreads) amax = fmaxf(amax, p.part[i]);
   amax = block_max(amax);
   const int e = amax > 0.f ? 14 - ilogbf(amax) : 0;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *exp = e;
+  if (block == 0 && threadIdx.x == 0) *p.exp = e;
   if (!mine) return;
   float h[8], l[8];
 #pragma unroll
@@ -111,8 +132,8 @@ __global__ __launch_bounds__(kThreads) void k_split(const float *__restrict__ sr
     h[i] = f16_to_f(f_to_f16(s));
     l[i] = fabsf(s) < INFINITY ? s - h[i] : 0.f;
   }
-  store_w<8>(hi, kF16, (long long)r * ldd + c, h);
-  store_w<8>(lo, kF16, (long long)r * ldd + c, l);
+  store_w<8>(p.hi, kF16, (long long)r * p.ldd + c, h);
+  store_w<8>(p.lo, kF16, (long long)r * p.ldd + c, l);
 }
 
 // dz = dy * slope (no slope: dz = dy), rounded to the products' format, and
@@ -274,6 +295,7 @@ struct Walk {
   hipStream_t st = nullptr;
   bool run = false;
   hipError_t err = hipSuccess;
+  PrepBatch repack = {}, split = {};  // laid out by flush(), before the next product
 
   void *take(size_t bytes) {
     void *p = base + at;
@@ -285,6 +307,11 @@ struct Walk {
     if (err == hipSuccess) err = e;
   }
   bool go() const { return run && err == hipSuccess; }
+  void add(PrepBatch &b, const Prep &p) {
+    if (b.count == kMaxPrep) flush();
+    b.item[b.count++] = p;
+  }
+  void flush();
 };
 
 // A matrix as the products read it: one 16-bit plane, or two of a split fp32.
@@ -302,9 +329,38 @@ unsigned parts_for(long long threads) {
   return (unsigned)(b < 1 ? 1 : b < kParts ? b : kParts);
 }
 
+void Walk::flush() {
+  if (go()) {
+    unsigned blocks = 0, parts = 0;
+    for (int i = 0; i < repack.count; ++i) {
+      Prep &p = repack.item[i];
+      p.first = blocks;
+      blocks += blocks_for((long long)p.rows * p.groups.d);
+    }
+    if (blocks) hipLaunchKernelGGL(k_repack, dim3(blocks), dim3(kThreads), 0, st, repack);
+    // the matrices whose largest value is not known yet come first
+    PrepBatch scan = {};
+    blocks = 0;
+    for (int i = 0; i < split.count; ++i) {
+      Prep &p = split.item[i];
+      p.first = blocks;
+      blocks += blocks_for((long long)p.rows * p.groups.d);
+      if (p.parts) continue;
+      p.parts = (int)parts_for((long long)p.rows * p.groups.d);
+      p.first_part = parts;
+      parts += (unsigned)p.parts;
+      scan.item[scan.count++] = p;
+    }
+    if (parts) hipLaunchKernelGGL(k_amax, dim3(parts), dim3(kThreads), 0, st, scan);
+    if (blocks) hipLaunchKernelGGL(k_split, dim3(blocks), dim3(kThreads), 0, st, split);
+    done(hipGetLastError());
+  }
+  repack.count = split.count = 0;
+}
+
 // `amax`, if given: `parts` values whose largest is p's largest magnitude.
 Planes lay_out(Walk &w, const void *p, int fmt, long long ld, long long rows, long long cols,
-               bool summed_along_row, const float *amax = nullptr, int parts = 0) {
+               bool summed_along_row, float *amax = nullptr, int parts = 0) {
   Planes r;
   if (rows == 0 || cols == 0) {
     r.ld = round8(cols > 0 ? cols : 1);
@@ -315,36 +371,27 @@ Planes lay_out(Walk &w, const void *p, int fmt, long long ld, long long rows, lo
     r.ld = ld;
     return r;
   }
-  const long long ldd = round8(cols), threads = rows * (ldd / 8);
-  const FastDiv groups = make_fastdiv((uint32_t)(ldd / 8));
-  uint16_t *hi = (uint16_t *)w.take((size_t)(rows * ldd) * 2);
-  r.hi = hi;
+  const long long ldd = round8(cols);
+  Prep m = {};
+  m.src = p;
+  m.ld = ld;
+  m.rows = (int)rows;
+  m.cols = (int)cols;
+  m.vec = aligned16(p) && (ld & 7) == 0;
+  m.groups = make_fastdiv((uint32_t)(ldd / 8));
+  m.ldd = (int)ldd;
+  m.hi = (uint16_t *)w.take((size_t)(rows * ldd) * 2);
+  if (fmt == kF32) {
+    m.lo = (uint16_t *)w.take((size_t)(rows * ldd) * 2);
+    m.part = amax ? amax : (float *)w.take(kParts * sizeof(float));
+    m.parts = amax ? parts : 0;
+    m.exp = (int *)w.take(sizeof(int));
+  }
+  r.hi = m.hi;
+  r.lo = m.lo;
+  r.exp = m.exp;
   r.ld = ldd;
-  if (fmt != kF32) {
-    if (w.go()) {
-      hipLaunchKernelGGL(k_repack, dim3(blocks_for(threads)), dim3(kThreads), 0, w.st,
-                         (const uint16_t *)p, ld, (int)rows, (int)cols, hi, (int)ldd, groups);
-      w.done(hipGetLastError());
-    }
-    return r;
-  }
-  uint16_t *lo = (uint16_t *)w.take((size_t)(rows * ldd) * 2);
-  float *part = amax ? nullptr : (float *)w.take(kParts * sizeof(float));
-  int *exp = (int *)w.take(sizeof(int));
-  r.lo = lo;
-  r.exp = exp;
-  if (w.go()) {
-    const int vec = aligned16(p) && (ld & 7) == 0;
-    if (!amax) {
-      parts = (int)parts_for(threads);
-      hipLaunchKernelGGL(k_amax, dim3((unsigned)parts), dim3(kThreads), 0, w.st, (const float *)p, ld,
-                         (int)rows, (int)cols, vec, groups, part);
-      amax = part;
-    }
-    hipLaunchKernelGGL(k_split, dim3(blocks_for(threads)), dim3(kThreads), 0, w.st, (const float *)p,
-                       ld, (int)rows, (int)cols, vec, groups, amax, parts, hi, lo, (int)ldd, exp);
-    w.done(hipGetLastError());
-  }
+  w.add(fmt == kF32 ? w.split : w.repack, m);
   return r;
 }
 
@@ -376,6 +423,7 @@ GemmArgs product(long long M, long long N, long long K) {
 }
 
 void multiply(Walk &w, const GemmArgs &g, int fmt, bool a_mc, bool b_mc, EpiKind kind) {
+  w.flush();
   const size_t keep = w.at;
   void *ws = w.take(gemm_scratch_bytes(g, kind));
   if (w.go())
@@ -511,9 +559,9 @@ void linear_backward(Walk &w, const pdr_linear &p) {
   if (!products) return;
   const Planes z = lay_out(w, dz, p.fmt, ld_dz, p.M, write ? round8(p.N) : p.N, p.dx != nullptr, amax,
                            (int)(row_blocks * col_blocks));
+  const Planes wt = p.dx ? lay_out(w, p.w, p.fmt, p.ldw, p.N, p.K, false) : Planes();
+  const Planes x = p.dw ? lay_out(w, p.x, p.fmt, p.ldx, p.M, p.K, false) : Planes();
   if (p.dx) {
-    const size_t keep = w.at;
-    const Planes wt = lay_out(w, p.w, p.fmt, p.ldw, p.N, p.K, false);
     GemmArgs g = product(p.M, p.K, round8(p.N));
     g.kb = (int)p.N;
     add_product(g, z, 0, wt, 0);
@@ -521,10 +569,8 @@ void linear_backward(Walk &w, const pdr_linear &p) {
     g.epi.exp_a = z.exp;
     g.epi.exp_b = wt.exp;
     multiply(w, g, p.fmt, false, true, kEpiLinear);
-    w.at = keep;
   }
   if (p.dw) {
-    const Planes x = lay_out(w, p.x, p.fmt, p.ldx, p.M, p.K, false);
     GemmArgs g = product(p.N, p.K, p.M);
     add_product(g, z, 0, x, 0);
     set_out(g.epi, p.dw, p.fmt, p.lddw);
@@ -577,6 +623,7 @@ void gated_forward(Walk &w, const pdr_gated_mlp &p) {
     multiply_few(w, p.x, p.ldx, p.w_in, p.ld_in, p.F * p.ld_in, p.M, p.F, p.D, in, p.fmt, true);
     return multiply_few(w, p.h, Fp, p.w_out, p.ld_out, 0, p.M, p.O, p.F, out, p.fmt, false);
   }
+  const Planes wo = lay_out(w, p.w_out, p.fmt, p.ld_out, p.O, p.F, true);
   {
     const size_t keep = w.at;
     const Planes x = lay_out(w, p.x, p.fmt, p.ldx, p.M, p.D, true);
@@ -591,7 +638,6 @@ void gated_forward(Walk &w, const pdr_gated_mlp &p) {
     w.at = keep;
   }
   const Planes h = lay_out(w, p.h, p.fmt, Fp, p.M, Fp, true);
-  const Planes wo = lay_out(w, p.w_out, p.fmt, p.ld_out, p.O, p.F, true);
   GemmArgs g = product(p.M, p.O, Fp);
   add_product(g, h, 0, wo, 0);
   g.epi = out;
@@ -604,6 +650,9 @@ void gated_backward(Walk &w, const pdr_gated_mlp &p) {
   const long long Fp = round8(p.F);
   const bool through = p.dx || p.dw_in;
   const Planes dy = lay_out(w, p.dy, p.fmt, p.lddy, p.M, p.O, through);
+  const Planes x = p.dw_in ? lay_out(w, p.x, p.fmt, p.ldx, p.M, p.D, false) : Planes();
+  const Planes wi = p.dx ? lay_out(w, p.w_in, p.fmt, p.ld_in, 2 * p.F, p.D, false) : Planes();
+  const Planes wo = through ? lay_out(w, p.w_out, p.fmt, p.ld_out, p.O, p.F, false) : Planes();
   if (p.dw_out) {
     const size_t keep = w.at;
     const Planes h = lay_out(w, p.h, p.fmt, Fp, p.M, Fp, false);
@@ -618,8 +667,6 @@ void gated_backward(Walk &w, const pdr_gated_mlp &p) {
   if (!through) return;
   void *dgu = w.take((size_t)(p.M * 2 * Fp) * fmt_bytes(p.fmt));
   {
-    const size_t keep = w.at;
-    const Planes wo = lay_out(w, p.w_out, p.fmt, p.ld_out, p.O, p.F, false);
     GemmArgs g = product(p.M, p.F, round8(p.O));
     g.kb = (int)p.O;
     add_product(g, dy, 0, wo, 0);
@@ -632,12 +679,9 @@ void gated_backward(Walk &w, const pdr_gated_mlp &p) {
     g.epi.gu = (float *)p.gu;
     g.epi.ld_gu = (int)Fp;
     multiply(w, g, p.fmt, false, true, kEpiGatedGrad);
-    w.at = keep;
   }
   const Planes d = lay_out(w, dgu, p.fmt, 2 * Fp, p.M, 2 * Fp, true);
   if (p.dx) {
-    const size_t keep = w.at;
-    const Planes wi = lay_out(w, p.w_in, p.fmt, p.ld_in, 2 * p.F, p.D, false);
     GemmArgs g = product(p.M, p.D, Fp);
     g.kb = (int)p.F;
     add_product(g, d, 0, wi, 0);
@@ -646,10 +690,8 @@ void gated_backward(Walk &w, const pdr_gated_mlp &p) {
     g.epi.exp_a = d.exp;
     g.epi.exp_b = wi.exp;
     multiply(w, g, p.fmt, false, true, kEpiLinear);
-    w.at = keep;
   }
   if (p.dw_in) {
-    const Planes x = lay_out(w, p.x, p.fmt, p.ldx, p.M, p.D, false);
     GemmArgs g = product(p.F, p.D, p.M);
     add_product(g, d, 0, x, 0);
     g.batches = 2;  // the gate rows, then the up rows
@@ -753,6 +795,7 @@ void orthogonalize(Walk &w, const pdr_orthogonalize_args &p) {
     {  // A = X X^T or X^T X
       GemmArgs g = product(s, s, tall ? p.m : np);
       add_product(g, xi, 0, xi, 0);
+      g.symmetric = 1;
       g.batches = (int)p.batch;
       g.batch_a = g.batch_b = p.m * np;
       to(g.epi, a, s * sp);
@@ -763,6 +806,7 @@ void orthogonalize(Walk &w, const pdr_orthogonalize_args &p) {
     {  // B = b A + c A A; A is symmetric, so its rows serve as its columns
       GemmArgs g = product(s, s, sp);
       add_product(g, a, 0, a, 0);
+      g.symmetric = 1;
       g.batches = (int)p.batch;
       g.batch_a = g.batch_b = s * sp;
       to(g.epi, b, s * sp);
@@ -888,14 +932,16 @@ int pdr_orthogonalize(const pdr_orthogonalize_args *p, void *workspace, size_t w
 //        16384x2048x11264 (512, two rounds) 582; in 128 tiles: 15.1, 38.8, 687
 //   parts: 2048x2048x11264 in 256 tiles: one part 214, four 91.9;
 //        512x512x4096 in 64 tiles: one 18.5, four 12.7
+//   a symmetric result's lower tiles alone: 2048x2048x11264 (mc, mc), three
+//        parts, 88, all tiles 133; 2048x2048x2048 32.1, all tiles 31
 namespace pdr {
 namespace dense {
 
 namespace {
 
-double tiles_us(int tile, double workgroups, double steps) {
+double tiles_us(int tile, double workgroups, double steps, double slow) {
   const double slots = tile == 256 ? 256.0 : 512.0;
-  const double fixed = tile == 256 ? 9.0 : tile == 128 ? 5.0 : 3.0;
+  const double fixed = slow + (tile == 256 ? 9.0 : tile == 128 ? 5.0 : 3.0);
   // a round with every slot taken, with half of them, with fewer
   const double full = tile == 256 ? 1.5 : tile == 128 ? 0.9 : 0.43;
   const double half = tile == 256 ? 1.2 : tile == 128 ? 0.57 : 0.28;
@@ -922,14 +968,25 @@ TilePlan plan_tiles(const GemmArgs &g, EpiKind kind) {
     p.tile = bm;
     p.tiles_m = (g.M + bm - 1) / bm;
     p.tiles_n = (g.epi.store_n + bn - 1) / bn;
-    for (p.splits = 1; p.splits <= most; ++p.splits) {
-      double us = tiles_us(bm, batches * p.tiles_m * p.tiles_n * p.splits,
-                           (double)((steps + p.splits - 1) / p.splits));
-      // the parts are written and read once, at 4.6 TB/s
-      if (p.splits > 1) us += 3.0 + 8.0 * sums * p.splits / 4.6e6;
-      if (least == 0.0 || us < least) {
-        least = us;
-        best = p;
+    // rows that do not begin on 16 bytes are stored value by value
+    const double slow = kind == kEpiLinear && !(g.epi.vec && (g.epi.store_n & 7) == 0)
+                            ? bm == 256 ? 40.0 : bm == 128 ? 12.0 : 4.0
+                            : 0.0;
+    for (int lower = 0; lower <= (g.symmetric ? 1 : 0); ++lower) {
+      p.lower = lower != 0;
+      p.tiles = lower ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * p.tiles_n;
+      // storing a tile on both sides
+      const double mirror = lower ? bm == 256 ? 14.0 : bm == 128 ? 4.0 : 2.0 : 0.0;
+      for (p.splits = 1; p.splits <= most; ++p.splits) {
+        double us = tiles_us(bm, batches * p.tiles * p.splits,
+                             (double)((steps + p.splits - 1) / p.splits),
+                             mirror + (p.splits > 1 ? 0.0 : slow));
+        // the parts are written and read once, at 4.6 TB/s
+        if (p.splits > 1) us += 5.0 + 8.0 * sums * p.splits / 4.6e6;
+        if (least == 0.0 || us < least) {
+          least = us;
+          best = p;
+        }
       }
     }
   }

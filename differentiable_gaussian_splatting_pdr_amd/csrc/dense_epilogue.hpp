@@ -393,12 +393,13 @@ __device__ __forceinline__ const char *staged(const char *mine, int r, int c) {
 // The epilogue of `rows` staged rows m0.. and their columns n0..,
 // W columns of a row to a lane at a time.  A gated product's staged columns
 // are 8 gate sums, the 8 up sums of the same columns, and so on.  The next
-// rows are fetched before the present ones are stored.
-template <int KIND, int COLS, int W, int FLAGS>
+// rows are fetched before the present ones are stored.  FLIP: the columns of
+// the FLIP staged rows are the result's rows, and its columns the staged rows.
+template <int KIND, int COLS, int W, int FLAGS, int FLIP>
 __device__ __forceinline__ void finish_rows(const Epi &e, const char *mine, int lane, int batch,
                                             int m0, int rows, int n0, int N) {
   constexpr bool DUAL = KIND == kEpiGated;
-  constexpr int kOut = DUAL ? COLS / 2 : COLS;  // columns of the result
+  constexpr int kOut = DUAL ? COLS / 2 : FLIP ? FLIP : COLS;  // columns of the result
   constexpr int kLanes = kOut / W < 64 ? kOut / W : 64;
   constexpr int kRows = 64 / kLanes, kAtOnce = W == 1 ? 4 : 2;
 #pragma unroll 1
@@ -429,7 +430,10 @@ __device__ __forceinline__ void finish_rows(const Epi &e, const char *mine, int 
 #pragma unroll
         for (int k = 0; k < (DUAL ? 2 : 1); ++k) {
           const int s = DUAL ? (c >> 3) * 16 + (c & 7) + k * 8 : c;
-          if constexpr (W == 1) {
+          if constexpr (FLIP != 0) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[u][i] = *(const float *)staged<COLS>(mine, s + i, r);
+          } else if constexpr (W == 1) {
             v[u][k] = *(const float *)staged<COLS>(mine, r, s);
           } else {
 #pragma unroll
@@ -448,12 +452,12 @@ __device__ __forceinline__ void finish_rows(const Epi &e, const char *mine, int 
   }
 }
 
-template <int KIND, int COLS, int W>
+template <int KIND, int COLS, int W, int FLIP>
 __device__ __forceinline__ void finish_flags(const Epi &e, const char *mine, int lane, int batch,
                                              int m0, int rows, int n0, int N) {
   const int f = epi_flags(KIND, e);
   auto with = [&](auto flags) {
-    finish_rows<KIND, COLS, W, decltype(flags)::value>(e, mine, lane, batch, m0, rows, n0, N);
+    finish_rows<KIND, COLS, W, decltype(flags)::value, FLIP>(e, mine, lane, batch, m0, rows, n0, N);
   };
   if constexpr (KIND == kEpiGatedGrad) {
     (f & kWide) ? with(Flags<kWide>()) : with(Flags<0>());
@@ -476,28 +480,34 @@ __device__ __forceinline__ void finish_flags(const Epi &e, const char *mine, int
   }
 }
 
-template <int KIND, int COLS>
+template <int KIND, int COLS, int FLIP = 0>
 __device__ __forceinline__ void finish_staged(const Epi &e, const char *mine, int lane, int batch,
                                               int m0, int rows, int n0, int N) {
   if (rows <= 0) return;
   if (e.vec)
-    finish_flags<KIND, COLS, 8>(e, mine, lane, batch, m0, rows, n0, N);
+    finish_flags<KIND, COLS, 8, FLIP>(e, mine, lane, batch, m0, rows, n0, N);
   else if constexpr (KIND == kEpiLinear || KIND == kEpiPoly)  // the others write rows of their own
-    finish_flags<KIND, COLS, 1>(e, mine, lane, batch, m0, rows, n0, N);
+    finish_flags<KIND, COLS, 1, FLIP>(e, mine, lane, batch, m0, rows, n0, N);
 }
 
-// The sums themselves, as one part of a contraction that is cut.
-template <int COLS>
+// The sums themselves, as one part of a contraction that is cut: rows m0..
+// and columns n0.. of a part's N columns.  FLIP: as above.
+template <int COLS, int FLIP>
 __device__ __forceinline__ void store_staged(const char *mine, int lane, float *part, int m0,
-                                             int rows, int n0, int M, int N) {
-  (void)M;
-  constexpr int kLanes = COLS / 4, kRows = 64 / kLanes;
+                                             int rows, int n0, int N) {
+  constexpr int kLanes = (FLIP ? FLIP : COLS) / 4, kRows = 64 / kLanes;
   const int c = (lane % kLanes) * 4;
   const int left = N - n0 - c;
   if (left <= 0) return;
 #pragma unroll 2
   for (int r = lane / kLanes; r < rows; r += kRows) {
-    const f32x4 w = *(const f32x4 *)staged<COLS>(mine, r, c);
+    f32x4 w;
+    if constexpr (FLIP != 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = *(const float *)staged<COLS>(mine, c + i, r);
+    } else {
+      w = *(const f32x4 *)staged<COLS>(mine, r, c);
+    }
     float *to = part + (long long)(m0 + r) * N + n0 + c;
     if ((N & 3) == 0) {
       *(f32x4 *)to = w;

@@ -54,6 +54,9 @@ struct GemmArgs {
   long long up_at;                     // dual products: elements from the gate rows to the up rows
   long long batch_a, batch_b;          // elements between the operands of two batches
   int tiles_m, tiles_n, batches;
+  int symmetric;                       // kEpiPoly: C is
+  int lower;                           // then tiles above the diagonal may be left out, and those
+                                       // below it stored on both sides
   int splits;                          // parts that the contraction is cut into
   int steps, steps_more;               // kBK steps of a part; the first steps_more parts take one more
   FastDiv band;                        // by kBand * tiles_n
@@ -259,9 +262,17 @@ struct Reader {
 // operand rows.
 constexpr int kBand = 4;
 __device__ __forceinline__ void pick_tile(const GemmArgs &g, int id, int *tm, int *tn) {
-  const int total = g.tiles_m * g.tiles_n;
+  const int total = g.lower ? g.tiles_m * (g.tiles_m + 1) / 2 : g.tiles_m * g.tiles_n;
   const int xcd = id & 7, at = id >> 3, each = total >> 3, extra = total & 7;
   const int t = xcd * each + (xcd < extra ? xcd : extra) + at;
+  if (g.lower) {  // t = tm (tm + 1) / 2 + tn, tn <= tm
+    int m = (int)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
+    while (m * (m + 1) / 2 > t) --m;
+    while ((m + 1) * (m + 2) / 2 <= t) ++m;
+    *tm = m;
+    *tn = t - m * (m + 1) / 2;
+    return;
+  }
   const int band = (int)fdiv((uint32_t)t, g.band), in = t - band * kBand * g.tiles_n;
   const int rows = g.tiles_m - band * kBand;
   if (rows >= kBand) {
@@ -459,12 +470,20 @@ __global__ __launch_bounds__(256) void k_gemm(GemmArgs g) {
                 acc[hh * kTiles + i][j];
       }
     const int m0 = first + h * kStaged, rows = g.M - m0 < kStaged ? g.M - m0 : kStaged;
-    if (g.splits > 1) {
-      if constexpr (!DUAL)
-        store_staged<WS>(mine, lane, g.partial + ((long long)split * g.batches + batch) * g.M * g.N,
-                         m0, rows, n0, g.M, g.N);
-    } else {
+    float *const part =
+        g.splits > 1 ? g.partial + ((long long)split * g.batches + batch) * g.M * g.N : nullptr;
+    if (!part)
       finish_staged<EPI, WS>(g.epi, mine, lane, batch, m0, rows, n0, g.N);
+    else if constexpr (!DUAL)
+      store_staged<WS, 0>(mine, lane, part, m0, rows, n0, g.N);
+    if constexpr (EPI == kEpiPoly) {
+      if (g.lower && tm != tn) {
+        const int cols = g.N - n0 < WS ? g.N - n0 : WS;
+        if (!part)
+          finish_staged<EPI, WS, kStaged>(g.epi, mine, lane, batch, n0, cols, m0, g.M);
+        else
+          store_staged<WS, kStaged>(mine, lane, part, n0, cols, m0, g.M);
+      }
     }
   }
 #endif

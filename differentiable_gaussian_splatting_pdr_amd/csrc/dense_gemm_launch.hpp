@@ -43,13 +43,14 @@ hipError_t launch_one(GemmArgs g, void *ws, hipStream_t st) {
   g.tiles_m = p.tiles_m;
   g.tiles_n = p.tiles_n;
   g.splits = p.splits;
+  g.lower = p.lower;
   const int steps = (g.K + kBK - 1) / kBK * g.segs;
   g.steps = steps / p.splits;
   g.steps_more = steps % p.splits;
   g.band = make_fastdiv((uint32_t)(kBand * p.tiles_n));
   g.partial = (float *)ws;
   g.epi.vec = g.epi.vec && (g.epi.store_n & 7) == 0;
-  const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)p.splits, (unsigned)g.batches);
+  const dim3 grid((unsigned)p.tiles, (unsigned)p.splits, (unsigned)g.batches);
   if (p.tile == 256)
     hipLaunchKernelGGL((k_gemm<FMT, 256, A_MC, B_MC, EPI>), grid, dim3(256), 0, st, g);
   else if (p.tile == 128)

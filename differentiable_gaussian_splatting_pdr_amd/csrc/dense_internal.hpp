@@ -14,7 +14,8 @@ hipError_t launch_gemm_f16(GemmArgs g, bool a_mc, bool b_mc, EpiKind kind, void 
 size_t gemm_scratch_bytes(const GemmArgs &g, EpiKind kind);
 
 struct TilePlan {
-  int tiles_m, tiles_n, splits;
+  int tiles_m, tiles_n, tiles, splits;  // tiles: of one batch and part
+  bool lower;
   int tile;  // rows and columns: 256, 128 or 64
 };
 TilePlan plan_tiles(const GemmArgs &g, EpiKind kind);
