@@ -315,20 +315,21 @@ class Muon(torch.optim.Optimizer):
 
     buf <- momentum buf + grad;  u = grad + momentum buf (nesterov) or buf;
     p <- p (1 - lr weight_decay) - lr max(1, m / n)^(1/2) orthogonalize(u).
-    The momentum is kept in `state_dtype` (float32 by default); weights of one
-    shape and type are orthogonalised in one batch, in bfloat16 unless they
-    are float32 or float16.
+    The momentum is kept in `state_dtype` (float32 by default).  Weights of one
+    shape and type are orthogonalised in one batch, in `work_dtype` (their own
+    type by default; bfloat16 takes a third of the products of float32).
     """
 
     def __init__(self, params, lr: float = 0.02, momentum: float = 0.95, nesterov: bool = True,
                  weight_decay: float = 0.0, steps: int = 5, coefficients=MUON_COEFFICIENTS,
-                 eps: float = 1e-7, state_dtype: torch.dtype = torch.float32):
+                 eps: float = 1e-7, state_dtype: torch.dtype = torch.float32,
+                 work_dtype: torch.dtype | None = None):
         if lr < 0 or not 0 <= momentum < 1 or weight_decay < 0:
             raise ValueError("lr and weight_decay must be >= 0 and momentum in [0, 1)")
         super().__init__(params, dict(lr=lr, momentum=momentum, nesterov=nesterov,
                                       weight_decay=weight_decay, steps=steps,
                                       coefficients=tuple(coefficients), eps=eps,
-                                      state_dtype=state_dtype))
+                                      state_dtype=state_dtype, work_dtype=work_dtype))
         for group in self.param_groups:
             for p in group["params"]:
                 if p.dim() != 2:
@@ -353,12 +354,13 @@ class Muon(torch.optim.Optimizer):
                 grad = p.grad.to(buf.dtype)
                 buf.mul_(group["momentum"]).add_(grad)
                 u = grad.add(buf, alpha=group["momentum"]) if group["nesterov"] else buf
-                alike.setdefault((p.shape, p.dtype, p.device), []).append((p, u.to(p.dtype)))
+                u = u.to(group["work_dtype"] or p.dtype)
+                alike.setdefault((p.shape, p.dtype, p.device), []).append((p, u))
             for (shape, _, _), pairs in alike.items():
                 scale = max(1.0, shape[0] / max(1, shape[1])) ** 0.5
                 updates = orthogonalize(torch.stack([u for _, u in pairs]), group["steps"],
                                         group["coefficients"], group["eps"])
                 for (p, _), u in zip(pairs, updates):
                     p.mul_(1 - group["lr"] * group["weight_decay"])
-                    p.add_(u, alpha=-group["lr"] * scale)
+                    p.add_(u.to(p.dtype), alpha=-group["lr"] * scale)
         return loss

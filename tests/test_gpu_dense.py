@@ -385,3 +385,27 @@ def test_refusals():
         d.orthogonalize(x, coefficients=(1.0, float("nan"), 0.0))
     with pytest.raises(PdrError):
         d.orthogonalize(x, eps=-1.0)
+
+
+def test_predictor_learns_through_the_splatting_layer():
+    # the example: projections, gated blocks and Muon in front of the renderer
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import fit_predictor
+    losses = fit_predictor.train(steps=30)
+    assert all(v == v for v in losses)
+    assert sum(losses[-5:]) / 5 < 0.7 * losses[0], losses
+
+
+def test_muon_work_dtype():
+    d = dense()
+    p = normal(1, 48, 96).cuda().requires_grad_()
+    q = p.detach().clone().requires_grad_()
+    p.grad = normal(2, 48, 96).cuda()
+    q.grad = p.grad.clone()
+    d.Muon([p], lr=0.1, momentum=0.0, nesterov=False).step()
+    d.Muon([q], lr=0.1, momentum=0.0, nesterov=False, work_dtype=BF).step()
+    u = d.orthogonalize(p.grad.to(BF)).float()
+    assert torch.equal(q, normal(1, 48, 96).cuda().add_(u, alpha=-0.1))
+    assert (p - q).abs().max() < 0.1 * 0.05
