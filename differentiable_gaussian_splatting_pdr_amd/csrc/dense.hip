@@ -930,6 +930,8 @@ int pdr_orthogonalize(const pdr_orthogonalize_args *p, void *workspace, size_t w
 //        (512) 36.8, 8192x1024x2816 (512) 45.7; in 64 tiles: 32.3, 20.6, 59.9, 76.8
 //   256: 8192x1024x512 (128) 24.7, 16384x1024x1024 (256) 37.6,
 //        16384x2048x11264 (512, two rounds) 582; in 128 tiles: 15.1, 38.8, 687
+//   16384x2048x2048 with gelu, its slope and a residual: 194 in 256 tiles, 166
+//        in 128 tiles; with nothing: 132 (114 at its best), 150 (123)
 //   parts: 2048x2048x11264 in 256 tiles: one part 214, four 91.9;
 //        512x512x4096 in 64 tiles: one 18.5, four 12.7
 //   a symmetric result's lower tiles alone: 2048x2048x11264 (mc, mc), three
@@ -968,10 +970,15 @@ TilePlan plan_tiles(const GemmArgs &g, EpiKind kind) {
     p.tile = bm;
     p.tiles_m = (g.M + bm - 1) / bm;
     p.tiles_n = (g.epi.store_n + bn - 1) / bn;
-    // rows that do not begin on 16 bytes are stored value by value
-    const double slow = kind == kEpiLinear && !(g.epi.vec && (g.epi.store_n & 7) == 0)
-                            ? bm == 256 ? 40.0 : bm == 128 ? 12.0 : 4.0
-                            : 0.0;
+    // What an epilogue adds to a round: rows that do not begin on 16 bytes are
+    // stored value by value; activations and a residual take time that only
+    // two workgroups on a compute unit hide behind each other's products.
+    double slow = 0.0;
+    if (kind == kEpiLinear) {
+      if (!(g.epi.vec && (g.epi.store_n & 7) == 0)) slow += bm == 256 ? 40.0 : bm == 128 ? 12.0 : 4.0;
+      const int more = (g.epi.act != PDR_ACT_NONE) + 2 * (g.epi.slope != nullptr) + 2 * (g.epi.res != nullptr);
+      slow += more * (bm == 256 ? 5.0 : bm == 128 ? 1.0 : 0.5);
+    }
     for (int lower = 0; lower <= (g.symmetric ? 1 : 0); ++lower) {
       p.lower = lower != 0;
       p.tiles = lower ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * p.tiles_n;

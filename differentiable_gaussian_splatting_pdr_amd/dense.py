@@ -26,6 +26,9 @@ _ACTS = {"none": _lib.PDR_ACT_NONE, "relu": _lib.PDR_ACT_RELU, "silu": _lib.PDR_
 
 
 def _check(name: str, t, dtype=None, device=None, dim=None):
+    if (dtype is not None and isinstance(t, torch.Tensor) and t.dtype == dtype
+            and t.device == device and dim in (None, t.dim())):
+        return   # like a tensor that has passed
     if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
         raise ValueError("%s must be a tensor on a ROCm device" % name)
     if t.dtype not in _FMT:
@@ -72,14 +75,17 @@ def _call(name: str, args, device):
         with torch.cuda.device(device):
             return _call(name, args, device)
     if name not in _CALLS:
-        _CALLS[name] = (getattr(_lib, name + "_workspace_bytes"), getattr(_lib, name))
+        lib = _lib.lib()
+        _CALLS[name] = (getattr(lib, name + "_workspace_bytes"), getattr(lib, name))
     size_of, run = _CALLS[name]
-    size = size_of(args)
-    if size:
+    rc = size = size_of(args)
+    if size > 0:
         ws = torch.empty(size, dtype=torch.uint8, device=device)
-        run(args, ws.data_ptr(), size, _raw_stream(device.index))
-    else:
-        run(args, None, 0, _raw_stream(device.index))
+        rc = run(args, ws.data_ptr(), size, _raw_stream(device.index))
+    elif size == 0:
+        rc = run(args, None, 0, _raw_stream(device.index))
+    if rc < 0:
+        raise _lib.PdrError(rc, name)
 
 
 def _wants_grad(*tensors) -> bool:
