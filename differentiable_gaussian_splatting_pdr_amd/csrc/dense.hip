@@ -919,21 +919,24 @@ int pdr_orthogonalize(const pdr_orthogonalize_args *p, void *workspace, size_t w
 }  // extern "C"
 
 // How a product is cut into workgroups: 256x256 tiles, one workgroup on a
-// compute unit, 128x128 or 64x64 tiles, two; and the contraction in one part or
-// in several, which a second kernel joins.  The choice is the least of an
-// estimate in microseconds whose constants are fits to measured products
-// (bf16, M x N x K, this card): a step is 64 contraction values of every
-// workgroup in flight.
-//   64:  512x512x512 (64 workgroups) 6.1, 1024x1024x1024 (256) 8.1,
-//        2048x1024x1024 (512) 10.8; in 128 tiles: 8.7, 12.2, 12.7
-//   128: 2048x2048x2048 (256) 22.8, 1024x1024x4096 (64) 33.6, 4096x2048x2048
-//        (512) 36.8, 8192x1024x2816 (512) 45.7; in 64 tiles: 32.3, 20.6, 59.9, 76.8
-//   256: 8192x1024x512 (128) 24.7, 16384x1024x1024 (256) 37.6,
-//        16384x2048x11264 (512, two rounds) 582; in 128 tiles: 15.1, 38.8, 687
+// compute unit; 128x128 or 64x64 tiles, two workgroups, or one whose groups of
+// waves share the contraction; and the contraction in one part or in several,
+// which a second kernel joins.  The choice is the least of an estimate in
+// microseconds whose constants are fits to measured products (bf16, M x N x K,
+// this card): a step is 64 contraction values of every workgroup in flight.
+//   64:  512x512x512 (64 workgroups) 6.2, 1024x1024x1024 (256) 8.3,
+//        2048x1024x1024 (512) 10.9; in 128 tiles: 9.0, 12.7, 12.8
+//   64, four groups: 512x512x4096 (64) 14.3, 1024x1024x4096 (256) 18.7; with
+//        one group 19.0, 20.7
+//   128: 4096x2048x2048 (512) 34.4, 8192x1024x2816 (512) 44.3; in 64 tiles:
+//        60.1, 81.1
+//   128, two groups: 2048x2048x2048 (256) 21.9, 2816x1024x8192 (176) 51.8,
+//        2048x2048x11264 (256) 80.1; with one group 22.9, 63.4, 92.5
+//   256: 8192x1024x512 (128) 25.8, 16384x1024x1024 (256) 38.0,
+//        16384x2048x11264 (512, two rounds) 582; in 128 tiles: 15.3, 37.3, 687
 //   16384x2048x2048 with gelu, its slope and a residual: 194 in 256 tiles, 166
 //        in 128 tiles; with nothing: 132 (114 at its best), 150 (123)
-//   parts: 2048x2048x11264 in 256 tiles: one part 214, four 91.9;
-//        512x512x4096 in 64 tiles: one 18.5, four 12.7
+//   parts: 512x512x4096 in 64 tiles: one 19.0, four 13.1
 //   a symmetric result's lower tiles alone: 2048x2048x11264 (mc, mc), three
 //        parts, 88, all tiles 133; 2048x2048x2048 32.1, all tiles 31
 namespace pdr {
@@ -941,17 +944,25 @@ namespace dense {
 
 namespace {
 
-double tiles_us(int tile, double workgroups, double steps, double slow) {
-  const double slots = tile == 256 ? 256.0 : 512.0;
-  const double fixed = slow + (tile == 256 ? 9.0 : tile == 128 ? 5.0 : 3.0);
-  // a round with every slot taken, with half of them, with fewer
-  const double full = tile == 256 ? 1.5 : tile == 128 ? 0.9 : 0.43;
-  const double half = tile == 256 ? 1.2 : tile == 128 ? 0.57 : 0.28;
-  const double few = tile == 256 ? 1.2 : tile == 128 ? 0.45 : 0.25;
-  const double rounds = floor(workgroups / slots), rest = workgroups - rounds * slots;
-  double us = rounds * (full * steps + fixed);
+struct TileCost {
+  int tile, groups;
+  double slots, fixed;     // workgroups in a round, microseconds of one beside its steps
+  double full, half, few;  // microseconds of a step in a round with every slot taken, half, fewer
+};
+constexpr TileCost kCosts[] = {
+    {64, 1, 512, 3.0, 0.43, 0.28, 0.25}, {64, 4, 256, 4.0, 0.20, 0.20, 0.13},
+    {128, 1, 512, 5.0, 0.90, 0.57, 0.45}, {128, 2, 256, 6.0, 0.42, 0.38, 0.35},
+    {256, 1, 256, 9.0, 1.50, 1.50, 1.20},
+};
+
+double tiles_us(const TileCost &c, double workgroups, double steps, double slow) {
+  const double rounds = floor(workgroups / c.slots), rest = workgroups - rounds * c.slots;
+  const double fixed = c.fixed + slow;
+  double us = rounds * (c.full * steps + fixed);
   if (rest > 0.0)
-    us += (rest > slots / 2 ? full : rest > slots / 4 ? half : few) * steps + fixed;
+    us += (rest > 0.75 * c.slots  ? c.full
+           : rest > 0.375 * c.slots ? c.half
+                                    : c.few) * steps + fixed;
   return us;
 }
 
@@ -964,10 +975,12 @@ TilePlan plan_tiles(const GemmArgs &g, EpiKind kind) {
   const int most = kind == kEpiGated ? 1 : steps / 2 > 32 ? 32 : steps / 2 > 1 ? steps / 2 : 1;
   TilePlan best = {};
   double least = 0.0;
-  for (int bm = 64; bm <= 256; bm *= 2) {
+  for (const TileCost &c : kCosts) {
+    const int bm = c.tile;
     const int bn = kind == kEpiGated ? bm / 2 : bm;
     TilePlan p;
     p.tile = bm;
+    p.groups = c.groups;
     p.tiles_m = (g.M + bm - 1) / bm;
     p.tiles_n = (g.epi.store_n + bn - 1) / bn;
     // What an epilogue adds to a round: rows that do not begin on 16 bytes are
@@ -985,7 +998,7 @@ TilePlan plan_tiles(const GemmArgs &g, EpiKind kind) {
       // storing a tile on both sides
       const double mirror = lower ? bm == 256 ? 14.0 : bm == 128 ? 4.0 : 2.0 : 0.0;
       for (p.splits = 1; p.splits <= most; ++p.splits) {
-        double us = tiles_us(bm, batches * p.tiles * p.splits,
+        double us = tiles_us(c, batches * p.tiles * p.splits,
                              (double)((steps + p.splits - 1) / p.splits),
                              mirror + (p.splits > 1 ? 0.0 : slow));
         // the parts are written and read once, at 4.6 TB/s

@@ -190,6 +190,12 @@ struct Loader {
       ++seg;
     }
   }
+  // No tiles at all.
+  __device__ __forceinline__ void none() {
+    base = (const char *)uniform((uint64_t)segs[0]);
+    bytes = 0;
+    plain = 0;
+  }
   __device__ __forceinline__ void next(int wave, int lane) {
     --more;
     if (--plain > 0) {
@@ -300,24 +306,40 @@ __device__ __forceinline__ void pick_tile(const GemmArgs &g, int id, int *tm, in
 // instruction.  Loads are spread out between the matrix instructions: a load
 // holds the address path for 16 clocks and a wave that meets it busy stops
 // issuing matrix instructions too.
-template <int FMT, int TS, bool A_MC, bool B_MC, int EPI>
-__global__ __launch_bounds__(256) void k_gemm(GemmArgs g) {
+//
+// With GROUPS of 4 waves, each takes a part of the contraction in a ring of its
+// own, and the first adds the others' sums up in order: small results, whose
+// tiles are fewer than the compute units, keep the matrix cores busier so than
+// with the parts in other workgroups and a second kernel to join them.
+template <int FMT, int TS, int GROUPS, bool A_MC, bool B_MC, int EPI>
+__global__ __launch_bounds__(256 * GROUPS) void k_gemm(GemmArgs g) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the body is device builtins throughout
   constexpr int NW = 4, WN = 2, WS = TS / 2, MT = WS / 16, NT = WS / 16;
   constexpr bool DUAL = EPI == kEpiGated;
   using LA = Loader<TS, A_MC, NW, false>;
   using LB = Loader<TS, B_MC, NW, DUAL>;
-  constexpr int kHalf = LA::kBytes, kRing = TS == 64 ? 9 : 5, kAhead = kRing / 2;
-  __shared__ __align__(1024) char smem[kRing * kHalf];
+  constexpr int kHalf = LA::kBytes, kRing = TS == 64 && GROUPS == 1 ? 9 : 5, kAhead = kRing / 2;
+  __shared__ __align__(1024) char all_smem[GROUPS * kRing * kHalf];
 
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int every = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = every & (NW - 1), group = every / NW;
+  char *const smem = all_smem + group * kRing * kHalf;
   const int wm = wave / WN, wn = wave % WN;
   int tm, tn;
   pick_tile(g, blockIdx.x, &tm, &tn);
   const int split = blockIdx.y, batch = blockIdx.z;
   const int row0 = tm * TS, col0 = tn * (DUAL ? TS / 2 : TS);
-  const int tiles = g.steps + (split < g.steps_more ? 1 : 0);
+  // this group's contraction tiles; all groups go through as many turns (and
+  // barriers), those without a tile with zeros
+  int kt = split * g.steps + (split < g.steps_more ? split : g.steps_more);
+  int mine_tiles = g.steps + (split < g.steps_more ? 1 : 0), tiles = mine_tiles;
+  if constexpr (GROUPS > 1) {
+    const int each = tiles / GROUPS, extra = tiles % GROUPS;
+    tiles = each + (extra ? 1 : 0);
+    mine_tiles = each + (group < extra ? 1 : 0);
+    kt += group * each + (group < extra ? group : extra);
+  }
 
   f32x4 acc[MT][NT];
 #pragma unroll
@@ -341,11 +363,10 @@ __global__ __launch_bounds__(256) void k_gemm(GemmArgs g) {
     la.K = lb.K = g.K;
     la.have = g.ka;
     lb.have = g.kb;
-    la.more = lb.more = tiles;
+    la.more = lb.more = mine_tiles;
     la.seg = la.kin = 0;
-    if (split > 0) {
+    if (kt > 0) {
       const int per = (g.K + kBK - 1) / kBK;
-      const int kt = split * g.steps + (split < g.steps_more ? split : g.steps_more);
       la.seg = kt / per;
       la.kin = kt - la.seg * per;
     }
@@ -353,8 +374,13 @@ __global__ __launch_bounds__(256) void k_gemm(GemmArgs g) {
     lb.kin = la.kin;
     la.place_lanes(wave, lane);
     lb.place_lanes(wave, lane);
-    la.seek(wave, lane);
-    lb.seek(wave, lane);
+    if (GROUPS == 1 || mine_tiles > 0) {
+      la.seek(wave, lane);
+      lb.seek(wave, lane);
+    } else {
+      la.none();
+      lb.none();
+    }
     auto load_a = [&](char *s) {
 #pragma unroll
       for (int i = 0; i < LA::kIssues; ++i) la.load(i, s, wave);
@@ -453,6 +479,26 @@ __global__ __launch_bounds__(256) void k_gemm(GemmArgs g) {
   // Sums go through LDS, up to 64 rows of a wave at a time, so that what follows
   // reads and writes whole rows, and its code is small: it runs once, and
   // instructions that run once are paid for in fetches.
+  if constexpr (GROUPS > 1) {
+    // the other groups' sums through LDS, lane by lane
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          *(f32x4 *)(smem + ((wave * MT + i) * NT + j) * 1024 + lane * 16) = acc[i][j];
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll 1
+    for (int o = 1; o < GROUPS; ++o)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          acc[i][j] += *(const f32x4 *)(smem + o * kRing * kHalf + ((wave * MT + i) * NT + j) * 1024 +
+                                        lane * 16);
+  }
   constexpr int kStaged = WS < 64 ? WS : 64, kTiles = kStaged / 16;
   char *const mine = smem + wave * kStaged * (WS * 4);
   const int first = row0 + wm * WS, n0 = col0 + wn * (DUAL ? WS / 2 : WS);

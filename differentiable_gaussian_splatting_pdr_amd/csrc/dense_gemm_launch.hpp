@@ -52,11 +52,15 @@ hipError_t launch_one(GemmArgs g, void *ws, hipStream_t st) {
   g.epi.vec = g.epi.vec && (g.epi.store_n & 7) == 0;
   const dim3 grid((unsigned)p.tiles, (unsigned)p.splits, (unsigned)g.batches);
   if (p.tile == 256)
-    hipLaunchKernelGGL((k_gemm<FMT, 256, A_MC, B_MC, EPI>), grid, dim3(256), 0, st, g);
+    hipLaunchKernelGGL((k_gemm<FMT, 256, 1, A_MC, B_MC, EPI>), grid, dim3(256), 0, st, g);
+  else if (p.tile == 128 && p.groups == 1)
+    hipLaunchKernelGGL((k_gemm<FMT, 128, 1, A_MC, B_MC, EPI>), grid, dim3(256), 0, st, g);
   else if (p.tile == 128)
-    hipLaunchKernelGGL((k_gemm<FMT, 128, A_MC, B_MC, EPI>), grid, dim3(256), 0, st, g);
+    hipLaunchKernelGGL((k_gemm<FMT, 128, 2, A_MC, B_MC, EPI>), grid, dim3(512), 0, st, g);
+  else if (p.groups == 1)
+    hipLaunchKernelGGL((k_gemm<FMT, 64, 1, A_MC, B_MC, EPI>), grid, dim3(256), 0, st, g);
   else
-    hipLaunchKernelGGL((k_gemm<FMT, 64, A_MC, B_MC, EPI>), grid, dim3(256), 0, st, g);
+    hipLaunchKernelGGL((k_gemm<FMT, 64, 4, A_MC, B_MC, EPI>), grid, dim3(1024), 0, st, g);
   if constexpr (EPI != kEpiGated) {
     if (p.splits > 1) {
       const int w = g.epi.vec ? 8 : 1;

@@ -16,7 +16,8 @@ size_t gemm_scratch_bytes(const GemmArgs &g, EpiKind kind);
 struct TilePlan {
   int tiles_m, tiles_n, tiles, splits;  // tiles: of one batch and part
   bool lower;
-  int tile;  // rows and columns: 256, 128 or 64
+  int tile;    // rows and columns: 256, 128 or 64
+  int groups;  // of waves that share a tile's contraction: 1, or 2 (128) or 4 (64)
 };
 TilePlan plan_tiles(const GemmArgs &g, EpiKind kind);
 
