@@ -931,7 +931,8 @@ int pdr_orthogonalize(const pdr_orthogonalize_args *p, void *workspace, size_t w
 //   128: 4096x2048x2048 (512) 34.4, 8192x1024x2816 (512) 44.3; in 64 tiles:
 //        60.1, 81.1
 //   128, two groups: 2048x2048x2048 (256) 21.9, 2816x1024x8192 (176) 51.8,
-//        2048x2048x11264 (256) 80.1; with one group 22.9, 63.4, 92.5
+//        2048x2048x11264 (256) 80.1 (91.0 with both operands mc); with one
+//        group 22.9, 63.4, 92.5 (108.7)
 //   256: 8192x1024x512 (128) 25.8, 16384x1024x1024 (256) 38.0,
 //        16384x2048x11264 (512, two rounds) 582; in 128 tiles: 15.3, 37.3, 687
 //   16384x2048x2048 with gelu, its slope and a residual: 194 in 256 tiles, 166
@@ -947,12 +948,12 @@ namespace {
 struct TileCost {
   int tile, groups;
   double slots, fixed;     // workgroups in a round, microseconds of one beside its steps
-  double full, half, few;  // microseconds of a step in a round with every slot taken, half, fewer
+  double full, half, few;  // microseconds of a step with over 1/2 of the slots taken, over 1/4, fewer
 };
 constexpr TileCost kCosts[] = {
     {64, 1, 512, 3.0, 0.43, 0.28, 0.25}, {64, 4, 256, 4.0, 0.20, 0.20, 0.13},
-    {128, 1, 512, 5.0, 0.90, 0.57, 0.45}, {128, 2, 256, 6.0, 0.42, 0.38, 0.35},
-    {256, 1, 256, 9.0, 1.50, 1.50, 1.20},
+    {128, 1, 512, 5.0, 0.90, 0.57, 0.45}, {128, 2, 256, 6.0, 0.48, 0.42, 0.36},
+    {256, 1, 256, 9.0, 1.50, 1.30, 1.20},
 };
 
 double tiles_us(const TileCost &c, double workgroups, double steps, double slow) {
@@ -960,9 +961,7 @@ double tiles_us(const TileCost &c, double workgroups, double steps, double slow)
   const double fixed = c.fixed + slow;
   double us = rounds * (c.full * steps + fixed);
   if (rest > 0.0)
-    us += (rest > 0.75 * c.slots  ? c.full
-           : rest > 0.375 * c.slots ? c.half
-                                    : c.few) * steps + fixed;
+    us += (rest > c.slots / 2 ? c.full : rest > c.slots / 4 ? c.half : c.few) * steps + fixed;
   return us;
 }
 
