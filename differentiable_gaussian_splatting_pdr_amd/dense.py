@@ -14,6 +14,7 @@ strided; the last dimension is packed (anything else is copied first).
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from .splat import _FMT
@@ -130,6 +131,7 @@ class Linear(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, w, slope = ctx.saved_tensors
         activation, out_dtype, has_bias = ctx.meta
@@ -231,6 +233,7 @@ class GatedMLP(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, w_in, w_out, h, gu = ctx.saved_tensors
         need = ctx.needs_input_grad

@@ -409,3 +409,34 @@ def test_muon_work_dtype():
     u = d.orthogonalize(p.grad.to(BF)).float()
     assert torch.equal(q, normal(1, 48, 96).cuda().add_(u, alpha=-0.1))
     assert (p - q).abs().max() < 0.1 * 0.05
+
+
+def test_offsets_beyond_31_bits():
+    # a result of 2.25e9 values (4.5 GB): its last rows, and the gradients that read it
+    d = dense()
+    M, K, N = 1_100_003, 16, 2048
+    x = torch.randn(M, K, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(BF).requires_grad_()
+    w = leaf(normal(2, N, K, scale=K ** -0.5, dtype=BF))
+    y = d.linear(x, w)
+    at = torch.tensor([0, 1, 524287, 524288, 1048575, 1048576, M - 130, M - 2, M - 1])
+    rows = x.detach()[at.cuda()].cpu()
+    ref.within(y[at.cuda()], ref.linear(rows, w.detach().cpu(), None, None, "none", None, BF)["y"], "y")
+    dy = torch.zeros_like(y)
+    some = normal(3, len(at), N, dtype=BF)
+    dy[at.cuda()] = some.cuda()
+    gx, gw = torch.autograd.grad(y, (x, w), dy)
+    want = ref.linear(rows, w.detach().cpu(), None, None, "none", some, BF)
+    ref.within(gx[at.cuda()], want["dx"], "dx")
+    others = torch.ones(M, dtype=torch.bool, device="cuda")
+    others[at.cuda()] = False
+    assert not gx[others].any()
+    # the sum over a million rows of zeros and nine others
+    ref.within(gw, want["dw"], "dw")
+
+
+def test_twice_differentiated_is_refused():
+    d = dense()
+    x, w = leaf(normal(1, 70, 32)), leaf(normal(2, 16, 32))
+    (g,) = torch.autograd.grad(d.linear(x, w, activation="silu").sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
