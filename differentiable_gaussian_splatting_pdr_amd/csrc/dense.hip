@@ -21,7 +21,9 @@ constexpr int kParts = 1024;  // workgroups of a pass that reduces, at most
 // The passes around the products are bound by memory (4.6 TB/s for a copy on
 // this card): 8 values to a thread in 16-byte accesses where rows allow, a few
 // rows in flight to a thread, and enough workgroups (about a thousand) to
-// cover the latency.
+// cover the latency.  k_dz of 16384 x 2048 bf16 (200 MB) takes 38.5 us, 5.2 TB/s;
+// k_split of 4096 x 1024 fp32 (34 MB) 7.3 us; k_squares and k_normalise of
+// 11264 x 2048 bf16 10 and 26 us.
 
 // The largest of a workgroup's values, in every thread.
 __device__ __forceinline__ float block_max(float v) {
@@ -951,8 +953,8 @@ struct TileCost {
   double full, half, few;  // microseconds of a step with over 1/2 of the slots taken, over 1/4, fewer
 };
 constexpr TileCost kCosts[] = {
-    {64, 1, 512, 3.0, 0.43, 0.28, 0.25}, {64, 4, 256, 4.0, 0.20, 0.20, 0.13},
-    {128, 1, 512, 5.0, 0.90, 0.57, 0.45}, {128, 2, 256, 6.0, 0.48, 0.42, 0.36},
+    {64, 1, 512, 3.0, 0.43, 0.28, 0.25}, {64, 4, 256, 4.0, 0.20, 0.15, 0.13},
+    {128, 1, 512, 5.0, 0.90, 0.57, 0.45}, {128, 2, 256, 7.0, 0.48, 0.42, 0.36},
     {256, 1, 256, 9.0, 1.50, 1.30, 1.20},
 };
 

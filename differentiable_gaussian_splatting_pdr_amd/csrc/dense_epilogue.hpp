@@ -5,8 +5,6 @@
 // Everything here is computed in fp32 and rounded once, when it is stored.
 #pragma once
 
-#include <hip/hip_bf16.h>
-#include <hip/hip_fp16.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
