@@ -6,7 +6,9 @@ accumulation of truncated Gaussian kernels; the backward returns gradients
 for every parameter.  The computation runs in hand-written HIP kernels for
 gfx950 behind the C ABI of ``include/pdr_splat.h``; this package is the
 Python binding (``_lib``: ctypes, same names as the C entry points;
-``splat``: PyTorch tensors, workspace handling, autograd).
+``splat``: PyTorch tensors, workspace handling, autograd).  ``dense`` holds the
+operators of the network in front of the layer and of its optimiser
+(``include/pdr_dense.h``).
 """
 from ._lib import (  # noqa: F401
     LIB_PATH,

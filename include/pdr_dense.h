@@ -17,7 +17,8 @@
  *    scale per tensor; values below 2^-38 of the tensor's largest lose
  *    relative accuracy) and multiplied as hi*hi + hi*lo + lo*hi; an infinity
  *    in an fp32 operand makes the results it reaches not finite, as NaN or as
- *    an infinity.
+ *    an infinity.  (Forward products of at most 64 rows use the fp32 matrix
+ *    instruction instead.)
  *  - Matrices are row-major; ld* is the distance between rows in elements
  *    (>= the row's length, <= 2^22).  Rows that begin on 16 bytes (and, where
  *    a row is summed along, hold a multiple of 8 values) are read in place;
