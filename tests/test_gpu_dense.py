@@ -240,6 +240,19 @@ def test_orthogonalize(shape, dtype):
     assert off <= ortho_bound(shape[-2], shape[-1], 5, dtype), off
 
 
+@pytest.mark.parametrize("dtype", (BF, FP))
+@pytest.mark.parametrize("shape", [(2049, 6001), (6001, 2049), (2, 1288, 2120)])
+def test_orthogonalize_large(shape, dtype):
+    # sizes whose symmetric products are computed by their lower tiles, in one
+    # part and in several; the fp64 form runs on the GPU
+    c = (3.4445, -4.7750, 2.0315)
+    g = torch.randn(*shape, device="cuda", generator=torch.Generator("cuda").manual_seed(sum(shape))).to(dtype)
+    want = ref.orthogonalize(g, 5, c, 1e-7)
+    got = dense().orthogonalize(g).double()
+    off = ((got - want).norm() / want.norm()).item()
+    assert off <= ortho_bound(shape[-2], shape[-1], 5, dtype), off
+
+
 @pytest.mark.parametrize("steps", [0, 1, 2, 7])
 def test_orthogonalize_steps_and_coefficients(steps):
     c = (15 / 8, -10 / 8, 3 / 8)
