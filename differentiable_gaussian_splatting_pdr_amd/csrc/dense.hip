@@ -155,14 +155,16 @@ __global__ __launch_bounds__(kThreads) void k_dz(DzArgs a) {
   constexpr int TY = kThreads / TX, kAtOnce = 4;
   const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
   const int n = (blockIdx.y * TX + tx) * 8;
-  const int m0 = blockIdx.x * a.rows, m1 = m0 + a.rows < a.M ? m0 + a.rows : a.M;
+  // unsigned: the last workgroup's rows may end, and a thread's last step go, past 2^31
+  const uint32_t rows = (uint32_t)a.rows, m0 = blockIdx.x * rows;
+  const uint32_t m1 = m0 + rows < (uint32_t)a.M ? m0 + rows : (uint32_t)a.M;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, best = 0.f;
   if (n < a.N) {
-    for (int m = m0 + ty; m < m1; m += TY * kAtOnce) {
+    for (uint32_t m = m0 + ty; m < m1; m += TY * kAtOnce) {
       float v[kAtOnce][8], s[kAtOnce][8];
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u) {
-        const int r = m + u * TY < m1 ? m + u * TY : m;
+        const uint32_t r = m + u * TY < m1 ? m + u * TY : m;
         load8(a.dy, a.dy_fmt, r * a.lddy + n, a.N - n, a.vec, v[u]);
         if constexpr (SLOPE) load_w<8>(a.slope, a.slope_fmt, r * a.ld_slope + n, s[u]);
       }
