@@ -281,11 +281,14 @@ __global__ __launch_bounds__(kThreads) void k_normalise(NormaliseArgs a) {
 
 bool good_fmt(int f) { return f == kF32 || f == kF16 || f == kBf16; }
 bool good_len(long long n) { return n >= 0 && n <= 0x7fffffffLL - 256; }
+// Passes index a matrix by 8 values in 31 bits.
+bool good_size(long long rows, long long cols) {
+  return rows * ((cols + 7) / 8) <= 0x7fffffffLL - kThreads;
+}
 // A matrix of this many rows and columns: its pointer and row distance.
 bool good_mat(const void *p, long long ld, long long rows, long long cols, int fmt) {
   if (rows == 0 || cols == 0) return true;
-  // passes index a matrix by 8 values in 31 bits
-  if (rows * ((cols + 7) / 8) > 0x7fffffffLL - kThreads) return false;
+  if (!good_size(rows, cols)) return false;
   if (!p || ((uintptr_t)p & (uintptr_t)(fmt_bytes(fmt) - 1))) return false;
   return ld >= cols && ld <= kMaxLd;
 }
@@ -591,6 +594,8 @@ int check_gated(const pdr_gated_mlp *p, bool backward) {
   if (p->activation < PDR_ACT_NONE || p->activation > PDR_ACT_GELU) return PDR_ERR_INVALID_ARG;
   if (!good_len(p->M) || !good_len(p->D) || !good_len(p->F) || !good_len(p->O)) return PDR_ERR_INVALID_ARG;
   if (2 * round8(p->F) > kMaxLd) return PDR_ERR_INVALID_ARG;
+  // h and [dg | du] of fp32 are laid out anew for the products
+  if (p->fmt == kF32 && !good_size(p->M, (backward ? 2 : 1) * round8(p->F))) return PDR_ERR_INVALID_ARG;
   if (!good_mat(p->x, p->ldx, p->M, p->D, p->fmt) ||
       !good_mat(p->w_in, p->ld_in, 2 * p->F, p->D, p->fmt) ||
       !good_mat(p->w_out, p->ld_out, p->O, p->F, p->fmt))

@@ -24,7 +24,9 @@
  *    a row is summed along, hold a multiple of 8 values) are read in place;
  *    others are copied into the workspace first.
  *  - A length may be 0: sums over nothing are 0, and matrices without
- *    elements may be NULL.  Every length is below 2^31.
+ *    elements may be NULL.  Every length is below 2^31 - 256, and a matrix has
+ *    fewer than 2^34 - 2^11 values (rows counted in whole 8s); so do an fp32
+ *    gated block's h and, in its backward, [dg | du].
  *  - Results do not depend on the run: no atomics, one fixed order of sums
  *    for given sizes and alignments.
  *  - The *_workspace_bytes functions read the same struct as the call (sizes,

@@ -193,3 +193,15 @@ except ValueError:
 '''
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
     assert r.returncode == 0 and "refused" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("name,M,F", [("forward", 1 << 21, 1 << 13), ("forward", 3 << 19, 10921), ("backward", 1 << 20, 1 << 13),
+                                      ("backward", 3 << 19, 5461)])
+def test_gated_kept_values_beyond_the_passes_index_are_refused(name, M, F):
+    """fp32 layouts of h and [dg | du] count 8 values in 31 bits; 16-bit ones are read in place."""
+    L = _lib.lib()
+    size = getattr(L, "pdr_gated_mlp_%s_workspace_bytes" % name)
+    sizes = dict(M=M, F=F, D=8, ldx=8, ld_in=8, lddx=8, O=8, ldy=8, lddy=8, ld_out=F)
+    assert size(ctypes.byref(gated(fmt=0, **sizes))) == -1
+    assert size(ctypes.byref(gated(fmt=2, **sizes))) >= 0
+    assert size(ctypes.byref(gated(fmt=0, **{**sizes, "M": M // 2}))) >= 0
