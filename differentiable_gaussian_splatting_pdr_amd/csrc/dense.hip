@@ -22,20 +22,9 @@ constexpr int kParts = 1024;  // workgroups of a pass that reduces, at most
 // this card): 8 values to a thread in 16-byte accesses where rows allow, a few
 // rows in flight to a thread, and enough workgroups (about a thousand) to
 // cover the latency.  k_dz of 16384 x 2048 bf16 (200 MB) takes 38.5 us, 5.2 TB/s;
-// k_split of 4096 x 1024 fp32 (34 MB) 7.3 us; k_squares and k_normalise of
+// k_split of 5120 x 1024 fp32 (52 MB) 11 us; k_squares and k_normalise of
 // 11264 x 2048 bf16 10 and 26 us.
 
-// The largest of a workgroup's values, in every thread.
-__device__ __forceinline__ float block_max(float v) {
-  __shared__ float red[kThreads];
-  red[threadIdx.x] = v;
-  __syncthreads();
-  for (int s = kThreads / 2; s > 0; s >>= 1) {
-    if (threadIdx.x < s) red[threadIdx.x] = fmaxf(red[threadIdx.x], red[threadIdx.x + s]);
-    __syncthreads();
-  }
-  return red[0];
-}
 __device__ __forceinline__ double block_sum(double v) {
   __shared__ double red[kThreads];
   red[threadIdx.x] = v;
@@ -46,9 +35,27 @@ __device__ __forceinline__ double block_sum(double v) {
   }
   return red[0];
 }
-__device__ __forceinline__ float finite_abs(float v) {
-  const float a = fabsf(v);
-  return a < INFINITY ? a : 0.f;
+
+// fp32 values as sums of bf16 values, each the rest's nearest: three hold 24
+// bits, over fp32's own range (a rest below bf16's smallest step, 2^-133, is
+// lost: the last bits of values below 2^-110).
+constexpr int kMaxPlanes = 3;
+__device__ __forceinline__ void store_planes(uint16_t *const *plane, int planes, long long at,
+                                             float v[8]) {
+#pragma unroll
+  for (int k = 0; k < kMaxPlanes; ++k) {
+    if (k >= planes) return;
+    float h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      h[i] = bf16_to_f(f_to_bf16(v[i]));
+      // a finite value that rounds to infinity is cut short; an infinity or a NaN has no rest
+      const bool finite = fabsf(v[i]) < INFINITY;
+      if (finite && fabsf(h[i]) == INFINITY) h[i] = __uint_as_float(__float_as_uint(v[i]) & 0xffff0000u);
+      v[i] = finite ? v[i] - h[i] : 0.f;
+    }
+    store_w<8>(plane[k], kBf16, at, h);
+  }
 }
 
 // Matrices to lay out for the products, several to a launch: workgroups
@@ -58,13 +65,10 @@ struct Prep {
   const void *src;
   long long ld;
   int rows, cols, vec;
-  FastDiv groups;     // by the groups of 8 of a row
-  uint16_t *hi, *lo;  // rows of ldd elements (a multiple of 8), zeros after each row's end
-  int ldd;
-  float *part;        // largest magnitudes of an fp32 matrix, `parts` of them
-  int parts;
-  int *exp;           // the exponent of its scale
-  unsigned first, first_part;
+  FastDiv groups;               // by the groups of 8 of a row
+  uint16_t *plane[kMaxPlanes];  // rows of ldd elements (a multiple of 8), zeros after each row's end
+  int planes, ldd;
+  unsigned first;
 };
 struct PrepBatch {
   Prep item[kMaxPrep];
@@ -88,64 +92,29 @@ __global__ __launch_bounds__(kThreads) void k_repack(PrepBatch b) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (c + i < p.cols) w[i >> 1] |= (uint32_t)src[i] << ((i & 1) * 16);
-  *(uint4 *)(p.hi + (long long)r * p.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  *(uint4 *)(p.plane[0] + (long long)r * p.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Largest finite magnitudes of fp32 matrices, one value per workgroup.
-__global__ __launch_bounds__(kThreads) void k_amax(PrepBatch b) {
-  int i = 0;
-  while (i + 1 < b.count && blockIdx.x >= b.item[i + 1].first_part) ++i;
-  const Prep &p = b.item[i];
-  const uint32_t total = (uint32_t)p.rows * p.groups.d, block = blockIdx.x - p.first_part;
-  float best = 0.f;
-#pragma unroll 4
-  for (uint32_t at = block * kThreads + threadIdx.x; at < total; at += p.parts * kThreads) {
-    const uint32_t r = fdiv(at, p.groups);
-    const int c = (int)(at - r * p.groups.d) * 8;
-    float v[8];
-    load8(p.src, kF32, r * p.ld + c, p.cols - c, p.vec, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) best = fmaxf(best, finite_abs(v[j]));
-  }
-  best = block_max(best);
-  if (threadIdx.x == 0) p.part[block] = best;
-}
-
-// Split fp32 matrices into fp16 planes hi + lo under the scale 2^e that brings
-// a matrix's largest value to [2^14, 2^15); e goes to *exp.
+// Split fp32 matrices into bf16 planes.  One thread per 8 values.
 __global__ __launch_bounds__(kThreads) void k_split(PrepBatch b) {
   const Prep &p = b.item[prep_of(b, blockIdx.x)];
-  const uint32_t block = blockIdx.x - p.first, at = block * kThreads + threadIdx.x;
+  const uint32_t at = (blockIdx.x - p.first) * kThreads + threadIdx.x;
   const uint32_t r = fdiv(at, p.groups);
+  if (r >= (uint32_t)p.rows) return;
   const int c = (int)(at - r * p.groups.d) * 8;
-  const bool mine = r < (uint32_t)p.rows;
   float v[8];
-  if (mine) load8(p.src, kF32, r * p.ld + c, p.cols - c, p.vec, v);
-  float amax = 0.f;
-  for (int i = threadIdx.x; i < p.parts; i += kThreads) amax = fmaxf(amax, p.part[i]);
-  amax = block_max(amax);
-  const int e = amax > 0.f ? 14 - ilogbf(amax) : 0;
-  if (block == 0 && threadIdx.x == 0) *p.exp = e;
-  if (!mine) return;
-  float h[8], l[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float s = ldexpf(v[i], e);
-    h[i] = f16_to_f(f_to_f16(s));
-    l[i] = fabsf(s) < INFINITY ? s - h[i] : 0.f;
-  }
-  store_w<8>(p.hi, kF16, (long long)r * p.ldd + c, h);
-  store_w<8>(p.lo, kF16, (long long)r * p.ldd + c, l);
+  load8(p.src, kF32, r * p.ld + c, p.cols - c, p.vec, v);
+  store_planes(p.plane, p.planes, (long long)r * p.ldd + c, v);
 }
 
-// dz = dy * slope (no slope: dz = dy), rounded to the products' format, and
-// over this workgroup's rows the sums of dz and its largest finite magnitude.
-// A workgroup takes `rows` rows and TX * 8 columns.
+// dz = dy * slope (no slope: dz = dy), rounded to the products' format or in
+// bf16 planes, and the sums of dz over this workgroup's rows.  A workgroup
+// takes `rows` rows and TX * 8 columns.
 struct DzArgs {
   const void *dy, *slope;
-  void *dz;       // null: only the sums
+  uint16_t *plane[kMaxPlanes];
+  int planes;     // 0: only the sums; 1: dz in dz_fmt (16 bits)
   float *colsum;  // [row block][N], or null
-  float *amax;    // [workgroup], or null
   long long lddy, ld_slope, ld_dz;
   int dy_fmt, slope_fmt, dz_fmt;
   int M, N, rows, vec;
@@ -158,7 +127,7 @@ __global__ __launch_bounds__(kThreads) void k_dz(DzArgs a) {
   // unsigned: the last workgroup's rows may end, and a thread's last step go, past 2^31
   const uint32_t rows = (uint32_t)a.rows, m0 = blockIdx.x * rows;
   const uint32_t m1 = m0 + rows < (uint32_t)a.M ? m0 + rows : (uint32_t)a.M;
-  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, best = 0.f;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (n < a.N) {
     for (uint32_t m = m0 + ty; m < m1; m += TY * kAtOnce) {
       float v[kAtOnce][8], s[kAtOnce][8];
@@ -176,15 +145,14 @@ __global__ __launch_bounds__(kThreads) void k_dz(DzArgs a) {
           // past N the slope's rows hold nothing that was written
           if constexpr (SLOPE) v[u][j] = n + j < a.N ? v[u][j] * s[u][j] : 0.f;
           sum[j] += v[u][j];
-          best = fmaxf(best, finite_abs(v[u][j]));
         }
-        if (a.dz) store_w<8>(a.dz, a.dz_fmt, (m + u * TY) * a.ld_dz + n, v[u]);
+        const long long at = (m + u * TY) * a.ld_dz + n;
+        if (a.planes == 1)
+          store_w<8>(a.plane[0], a.dz_fmt, at, v[u]);
+        else if (a.planes)
+          store_planes(a.plane, a.planes, at, v[u]);
       }
     }
-  }
-  if (a.amax) {
-    best = block_max(best);
-    if (threadIdx.x == 0) a.amax[blockIdx.y * gridDim.x + blockIdx.x] = best;
   }
   if (!a.colsum) return;
   __shared__ float red[TY][TX * 8 + 1];
@@ -321,14 +289,16 @@ struct Walk {
   void flush();
 };
 
-// A matrix as the products read it: one 16-bit plane, or two of a split fp32.
+// A matrix as the products read it: 16-bit planes whose sum it is.
 struct Planes {
-  const uint16_t *hi = nullptr, *lo = nullptr;
-  const int *exp = nullptr;
+  const uint16_t *p[kMaxPlanes] = {nullptr, nullptr, nullptr};
+  int count = 1;
   long long ld = 0;
 };
 
-int product_fmt(int fmt) { return fmt == kBf16 ? kBf16 : kF16; }
+// The planes of a matrix of this format, and their format.
+int planes_of(int fmt) { return fmt == kF32 ? 3 : 1; }
+int product_fmt(int fmt) { return fmt == kF16 ? kF16 : kBf16; }
 
 unsigned blocks_for(long long threads) { return (unsigned)((threads + kThreads - 1) / kThreads); }
 unsigned parts_for(long long threads) {
@@ -338,83 +308,75 @@ unsigned parts_for(long long threads) {
 
 void Walk::flush() {
   if (go()) {
-    unsigned blocks = 0, parts = 0;
+    unsigned blocks = 0;
     for (int i = 0; i < repack.count; ++i) {
       Prep &p = repack.item[i];
       p.first = blocks;
       blocks += blocks_for((long long)p.rows * p.groups.d);
     }
     if (blocks) hipLaunchKernelGGL(k_repack, dim3(blocks), dim3(kThreads), 0, st, repack);
-    // the matrices whose largest value is not known yet come first
-    PrepBatch scan = {};
     blocks = 0;
     for (int i = 0; i < split.count; ++i) {
       Prep &p = split.item[i];
       p.first = blocks;
       blocks += blocks_for((long long)p.rows * p.groups.d);
-      if (p.parts) continue;
-      p.parts = (int)parts_for((long long)p.rows * p.groups.d);
-      p.first_part = parts;
-      parts += (unsigned)p.parts;
-      scan.item[scan.count++] = p;
     }
-    if (parts) hipLaunchKernelGGL(k_amax, dim3(parts), dim3(kThreads), 0, st, scan);
     if (blocks) hipLaunchKernelGGL(k_split, dim3(blocks), dim3(kThreads), 0, st, split);
     done(hipGetLastError());
   }
   repack.count = split.count = 0;
 }
 
-// `amax`, if given: `parts` values whose largest is p's largest magnitude.
+// Planes of this many rows and columns in the workspace.
+Planes take_planes(Walk &w, int count, long long rows, long long cols) {
+  Planes r;
+  r.count = count;
+  r.ld = round8(cols);
+  for (int k = 0; k < count; ++k) r.p[k] = (const uint16_t *)w.take((size_t)(rows * r.ld) * 2);
+  return r;
+}
+
 Planes lay_out(Walk &w, const void *p, int fmt, long long ld, long long rows, long long cols,
-               bool summed_along_row, float *amax = nullptr, int parts = 0) {
+               bool summed_along_row) {
   Planes r;
   if (rows == 0 || cols == 0) {
     r.ld = round8(cols > 0 ? cols : 1);
     return r;
   }
   if (fmt != kF32 && aligned16(p) && (ld & 7) == 0 && (!summed_along_row || (cols & 7) == 0)) {
-    r.hi = (const uint16_t *)p;
+    r.p[0] = (const uint16_t *)p;
     r.ld = ld;
     return r;
   }
-  const long long ldd = round8(cols);
+  r = take_planes(w, planes_of(fmt), rows, cols);
   Prep m = {};
   m.src = p;
   m.ld = ld;
   m.rows = (int)rows;
   m.cols = (int)cols;
   m.vec = aligned16(p) && (ld & 7) == 0;
-  m.groups = make_fastdiv((uint32_t)(ldd / 8));
-  m.ldd = (int)ldd;
-  m.hi = (uint16_t *)w.take((size_t)(rows * ldd) * 2);
-  if (fmt == kF32) {
-    m.lo = (uint16_t *)w.take((size_t)(rows * ldd) * 2);
-    m.part = amax ? amax : (float *)w.take(kParts * sizeof(float));
-    m.parts = amax ? parts : 0;
-    m.exp = (int *)w.take(sizeof(int));
-  }
-  r.hi = m.hi;
-  r.lo = m.lo;
-  r.exp = m.exp;
-  r.ld = ldd;
+  m.groups = make_fastdiv((uint32_t)(r.ld / 8));
+  m.ldd = (int)r.ld;
+  m.planes = r.count;
+  for (int k = 0; k < r.count; ++k) m.plane[k] = (uint16_t *)r.p[k];
   w.add(fmt == kF32 ? w.split : w.repack, m);
   return r;
 }
 
 // Add the product of two matrices, offset by so many elements, to the
-// segments: one, or three with split operands.
+// segments: of the planes' products those that matter (with three planes, whose
+// values are 2^-8 of each other's or less: six, down to 2^-16; the others are
+// at most 2^-23 of the product of two values), smallest first.
 void add_product(GemmArgs &g, const Planes &a, long long off_a, const Planes &b, long long off_b) {
-  auto add = [&](const uint16_t *pa, const uint16_t *pb) {
-    g.a[g.segs] = pa ? pa + off_a : nullptr;
-    g.b[g.segs] = pb ? pb + off_b : nullptr;
-    ++g.segs;
-  };
-  add(a.hi, b.hi);
-  if (a.lo && b.lo) {
-    add(a.hi, b.lo);
-    add(a.lo, b.hi);
-  }
+  const int most = a.count > b.count ? a.count : b.count;
+  for (int order = most - 1; order >= 0; --order)
+    for (int i = 0; i <= order; ++i) {
+      const int j = order - i;
+      if (i >= a.count || j >= b.count) continue;
+      g.a[g.segs] = a.p[i] ? a.p[i] + off_a : nullptr;
+      g.b[g.segs] = b.p[j] ? b.p[j] + off_b : nullptr;
+      ++g.segs;
+    }
   g.lda = a.ld;
   g.ldb = b.ld;
 }
@@ -500,42 +462,33 @@ void linear_forward(Walk &w, const pdr_linear &p) {
   GemmArgs g = product(p.M, p.N, round8(p.K));
   add_product(g, x, 0, wt, 0);
   g.epi = e;
-  g.epi.exp_a = x.exp;
-  g.epi.exp_b = wt.exp;
   multiply(w, g, p.fmt, false, false, kEpiLinear);
 }
 
 void linear_backward(Walk &w, const pdr_linear &p) {
   const bool act = p.activation != PDR_ACT_NONE;
   const bool products = p.dx || p.dw;
-  // dz in its own rows unless it is dy itself
-  const void *dz = p.dy;
-  long long ld_dz = p.lddy;
-  const bool write = products && p.M && p.N && (act || p.out_fmt != p.fmt);
-  void *buf = nullptr;
-  if (write) {
-    ld_dz = round8(p.N);
-    dz = buf = w.take((size_t)(p.M * ld_dz) * fmt_bytes(p.fmt));
-  }
+  // dz as the products read it, unless it is dy itself
+  Planes z;
+  const bool write = products && p.M && p.N && (act || p.out_fmt != p.fmt || planes_of(p.fmt) > 1);
+  if (write) z = take_planes(w, planes_of(p.fmt), p.M, p.N);
   // threads across a row's 8s, and rows to a workgroup for about kParts of them
   const int tx = p.N <= 8 ? 1 : p.N <= 64 ? 8 : 32, ty = kThreads / tx;
   const long long col_blocks = (p.N + tx * 8 - 1) / (tx * 8);
   long long rows = (p.M * col_blocks + kParts - 1) / kParts;
   rows = rows < ty ? ty : (rows + ty - 1) / ty * ty;
   const long long row_blocks = p.M ? (p.M + rows - 1) / rows : 0;
-  const bool split = write && p.fmt == kF32;
   float *part = p.dbias ? (float *)w.take((size_t)(row_blocks * p.N) * sizeof(float)) : nullptr;
-  float *amax = split ? (float *)w.take((size_t)(row_blocks * col_blocks) * sizeof(float)) : nullptr;
   if ((write || p.dbias) && p.N && w.go()) {
     DzArgs a = {};
     a.dy = p.dy;
     a.slope = act ? p.slope : nullptr;
-    a.dz = buf;
+    a.planes = write ? z.count : 0;
+    for (int k = 0; k < a.planes; ++k) a.plane[k] = (uint16_t *)z.p[k];
     a.colsum = part;
-    a.amax = amax;
     a.lddy = p.lddy;
     a.ld_slope = round8(p.N);
-    a.ld_dz = ld_dz;
+    a.ld_dz = z.ld;
     a.dy_fmt = p.out_fmt;
     a.slope_fmt = slope_fmt(p.fmt);
     a.dz_fmt = p.fmt;
@@ -564,8 +517,7 @@ void linear_backward(Walk &w, const pdr_linear &p) {
     w.done(hipGetLastError());
   }
   if (!products) return;
-  const Planes z = lay_out(w, dz, p.fmt, ld_dz, p.M, write ? round8(p.N) : p.N, p.dx != nullptr, amax,
-                           (int)(row_blocks * col_blocks));
+  if (!write) z = lay_out(w, p.dy, p.fmt, p.lddy, p.M, p.N, p.dx != nullptr);
   const Planes wt = p.dx ? lay_out(w, p.w, p.fmt, p.ldw, p.N, p.K, false) : Planes();
   const Planes x = p.dw ? lay_out(w, p.x, p.fmt, p.ldx, p.M, p.K, false) : Planes();
   if (p.dx) {
@@ -573,16 +525,12 @@ void linear_backward(Walk &w, const pdr_linear &p) {
     g.kb = (int)p.N;
     add_product(g, z, 0, wt, 0);
     set_out(g.epi, p.dx, p.fmt, p.lddx);
-    g.epi.exp_a = z.exp;
-    g.epi.exp_b = wt.exp;
     multiply(w, g, p.fmt, false, true, kEpiLinear);
   }
   if (p.dw) {
     GemmArgs g = product(p.N, p.K, p.M);
     add_product(g, z, 0, x, 0);
     set_out(g.epi, p.dw, p.fmt, p.lddw);
-    g.epi.exp_a = z.exp;
-    g.epi.exp_b = x.exp;
     multiply(w, g, p.fmt, true, true, kEpiLinear);
   }
 }
@@ -641,8 +589,6 @@ void gated_forward(Walk &w, const pdr_gated_mlp &p) {
     add_product(g, x, 0, wi, 0);
     g.up_at = p.F * wi.ld;
     g.epi = in;
-    g.epi.exp_a = x.exp;
-    g.epi.exp_b = wi.exp;
     multiply(w, g, p.fmt, false, false, kEpiGated);
     w.at = keep;
   }
@@ -650,8 +596,6 @@ void gated_forward(Walk &w, const pdr_gated_mlp &p) {
   GemmArgs g = product(p.M, p.O, Fp);
   add_product(g, h, 0, wo, 0);
   g.epi = out;
-  g.epi.exp_a = h.exp;
-  g.epi.exp_b = wo.exp;
   multiply(w, g, p.fmt, false, false, kEpiLinear);
 }
 
@@ -668,8 +612,6 @@ void gated_backward(Walk &w, const pdr_gated_mlp &p) {
     GemmArgs g = product(p.O, p.F, p.M);
     add_product(g, dy, 0, h, 0);
     set_out(g.epi, p.dw_out, p.fmt, p.ldd_out);
-    g.epi.exp_a = dy.exp;
-    g.epi.exp_b = h.exp;
     multiply(w, g, p.fmt, true, true, kEpiLinear);
     w.at = keep;
   }
@@ -682,8 +624,6 @@ void gated_backward(Walk &w, const pdr_gated_mlp &p) {
     set_out(g.epi, dgu, p.fmt, 2 * Fp);
     g.epi.store_n = (int)Fp;
     g.epi.up_at = (int)Fp;
-    g.epi.exp_a = dy.exp;
-    g.epi.exp_b = wo.exp;
     g.epi.act = p.activation;
     g.epi.gu = (float *)p.gu;
     g.epi.ld_gu = (int)Fp;
@@ -696,8 +636,6 @@ void gated_backward(Walk &w, const pdr_gated_mlp &p) {
     add_product(g, d, 0, wi, 0);
     add_product(g, d, Fp, wi, p.F * wi.ld);
     set_out(g.epi, p.dx, p.fmt, p.lddx);
-    g.epi.exp_a = d.exp;
-    g.epi.exp_b = wi.exp;
     multiply(w, g, p.fmt, false, true, kEpiLinear);
   }
   if (p.dw_in) {
@@ -708,8 +646,6 @@ void gated_backward(Walk &w, const pdr_gated_mlp &p) {
     set_out(g.epi, p.dw_in, p.fmt, p.ldd_in);
     g.epi.batch_y = p.F * p.ldd_in;
     g.epi.vec = g.epi.vec && (g.epi.batch_y * fmt_bytes(p.fmt)) % 16 == 0;
-    g.epi.exp_a = d.exp;
-    g.epi.exp_b = x.exp;
     multiply(w, g, p.fmt, true, true, kEpiLinear);
   }
 }
@@ -778,24 +714,24 @@ void orthogonalize(Walk &w, const pdr_orthogonalize_args &p) {
   }
   auto planes = [&](size_t bytes, long long ld) {
     Planes q;
-    q.hi = (const uint16_t *)w.take(bytes);
-    if (two) q.lo = (const uint16_t *)w.take(bytes);
+    q.count = two ? 2 : 1;
+    for (int k = 0; k < q.count; ++k) q.p[k] = (const uint16_t *)w.take(bytes);
     q.ld = ld;
     return q;
   };
   Planes x[2] = {planes(x_bytes, np), p.steps > 1 ? planes(x_bytes, np) : Planes()};
   const Planes a = planes(a_bytes, sp), b = planes(a_bytes, sp);
-  normalise((void *)x[0].hi, (void *)x[0].lo, kShiftX, kF16, np, p.m * np, np, 1);
+  normalise((void *)x[0].p[0], (void *)x[0].p[1], kShiftX, kF16, np, p.m * np, np, 1);
 
   auto to = [](Epi &e, const Planes &y, long long batch) {
-    set_out(e, (void *)y.hi, kF16, y.ld);
-    e.y_lo = (void *)y.lo;
+    set_out(e, (void *)y.p[0], kF16, y.ld);
+    e.y_lo = (void *)y.p[1];
     e.batch_y = batch;
   };
   auto plus = [](Epi &e, float beta, const Planes &c, long long batch) {
     e.beta = beta;
-    e.c = c.hi;
-    e.c_lo = c.lo;
+    e.c = c.p[0];
+    e.c_lo = c.p[1];
     e.ldc = (int)c.ld;
     e.batch_c = batch;
   };

@@ -34,8 +34,6 @@ struct Epi {
   int act;
   void *slope;  // format slope_fmt, or null
   int slope_fmt, ld_slope;
-  // binary exponents of the scales of fp32 operands split into fp16 planes (null: 0)
-  const int *exp_a, *exp_b;
   // kEpiGated: gate and up sums kept for the gradient, fp32 [rows][2][ld_gu] (null: not kept)
   // kEpiGatedGrad: reads them; y = [dg | du], du at column up_at
   float *gu;
@@ -242,13 +240,12 @@ template <int W, int FLAGS>
 struct Columns<kEpiLinear, W, FLAGS> {
   float bias[W];
   long long at_y;
-  int n, down;
+  int n;
   struct Row {
     float res[W];
   };
   __device__ __forceinline__ Columns(const Epi &e, int batch, int n_, int) : n(n_) {
     at_y = batch * e.batch_y + n;
-    down = e.exp_a ? -(*e.exp_a + *e.exp_b) : 0;
     if (e.bias) {
       load_w<W>(e.bias, e.bias_fmt, n, bias);
     } else {
@@ -260,10 +257,6 @@ struct Columns<kEpiLinear, W, FLAGS> {
     if (flag<FLAGS>(e, kEpiLinear, kReads)) load_w<W>(e.res, y_fmt<FLAGS>(e), place(m, e.ldr) + n, r.res);
   }
   __device__ __forceinline__ void finish(const Epi &e, int m, float v[W], const Row &r) const {
-    if (e.exp_a) {
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = ldexpf(v[i], down);
-    }
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] += bias[i];
     if (flag<FLAGS>(e, kEpiLinear, kKeeps)) {
@@ -283,13 +276,12 @@ struct Columns<kEpiLinear, W, FLAGS> {
 
 template <int W, int FLAGS>
 struct Columns<kEpiGatedGrad, W, FLAGS> {
-  int n, exist, down;
+  int n, exist;
   struct Row {
     float gate[W], up[W];
   };
-  __device__ __forceinline__ Columns(const Epi &e, int, int n_, int N) : n(n_) {
+  __device__ __forceinline__ Columns(const Epi &, int, int n_, int N) : n(n_) {
     exist = N - n;
-    down = e.exp_a ? -(*e.exp_a + *e.exp_b) : 0;
   }
   __device__ __forceinline__ void fetch(const Epi &e, int m, Row &r) const {
     const long long at = place(m, 2 * e.ld_gu) + n;
@@ -301,10 +293,6 @@ struct Columns<kEpiGatedGrad, W, FLAGS> {
 #pragma unroll
     for (int i = 0; i < W; ++i) a[i] = r.gate[i];
     activate<W>(e.act, a, slope);
-    if (e.exp_a) {
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = ldexpf(v[i], down);
-    }
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       // columns past N are stored as zeros whatever w_out's rows hold beyond
@@ -354,17 +342,11 @@ struct Columns<kEpiPoly, W, FLAGS> {
 // v: W gate sums, then the W up sums of the same columns.
 template <int W, int FLAGS>
 struct Columns<kEpiGated, W, FLAGS> {
-  int n, down;
+  int n;
   struct Row {};
-  __device__ __forceinline__ Columns(const Epi &e, int, int n_, int) : n(n_) {
-    down = e.exp_a ? -(*e.exp_a + *e.exp_b) : 0;
-  }
+  __device__ __forceinline__ Columns(const Epi &, int, int n_, int) : n(n_) {}
   __device__ __forceinline__ void fetch(const Epi &, int, Row &) const {}
   __device__ __forceinline__ void finish(const Epi &e, int m, float v[2 * W], const Row &) const {
-    if (e.exp_a) {
-#pragma unroll
-      for (int i = 0; i < 2 * W; ++i) v[i] = ldexpf(v[i], down);
-    }
     if (flag<FLAGS>(e, kEpiGated, kKeeps)) {
       const long long at = place(m, 2 * e.ld_gu) + n;
       store_w<W>(e.gu, kF32, at, v);

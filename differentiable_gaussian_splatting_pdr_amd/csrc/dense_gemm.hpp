@@ -15,8 +15,9 @@
 // blocks on the way to the registers.
 //
 // Segments let one launch sum several products of the same shape: the two
-// halves of a gated block's input gradient, and the three products
-// hi*hi + hi*lo + lo*hi of fp32 operands split into two fp16 planes.
+// halves of a gated block's input gradient, the six products of fp32 operands
+// split into three bf16 planes, and the three of Newton-Schulz iterates in two
+// fp16 planes.
 //
 // What bounds it (this card): at 8192 x 8192 x 8192 bf16 840 / 808 / 802 us for
 // the three layouts, 1309 / 1361 / 1371 TFLOP/s, 52-55% of the nominal peak.
@@ -48,7 +49,7 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) const char lds_char;
 
 constexpr int kBK = 64;  // contraction values per LDS tile (128 bytes of a kc row)
-constexpr int kMaxSegs = 6;
+constexpr int kMaxSegs = 12;  // a gated block's input gradient in fp32
 constexpr long long kMaxLd = 1 << 22;  // 256 rows' byte offsets stay below 2^31
 constexpr uint32_t kOutside = 0x80000000u;  // a byte offset beyond every bound used below
 

@@ -1,4 +1,5 @@
-// dense_gemm_bf16.hip -- the products of bf16 operands.
+// dense_gemm_bf16.hip -- the products of bf16 operands: bf16 tensors and the
+// planes of split fp32 tensors.
 #include "dense_gemm_launch.hpp"
 
 namespace pdr {

@@ -1,5 +1,5 @@
-// dense_gemm_f16.hip -- the products of fp16 operands: fp16 tensors, the
-// planes of split fp32 tensors, and the Newton-Schulz iterates.
+// dense_gemm_f16.hip -- the products of fp16 operands: fp16 tensors and the
+// Newton-Schulz iterates.
 #include "dense_gemm_launch.hpp"
 
 namespace pdr {

@@ -13,11 +13,12 @@
  *
  *  - Operands are PDR_FMT_F32, PDR_FMT_F16 or PDR_FMT_BF16, all of one format
  *    unless said otherwise.  Sums are held in fp32 and rounded once.  fp32
- *    operands are split into two fp16 planes (22 bits under a power-of-two
- *    scale per tensor; values below 2^-38 of the tensor's largest lose
- *    relative accuracy) and multiplied as hi*hi + hi*lo + lo*hi; an infinity
- *    in an fp32 operand makes the results it reaches not finite, as NaN or as
- *    an infinity.  (Forward products of at most 64 rows use the fp32 matrix
+ *    operands are split into three bf16 values each, 24 bits over fp32's own
+ *    range (of values below 2^-110, the bits above 2^-133), and multiplied as
+ *    the six products of those parts that matter: what is left out of a term
+ *    is at most 2^-22 of it, whatever the other terms are.  An infinity in an
+ *    fp32 operand makes the results it reaches not finite, as NaN or as an
+ *    infinity.  (Forward products of at most 64 rows use the fp32 matrix
  *    instruction instead.)
  *  - Matrices are row-major; ld* is the distance between rows in elements
  *    (>= the row's length, <= 2^22).  Rows that begin on 16 bytes (and, where

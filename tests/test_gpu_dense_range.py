@@ -1,0 +1,120 @@
+"""The dense operators on values of a wide range: rows, columns and gradients
+whose magnitudes lie far apart keep the accuracy that each has by itself.
+The tolerances are relative to the magnitudes of a result's own terms."""
+import pytest
+import torch
+
+import dense_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, FP = torch.bfloat16, torch.float16, torch.float32
+NS = (3.4445, -4.7750, 2.0315)
+
+
+def dense():
+    from differentiable_gaussian_splatting_pdr_amd import dense as d
+    return d
+
+
+def normal(seed, *shape, scale=1.0, dtype=FP):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(dtype)
+
+
+def leaf(t):
+    return t.cuda().requires_grad_()
+
+
+def spread(seed, n, low, high):
+    """n powers of ten from low to high, in random order."""
+    at = torch.randperm(n, generator=torch.Generator().manual_seed(seed)).double() / max(n - 1, 1)
+    return (10.0 ** (low + (high - low) * at)).float()
+
+
+def plain_product(a, b, split, ea=None, eb=None):
+    """dense_ref.product for 32-bit operands whose every value keeps 24 bits:
+    three 8-bit parts each, of whose nine products the three smallest (each at
+    most 2^-8 2^-16 of the whole) are left out; sums as in dense_ref."""
+    mag = a.abs() @ b.abs()
+    e = ((a.shape[1] + 8) * 2.0 ** -24 + 2.0 ** -22) * mag
+    if ea is not None:
+        e = e + ea @ (b.abs() + (0 if eb is None else eb))
+    if eb is not None:
+        e = e + a.abs() @ eb
+    return a @ b, e
+
+
+def check_linear(x, w, b, dy, what):
+    want = ref.linear(x, w, b, None, "none", dy, FP)
+    xs, ws, bs = leaf(x), leaf(w), leaf(b)
+    y = dense().linear(xs, ws, bs)
+    y.backward(dy.cuda())
+    for k, t in (("y", y), ("dx", xs.grad), ("dw", ws.grad), ("db", bs.grad)):
+        ref.within(t, want[k], "%s %s" % (k, what))
+
+
+@pytest.mark.parametrize("M,K,N", [(40, 72, 96), (65, 72, 96), (150, 61, 47), (700, 264, 130)])
+def test_linear_fp32_rows_far_apart(M, K, N, monkeypatch):
+    # a token's answer does not depend on how large another one is
+    monkeypatch.setattr(ref, "product", plain_product)
+    x, w, b, dy = normal(1, M, K), normal(2, N, K, scale=K ** -0.5), normal(3, N), normal(4, M, N)
+    rows = spread(5, M, -12, 12)[:, None]
+    check_linear(x * rows, w, b, dy, "rows of x")
+    check_linear(x, w, b, dy * rows, "rows of dy")
+    check_linear(x, w * spread(6, N, -12, 12)[:, None], b, dy, "rows of w")
+
+
+@pytest.mark.parametrize("M,K,N", [(65, 72, 96), (150, 61, 47), (700, 264, 130)])
+def test_linear_fp32_columns_far_apart(M, K, N, monkeypatch):
+    # large features meet small weights, and rows with large features small gradients
+    monkeypatch.setattr(ref, "product", plain_product)
+    x, w, b, dy = normal(1, M, K), normal(2, N, K, scale=K ** -0.5), normal(3, N), normal(4, M, N)
+    k, m, n = spread(5, K, -10, 10), spread(6, M, -10, 10)[:, None], spread(7, N, -10, 10)
+    check_linear(x * k, w / k, b, dy, "features")
+    check_linear(x * m, w, b, dy / m, "rows")
+    check_linear(x, w * n[:, None], b, dy / n, "outputs")
+
+
+@pytest.mark.parametrize("outlier", [1e8, 1e10, 1e12, 1e30])
+def test_linear_fp32_one_large_value(outlier, monkeypatch):
+    monkeypatch.setattr(ref, "product", plain_product)
+    x, w, b, dy = normal(1, 128, 512), normal(2, 64, 512, scale=512 ** -0.5), normal(3, 64), normal(4, 128, 64)
+    x[3, 5] = outlier
+    check_linear(x, w, b, dy, "one value of %g" % outlier)
+
+
+def test_linear_fp32_largest_and_smallest_values(monkeypatch):
+    # the ends of the type's range: the largest value, and values whose own
+    # parts begin to leave it
+    monkeypatch.setattr(ref, "product", plain_product)
+    x, w, b, dy = normal(1, 100, 72), normal(2, 40, 72), torch.zeros(40), torch.zeros(100, 40)
+    x[7, 3] = torch.finfo(FP).max
+    w[:, 3] *= 1e-30
+    x[9] *= 1e-30
+    check_linear(x, w, b, dy, "ends")
+
+
+@pytest.mark.parametrize("dtype", (BF, FP))
+def test_linear_below_the_smallest_normal_value(dtype):
+    # of a value, what lies above bf16's smallest step is kept: 2^-134 of each is lost at most
+    x, w = (normal(1, 100, 72) * 2.0 ** -125).to(dtype), (normal(2, 40, 72) * 2.0 ** 100).to(dtype)
+    X, W = x.double(), w.double()
+    y, e = plain_product(X, W.t(), True)
+    if dtype == FP:
+        e = e + 2.0 ** -134 * W.abs().sum(1)
+    ref.within(dense().linear(x.cuda(), w.cuda(), out_dtype=FP), (y, e + 2.0 ** -24 * y.abs()), "subnormal")
+
+
+@pytest.mark.parametrize("M,D,F,O", [(70, 40, 33, 24), (300, 72, 136, 72)])
+def test_gated_fp32_rows_far_apart(M, D, F, O, monkeypatch):
+    monkeypatch.setattr(ref, "product", plain_product)
+    x, dy = normal(1, M, D) * spread(5, M, 0, 10)[:, None], normal(4, M, O)
+    wi, wo = normal(2, 2 * F, D, scale=D ** -0.5), normal(3, O, F, scale=F ** -0.5)
+    for name, grad in (("x", dy), ("x and dy", dy * spread(6, M, 0, 10)[:, None])):
+        want = ref.gated(x, wi, wo, None, "silu", grad)
+        xs, wis, wos = leaf(x), leaf(wi), leaf(wo)
+        y = dense().gated_mlp(xs, wis, wos)
+        y.backward(grad.cuda())
+        for k, t in (("y", y), ("dx", xs.grad), ("dw_in", wis.grad), ("dw_out", wos.grad)):
+            ref.within(t, want[k], k + ", rows of " + name)
