@@ -36,8 +36,8 @@ __device__ __forceinline__ double block_sum(double v) {
   return red[0];
 }
 
-// fp32 values as sums of bf16 values, each the rest's nearest: three hold 24
-// bits, over fp32's own range (a rest below bf16's smallest step, 2^-133, is
+// Values as sums of bf16 values, each the rest's nearest: two hold fp16's 11
+// bits (and 16 of an fp32 value), three hold 24 bits, over fp32's own range (a rest below bf16's smallest step, 2^-133, is
 // lost: the last bits of values below 2^-110).
 constexpr int kMaxPlanes = 3;
 __device__ __forceinline__ void store_planes(uint16_t *const *plane, int planes, long long at,
@@ -64,7 +64,7 @@ constexpr int kMaxPrep = 6;
 struct Prep {
   const void *src;
   long long ld;
-  int rows, cols, vec;
+  int fmt, rows, cols, vec;
   FastDiv groups;               // by the groups of 8 of a row
   uint16_t *plane[kMaxPlanes];  // rows of ldd elements (a multiple of 8), zeros after each row's end
   int planes, ldd;
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(kThreads) void k_repack(PrepBatch b) {
   *(uint4 *)(p.plane[0] + (long long)r * p.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Split fp32 matrices into bf16 planes.  One thread per 8 values.
+// Split fp32 (or fp16) matrices into bf16 planes.  One thread per 8 values.
 __global__ __launch_bounds__(kThreads) void k_split(PrepBatch b) {
   const Prep &p = b.item[prep_of(b, blockIdx.x)];
   const uint32_t at = (blockIdx.x - p.first) * kThreads + threadIdx.x;
@@ -103,7 +103,7 @@ __global__ __launch_bounds__(kThreads) void k_split(PrepBatch b) {
   if (r >= (uint32_t)p.rows) return;
   const int c = (int)(at - r * p.groups.d) * 8;
   float v[8];
-  load8(p.src, kF32, r * p.ld + c, p.cols - c, p.vec, v);
+  load8(p.src, p.fmt, r * p.ld + c, p.cols - c, p.vec, v);
   store_planes(p.plane, p.planes, (long long)r * p.ldd + c, v);
 }
 
@@ -336,22 +336,25 @@ Planes take_planes(Walk &w, int count, long long rows, long long cols) {
   return r;
 }
 
-Planes lay_out(Walk &w, const void *p, int fmt, long long ld, long long rows, long long cols,
-               bool summed_along_row) {
+// A matrix of format fmt in so many planes: itself, where it can be read in
+// place, or laid out in the workspace.
+Planes lay_out(Walk &w, const void *p, int fmt, int planes, long long ld, long long rows,
+               long long cols, bool summed_along_row) {
   Planes r;
   if (rows == 0 || cols == 0) {
     r.ld = round8(cols > 0 ? cols : 1);
     return r;
   }
-  if (fmt != kF32 && aligned16(p) && (ld & 7) == 0 && (!summed_along_row || (cols & 7) == 0)) {
+  if (planes == 1 && aligned16(p) && (ld & 7) == 0 && (!summed_along_row || (cols & 7) == 0)) {
     r.p[0] = (const uint16_t *)p;
     r.ld = ld;
     return r;
   }
-  r = take_planes(w, planes_of(fmt), rows, cols);
+  r = take_planes(w, planes, rows, cols);
   Prep m = {};
   m.src = p;
   m.ld = ld;
+  m.fmt = fmt;
   m.rows = (int)rows;
   m.cols = (int)cols;
   m.vec = aligned16(p) && (ld & 7) == 0;
@@ -359,7 +362,7 @@ Planes lay_out(Walk &w, const void *p, int fmt, long long ld, long long rows, lo
   m.ldd = (int)r.ld;
   m.planes = r.count;
   for (int k = 0; k < r.count; ++k) m.plane[k] = (uint16_t *)r.p[k];
-  w.add(fmt == kF32 ? w.split : w.repack, m);
+  w.add(planes > 1 ? w.split : w.repack, m);
   return r;
 }
 
@@ -457,8 +460,8 @@ void linear_forward(Walk &w, const pdr_linear &p) {
   e.ld_slope = (int)round8(p.N);
   if (p.M <= kSkinnyRows)
     return multiply_few(w, p.x, p.ldx, p.w, p.ldw, 0, p.M, p.N, p.K, e, p.fmt, false);
-  const Planes x = lay_out(w, p.x, p.fmt, p.ldx, p.M, p.K, true);
-  const Planes wt = lay_out(w, p.w, p.fmt, p.ldw, p.N, p.K, true);
+  const Planes x = lay_out(w, p.x, p.fmt, planes_of(p.fmt), p.ldx, p.M, p.K, true);
+  const Planes wt = lay_out(w, p.w, p.fmt, planes_of(p.fmt), p.ldw, p.N, p.K, true);
   GemmArgs g = product(p.M, p.N, round8(p.K));
   add_product(g, x, 0, wt, 0);
   g.epi = e;
@@ -468,10 +471,17 @@ void linear_forward(Walk &w, const pdr_linear &p) {
 void linear_backward(Walk &w, const pdr_linear &p) {
   const bool act = p.activation != PDR_ACT_NONE;
   const bool products = p.dx || p.dw;
+  // fp32 gradients of an fp16 projection may be anywhere in fp32's range (a mean
+  // loss gives 1 / numel), which fp16 does not hold: dz has two bf16 planes, 16
+  // bits, and so have the other operands, which they hold exactly.  Three
+  // products instead of one; a scale to one dz in fp16 would cost small rows
+  // their bits where another is large.
+  const int planes = p.fmt == kF16 && p.out_fmt == kF32 ? 2 : planes_of(p.fmt);
+  const int in = planes > 1 ? kBf16 : p.fmt;
   // dz as the products read it, unless it is dy itself
   Planes z;
-  const bool write = products && p.M && p.N && (act || p.out_fmt != p.fmt || planes_of(p.fmt) > 1);
-  if (write) z = take_planes(w, planes_of(p.fmt), p.M, p.N);
+  const bool write = products && p.M && p.N && (act || p.out_fmt != p.fmt || planes > 1);
+  if (write) z = take_planes(w, planes, p.M, p.N);
   // threads across a row's 8s, and rows to a workgroup for about kParts of them
   const int tx = p.N <= 8 ? 1 : p.N <= 64 ? 8 : 32, ty = kThreads / tx;
   const long long col_blocks = (p.N + tx * 8 - 1) / (tx * 8);
@@ -491,7 +501,7 @@ void linear_backward(Walk &w, const pdr_linear &p) {
     a.ld_dz = z.ld;
     a.dy_fmt = p.out_fmt;
     a.slope_fmt = slope_fmt(p.fmt);
-    a.dz_fmt = p.fmt;
+    a.dz_fmt = in;
     a.M = (int)p.M;
     a.N = (int)p.N;
     a.rows = (int)rows;
@@ -517,21 +527,21 @@ void linear_backward(Walk &w, const pdr_linear &p) {
     w.done(hipGetLastError());
   }
   if (!products) return;
-  if (!write) z = lay_out(w, p.dy, p.fmt, p.lddy, p.M, p.N, p.dx != nullptr);
-  const Planes wt = p.dx ? lay_out(w, p.w, p.fmt, p.ldw, p.N, p.K, false) : Planes();
-  const Planes x = p.dw ? lay_out(w, p.x, p.fmt, p.ldx, p.M, p.K, false) : Planes();
+  if (!write) z = lay_out(w, p.dy, p.fmt, planes, p.lddy, p.M, p.N, p.dx != nullptr);
+  const Planes wt = p.dx ? lay_out(w, p.w, p.fmt, planes, p.ldw, p.N, p.K, false) : Planes();
+  const Planes x = p.dw ? lay_out(w, p.x, p.fmt, planes, p.ldx, p.M, p.K, false) : Planes();
   if (p.dx) {
     GemmArgs g = product(p.M, p.K, round8(p.N));
     g.kb = (int)p.N;
     add_product(g, z, 0, wt, 0);
     set_out(g.epi, p.dx, p.fmt, p.lddx);
-    multiply(w, g, p.fmt, false, true, kEpiLinear);
+    multiply(w, g, in, false, true, kEpiLinear);
   }
   if (p.dw) {
     GemmArgs g = product(p.N, p.K, p.M);
     add_product(g, z, 0, x, 0);
     set_out(g.epi, p.dw, p.fmt, p.lddw);
-    multiply(w, g, p.fmt, true, true, kEpiLinear);
+    multiply(w, g, in, true, true, kEpiLinear);
   }
 }
 
@@ -580,11 +590,11 @@ void gated_forward(Walk &w, const pdr_gated_mlp &p) {
     multiply_few(w, p.x, p.ldx, p.w_in, p.ld_in, p.F * p.ld_in, p.M, p.F, p.D, in, p.fmt, true);
     return multiply_few(w, p.h, Fp, p.w_out, p.ld_out, 0, p.M, p.O, p.F, out, p.fmt, false);
   }
-  const Planes wo = lay_out(w, p.w_out, p.fmt, p.ld_out, p.O, p.F, true);
+  const Planes wo = lay_out(w, p.w_out, p.fmt, planes_of(p.fmt), p.ld_out, p.O, p.F, true);
   {
     const size_t keep = w.at;
-    const Planes x = lay_out(w, p.x, p.fmt, p.ldx, p.M, p.D, true);
-    const Planes wi = lay_out(w, p.w_in, p.fmt, p.ld_in, 2 * p.F, p.D, true);
+    const Planes x = lay_out(w, p.x, p.fmt, planes_of(p.fmt), p.ldx, p.M, p.D, true);
+    const Planes wi = lay_out(w, p.w_in, p.fmt, planes_of(p.fmt), p.ld_in, 2 * p.F, p.D, true);
     GemmArgs g = product(p.M, p.F, round8(p.D));
     add_product(g, x, 0, wi, 0);
     g.up_at = p.F * wi.ld;
@@ -592,7 +602,7 @@ void gated_forward(Walk &w, const pdr_gated_mlp &p) {
     multiply(w, g, p.fmt, false, false, kEpiGated);
     w.at = keep;
   }
-  const Planes h = lay_out(w, p.h, p.fmt, Fp, p.M, Fp, true);
+  const Planes h = lay_out(w, p.h, p.fmt, planes_of(p.fmt), Fp, p.M, Fp, true);
   GemmArgs g = product(p.M, p.O, Fp);
   add_product(g, h, 0, wo, 0);
   g.epi = out;
@@ -602,13 +612,13 @@ void gated_forward(Walk &w, const pdr_gated_mlp &p) {
 void gated_backward(Walk &w, const pdr_gated_mlp &p) {
   const long long Fp = round8(p.F);
   const bool through = p.dx || p.dw_in;
-  const Planes dy = lay_out(w, p.dy, p.fmt, p.lddy, p.M, p.O, through);
-  const Planes x = p.dw_in ? lay_out(w, p.x, p.fmt, p.ldx, p.M, p.D, false) : Planes();
-  const Planes wi = p.dx ? lay_out(w, p.w_in, p.fmt, p.ld_in, 2 * p.F, p.D, false) : Planes();
-  const Planes wo = through ? lay_out(w, p.w_out, p.fmt, p.ld_out, p.O, p.F, false) : Planes();
+  const Planes dy = lay_out(w, p.dy, p.fmt, planes_of(p.fmt), p.lddy, p.M, p.O, through);
+  const Planes x = p.dw_in ? lay_out(w, p.x, p.fmt, planes_of(p.fmt), p.ldx, p.M, p.D, false) : Planes();
+  const Planes wi = p.dx ? lay_out(w, p.w_in, p.fmt, planes_of(p.fmt), p.ld_in, 2 * p.F, p.D, false) : Planes();
+  const Planes wo = through ? lay_out(w, p.w_out, p.fmt, planes_of(p.fmt), p.ld_out, p.O, p.F, false) : Planes();
   if (p.dw_out) {
     const size_t keep = w.at;
-    const Planes h = lay_out(w, p.h, p.fmt, Fp, p.M, Fp, false);
+    const Planes h = lay_out(w, p.h, p.fmt, planes_of(p.fmt), Fp, p.M, Fp, false);
     GemmArgs g = product(p.O, p.F, p.M);
     add_product(g, dy, 0, h, 0);
     set_out(g.epi, p.dw_out, p.fmt, p.ldd_out);
@@ -629,7 +639,7 @@ void gated_backward(Walk &w, const pdr_gated_mlp &p) {
     g.epi.ld_gu = (int)Fp;
     multiply(w, g, p.fmt, false, true, kEpiGatedGrad);
   }
-  const Planes d = lay_out(w, dgu, p.fmt, 2 * Fp, p.M, 2 * Fp, true);
+  const Planes d = lay_out(w, dgu, p.fmt, planes_of(p.fmt), 2 * Fp, p.M, 2 * Fp, true);
   if (p.dx) {
     GemmArgs g = product(p.M, p.D, Fp);
     g.kb = (int)p.F;

@@ -79,8 +79,10 @@ typedef struct {
 long long pdr_linear_forward_workspace_bytes(const pdr_linear *p);
 int pdr_linear_forward(const pdr_linear *p, void *workspace, size_t workspace_bytes, void *stream);
 
-/* dz = dy act'(z) (rounded to fmt where it enters the products), dx = dz w,
- * dw = dz^T x, dbias = sum of dz over rows.  The residual's gradient is dy. */
+/* dz = dy act'(z), dx = dz w, dw = dz^T x, dbias = sum of dz over rows.  The
+ * residual's gradient is dy.  Where dz enters the products it is rounded to
+ * fmt, like dy itself, which has that format; with 16-bit operands and an fp32
+ * dy, to bf16 for bf16, and for fp16 to 16 bits over fp32's range. */
 long long pdr_linear_backward_workspace_bytes(const pdr_linear *p);
 int pdr_linear_backward(const pdr_linear *p, void *workspace, size_t workspace_bytes,
                         void *stream);
@@ -112,7 +114,9 @@ long long pdr_gated_mlp_forward_workspace_bytes(const pdr_gated_mlp *p);
 int pdr_gated_mlp_forward(const pdr_gated_mlp *p, void *workspace, size_t workspace_bytes,
                           void *stream);
 /* dh = dy w_out, dg = dh u act'(g), du = dh act(g), dx = [dg | du] w_in,
- * dw_in = [dg | du]^T x, dw_out = dy^T h.  dg and du are rounded to fmt. */
+ * dw_in = [dg | du]^T x, dw_out = dy^T h.  dg and du are rounded to fmt, and
+ * so is h: in fp16 a product of gate and up values beyond 65504 is an infinity,
+ * and gradients are as coarse as fp16's step of 2^-24, as dy's are. */
 long long pdr_gated_mlp_backward_workspace_bytes(const pdr_gated_mlp *p);
 int pdr_gated_mlp_backward(const pdr_gated_mlp *p, void *workspace, size_t workspace_bytes,
                            void *stream);

@@ -118,3 +118,38 @@ def test_gated_fp32_rows_far_apart(M, D, F, O, monkeypatch):
         y.backward(grad.cuda())
         for k, t in (("y", y), ("dx", xs.grad), ("dw_in", wis.grad), ("dw_out", wos.grad)):
             ref.within(t, want[k], k + ", rows of " + name)
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("power", [-19, -24, -27, 20])
+@pytest.mark.parametrize("M,K,N", [(3000, 96, 8), (777, 61, 47)])
+def test_linear_fp16_with_a_32_bit_gradient(M, K, N, power, act):
+    # a mean loss gives the 32-bit result gradients of 1 / numel: they scale
+    # like the exact ones do, down and up.  The gradients of dy times 2^power
+    # are those of dy times 2^power; the bounds are those of dy, with the
+    # result's own rounding at its own magnitude.
+    small = 2.0 ** -14 if power > 0 else 1.0
+    x = normal(1, M, K, scale=small, dtype=HF)
+    w = normal(2, N, K, scale=small * K ** -0.5, dtype=HF)
+    dy = normal(3, M, N)
+    want = ref.linear(x, w, None, None, act, dy, FP)
+    xs, ws = leaf(x), leaf(w)
+    dense().linear(xs, ws, activation=act, out_dtype=FP).backward((dy * 2.0 ** power).cuda())
+    for k, t in (("dx", xs.grad), ("dw", ws.grad)):
+        value, bound = (v * 2.0 ** power for v in want[k])
+        ref.within(t, (value, bound + ref.STEP[HF]), "%s 2^%d" % (k, power))
+
+
+def test_linear_fp16_rows_of_a_32_bit_gradient_far_apart():
+    x, w, dy = normal(1, 500, 64, dtype=HF), normal(2, 24, 64, scale=0.125, dtype=HF), normal(3, 500, 24)
+    dy = dy * (2.0 ** (torch.arange(500) % 25 - 12).float())[:, None]
+    want = ref.linear(x, w, None, None, "none", dy, FP)
+    xs, ws = leaf(x), leaf(w)
+    dense().linear(xs, ws, out_dtype=FP).backward(dy.cuda())
+    ref.within(xs.grad, want["dx"], "dx")
+    # three sums lie beyond fp16's largest value
+    value, bound = want["dw"]
+    past = value.abs() > 65520
+    got = ws.grad.cpu()
+    assert past.sum() == 3 and torch.equal(got[past].double(), value[past].sign() * float("inf"))
+    ref.within(torch.where(past, torch.zeros_like(got), got), (torch.where(past, torch.zeros_like(value), value), bound), "dw")
