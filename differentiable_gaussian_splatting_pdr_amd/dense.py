@@ -14,6 +14,7 @@ strided; the last dimension is packed (anything else is copied first).
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _lib
@@ -89,8 +90,15 @@ def _call(name: str, args, device):
         raise _lib.PdrError(rc, name)
 
 
-def _wants_grad(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+def _has_tangent(t) -> bool:
+    return forward_ad.unpack_dual(t).tangent is not None
+
+
+def _differentiated(*tensors) -> bool:
+    """Whether autograd has to see the call: for a gradient, or to refuse a tangent
+    (forward mode), which would otherwise be lost."""
+    grad = torch.is_grad_enabled()
+    return any(t is not None and (grad and t.requires_grad or _has_tangent(t)) for t in tensors)
 
 
 # ------------------------------------------------------------------- linear
@@ -185,7 +193,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
             raise ValueError("residual must be %s" % (shape,))
         residual = _rows(residual)
     args = (_rows(x), _rows(weight), bias, residual, _activation(activation), out_dtype)
-    if _wants_grad(x, weight, bias, residual):
+    if _differentiated(x, weight, bias, residual):
         y = Linear.apply(*args)
     else:
         y, _ = _linear_forward(*args, False)
@@ -278,7 +286,7 @@ def gated_mlp(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor,
             raise ValueError("residual must be %s" % (shape,))
         residual = _rows(residual)
     args = (_rows(x), _rows(w_in), _rows(w_out), residual, _activation(activation))
-    if _wants_grad(x, w_in, w_out, residual):
+    if _differentiated(x, w_in, w_out, residual):
         y = GatedMLP.apply(*args)
     else:
         y = _gated_forward(*args, False)[0]
@@ -294,8 +302,12 @@ MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=MUON_COEFFICIENTS,
                   eps: float = 1e-7) -> torch.Tensor:
     """Bring the singular values of g [..., m, n] near one, by `steps` of
-    X <- a X + (b A + c A^2) X with A = X X^T, from X = g / (|g|_F + eps)."""
+    X <- a X + (b A + c A^2) X with A = X X^T, from X = g / (|g|_F + eps).
+
+    A step of an optimiser: the result is no function of g to autograd."""
     _check("g", g)
+    if _has_tangent(g):
+        raise NotImplementedError("orthogonalize has no forward-mode derivative")
     if g.dim() < 2:
         raise ValueError("g must be [..., m, n]")
     if int(steps) != steps or steps < 0:

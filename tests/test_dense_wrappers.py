@@ -1,0 +1,38 @@
+"""The dense operators' Python side without a GPU: what it passes on, copies
+and refuses, with the launches left out."""
+import pytest
+import torch
+from torch.autograd import forward_ad
+
+from differentiable_gaussian_splatting_pdr_amd import dense
+
+
+@pytest.fixture
+def no_launch(monkeypatch):
+    """Operators on CPU tensors that launch nothing; the names of the calls they would make."""
+    calls = []
+    monkeypatch.setattr(dense, "_check", lambda *a: None)
+    monkeypatch.setattr(dense, "_call", lambda name, *a: calls.append(name))
+    return calls
+
+
+def operators(x, w_in, w_out, g):
+    return ((lambda v: dense.linear(v, w_in), x), (lambda v: dense.linear(x, v, activation="gelu"), w_in),
+            (lambda v: dense.linear(x, w_in, residual=v), torch.zeros(5, 12)),
+            (lambda v: dense.linear(x, w_in, bias=v), torch.zeros(12)),
+            (lambda v: dense.gated_mlp(v, w_in, w_out), x), (lambda v: dense.gated_mlp(x, v, w_out), w_in),
+            (lambda v: dense.gated_mlp(x, w_in, w_out, residual=v), torch.zeros(5, 8)), (dense.orthogonalize, g))
+
+
+def test_forward_mode_is_refused(no_launch):
+    # no tangent may be lost without a word
+    for f, at in operators(torch.ones(5, 8), torch.ones(12, 8), torch.ones(8, 6), torch.ones(4, 6)):
+        for no_grad in (False, True):
+            with forward_ad.dual_level(), torch.set_grad_enabled(not no_grad):
+                with pytest.raises(NotImplementedError):
+                    f(forward_ad.make_dual(at, torch.ones_like(at)))
+                f(at)   # nothing is differentiated
+        with pytest.raises(RuntimeError):
+            torch.func.jvp(f, (at,), (torch.ones_like(at),))
+        with pytest.raises(RuntimeError):
+            torch.vmap(f)(torch.stack((at, at)))
