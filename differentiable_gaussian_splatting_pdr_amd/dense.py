@@ -49,11 +49,15 @@ def _activation(name: str) -> int:
     return _ACTS[name]
 
 
+_MAX_LD = 1 << 22   # the kernels' largest distance between rows
+
+
 def _rows(t: torch.Tensor) -> torch.Tensor:
     """t as [rows, columns] with packed columns; a view where its strides allow."""
     if t.dim() != 2:
         t = t.reshape(-1, t.shape[-1]) if t.numel() else t.new_empty((t.shape[:-1].numel(), t.shape[-1]))
-    if t.numel() and (t.stride(1) != 1 and t.shape[1] > 1 or t.stride(0) < t.shape[1]):
+    if t.numel() and (t.stride(1) != 1 and t.shape[1] > 1
+                      or not t.shape[1] <= t.stride(0) <= _MAX_LD):
         t = t.contiguous()
     return t
 
@@ -316,7 +320,8 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=MUON_COEFFICIENT
         raise ValueError("coefficients must be (a, b, c)")
     m, n = g.shape[-2:]
     flat = g if g.dim() == 2 else g.reshape((g.shape[:-2].numel(), m, n))
-    if g.numel() and (flat.stride(-1) != 1 and n > 1 or m > 1 and flat.stride(-2) < n):
+    if g.numel() and (flat.stride(-1) != 1 and n > 1
+                      or m > 1 and not n <= flat.stride(-2) <= _MAX_LD):
         flat = flat.contiguous()
     out = torch.empty(g.shape, dtype=g.dtype, device=g.device)
     a = _lib.pdr_orthogonalize_args()

@@ -36,3 +36,19 @@ def test_forward_mode_is_refused(no_launch):
             torch.func.jvp(f, (at,), (torch.ones_like(at),))
         with pytest.raises(RuntimeError):
             torch.vmap(f)(torch.stack((at, at)))
+
+
+@pytest.mark.parametrize("apart", [(1 << 22) - 1, 1 << 22, (1 << 22) + 1, 3 << 22])
+def test_rows_further_apart_than_the_kernels_take_are_copied(apart, monkeypatch):
+    v = torch.arange(2 * apart, dtype=torch.float16).view(2, apart)[:, 5:15]
+    rows = dense._rows(v)
+    assert torch.equal(rows, v) and dense._ld(rows) == (10 if apart > 1 << 22 else apart)
+    # the last token of each sequence
+    last = torch.zeros(2, 3, apart // 3 + 1, dtype=torch.float16)[:, -1, :8]
+    assert dense._ld(dense._rows(last)) == (8 if 3 * (apart // 3 + 1) > 1 << 22 else 3 * (apart // 3 + 1))
+    seen = []
+    monkeypatch.setattr(dense, "_check", lambda *a: None)
+    monkeypatch.setattr(dense, "_call", lambda name, args, device: seen.append((args.ldg, args.batch_g)))
+    dense.orthogonalize(v)
+    dense.orthogonalize(torch.stack((v, v))[:1])
+    assert seen == [(10 if apart > 1 << 22 else apart, 0), (10, 20)]

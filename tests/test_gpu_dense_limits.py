@@ -23,3 +23,25 @@ def test_bias_gradient_of_as_many_rows_as_there_may_be(M):
     assert _lib.lib().pdr_linear_backward(ctypes.byref(a), ws.data_ptr(), size,
                                           torch.cuda.current_stream().cuda_stream) == 0
     assert db.item() == 302   # a value of bf16
+
+
+def test_rows_far_apart():
+    # rows 2^22 + 64 values apart: a narrow view of a wide tensor
+    from differentiable_gaussian_splatting_pdr_amd import dense
+    wide = torch.zeros(5, (1 << 22) + 64, dtype=torch.bfloat16, device="cuda")
+    near = torch.randn(5, 40, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(torch.bfloat16)
+    wide[:, 8:48] = near
+    x = wide[:, 8:48]
+    w = near[:3].contiguous()
+    assert torch.equal(dense.linear(x, w), dense.linear(near, w))
+    assert torch.equal(dense.linear(near, x), dense.linear(near, near))
+    assert torch.equal(dense.linear(near, near[:, :40], residual=x[:, :5]),
+                       dense.linear(near, near[:, :40], residual=near[:, :5]))
+    y = dense.gated_mlp(x, near[:4], near[:, :2].contiguous())
+    assert torch.equal(y, dense.gated_mlp(near, near[:4], near[:, :2].contiguous()))
+    assert torch.equal(dense.orthogonalize(x), dense.orthogonalize(near))
+    # a gradient with such rows
+    v = near.clone().requires_grad_()
+    (want,) = torch.autograd.grad(dense.linear(v, near.repeat(8, 1)), v, near)
+    (got,) = torch.autograd.grad(dense.linear(v, near.repeat(8, 1)), v, x)
+    assert torch.equal(got, want)
