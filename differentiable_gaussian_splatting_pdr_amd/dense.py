@@ -55,7 +55,7 @@ _MAX_LD = 1 << 22   # the kernels' largest distance between rows
 def _rows(t: torch.Tensor) -> torch.Tensor:
     """t as [rows, columns] with packed columns; a view where its strides allow."""
     if t.dim() != 2:
-        t = t.reshape(-1, t.shape[-1]) if t.numel() else t.new_empty((t.shape[:-1].numel(), t.shape[-1]))
+        t = t.reshape(t.shape[:-1].numel(), t.shape[-1])
     if t.numel() and (t.stride(1) != 1 and t.shape[1] > 1
                       or not t.shape[1] <= t.stride(0) <= _MAX_LD):
         t = t.contiguous()

@@ -52,3 +52,15 @@ def test_rows_further_apart_than_the_kernels_take_are_copied(apart, monkeypatch)
     dense.orthogonalize(v)
     dense.orthogonalize(torch.stack((v, v))[:1])
     assert seen == [(10 if apart > 1 << 22 else apart, 0), (10, 20)]
+
+
+@pytest.mark.parametrize("shape", [(2, 0, 8), (0, 3, 8), (2, 3, 0), (0,)])
+def test_inputs_without_elements_keep_their_gradient(no_launch, shape):
+    x, n = torch.zeros(*shape, requires_grad=True), shape[-1]
+    for y in (dense.linear(x, torch.ones(4, n)), dense.gated_mlp(x, torch.ones(6, n), torch.ones(4, 3))):
+        assert y.shape == (*shape[:-1], 4) and y.requires_grad
+        (g,) = torch.autograd.grad(y.sum(), x)
+        assert g.shape == x.shape
+    r = torch.zeros(*shape[:-1], 4, requires_grad=True)
+    y = dense.linear(x.detach(), torch.ones(4, n), residual=r)
+    assert y.requires_grad and torch.autograd.grad(y.sum(), r)[0].shape == r.shape
