@@ -362,6 +362,26 @@ class Muon(torch.optim.Optimizer):
                     raise ValueError("Muon updates weights of two dimensions, got %s"
                                      % (tuple(p.shape),))
 
+    def load_state_dict(self, state_dict):
+        """As torch.optim.Optimizer's, but the momentum is taken in `state_dtype`:
+        the base class rounds it to the weight's type."""
+        taken = []
+        before = self.register_load_state_dict_pre_hook(lambda _, given: taken.append(given))
+        after = self.register_load_state_dict_post_hook(lambda _: self._take_momentum(taken[0]),
+                                                        prepend=True)
+        try:
+            super().load_state_dict(state_dict)
+        finally:
+            before.remove()
+            after.remove()
+
+    def _take_momentum(self, given):
+        for group, saved in zip(self.param_groups, given["param_groups"]):
+            for p, key in zip(group["params"], saved["params"]):
+                if "momentum" in given["state"].get(key, ()):
+                    self.state[p]["momentum"] = given["state"][key]["momentum"].to(
+                        device=p.device, dtype=group["state_dtype"], copy=True)
+
     @torch.no_grad()
     def step(self, closure=None):
         loss = None
