@@ -302,6 +302,13 @@ def gated_mlp(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor,
 MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
 
+def _check_steps(steps, coefficients):
+    if int(steps) != steps or steps < 0:
+        raise ValueError("steps must be a whole number >= 0")
+    if len(coefficients) != 3:
+        raise ValueError("coefficients must be (a, b, c)")
+
+
 @torch.no_grad()
 def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=MUON_COEFFICIENTS,
                   eps: float = 1e-7) -> torch.Tensor:
@@ -314,10 +321,7 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=MUON_COEFFICIENT
         raise NotImplementedError("orthogonalize has no forward-mode derivative")
     if g.dim() < 2:
         raise ValueError("g must be [..., m, n]")
-    if int(steps) != steps or steps < 0:
-        raise ValueError("steps must be a whole number >= 0")
-    if len(coefficients) != 3:
-        raise ValueError("coefficients must be (a, b, c)")
+    _check_steps(steps, coefficients)
     m, n = g.shape[-2:]
     flat = g if g.dim() == 2 else g.reshape((g.shape[:-2].numel(), m, n))
     if g.numel() and (flat.stride(-1) != 1 and n > 1
@@ -350,17 +354,32 @@ class Muon(torch.optim.Optimizer):
                  weight_decay: float = 0.0, steps: int = 5, coefficients=MUON_COEFFICIENTS,
                  eps: float = 1e-7, state_dtype: torch.dtype = torch.float32,
                  work_dtype: torch.dtype | None = None):
-        if lr < 0 or not 0 <= momentum < 1 or weight_decay < 0:
-            raise ValueError("lr and weight_decay must be >= 0 and momentum in [0, 1)")
         super().__init__(params, dict(lr=lr, momentum=momentum, nesterov=nesterov,
                                       weight_decay=weight_decay, steps=steps,
                                       coefficients=tuple(coefficients), eps=eps,
                                       state_dtype=state_dtype, work_dtype=work_dtype))
-        for group in self.param_groups:
-            for p in group["params"]:
-                if p.dim() != 2:
-                    raise ValueError("Muon updates weights of two dimensions, got %s"
-                                     % (tuple(p.shape),))
+
+    def add_param_group(self, param_group):
+        super().add_param_group(param_group)
+        try:
+            self._check_group(self.param_groups[-1])
+        except ValueError:
+            self.param_groups.pop()
+            raise
+
+    @staticmethod
+    def _check_group(group):
+        if group["lr"] < 0 or not 0 <= group["momentum"] < 1 or group["weight_decay"] < 0:
+            raise ValueError("lr and weight_decay must be >= 0 and momentum in [0, 1)")
+        _check_steps(group["steps"], group["coefficients"])
+        if not group["state_dtype"].is_floating_point:
+            raise ValueError("state_dtype must be a floating-point type")
+        if group["work_dtype"] is not None and group["work_dtype"] not in _FMT:
+            raise ValueError("work_dtype must be float32, float16 or bfloat16")
+        for p in group["params"]:
+            if p.dim() != 2:
+                raise ValueError("Muon updates weights of two dimensions, got %s"
+                                 % (tuple(p.shape),))
 
     def load_state_dict(self, state_dict):
         """As torch.optim.Optimizer's, but the momentum is taken in `state_dtype`:

@@ -78,3 +78,27 @@ def test_loading_shares_nothing_and_runs_the_hooks():
     # a weight that has had no gradient has no state
     fresh = dense.Muon(weights(torch.bfloat16))
     dense.Muon(weights(torch.bfloat16)).load_state_dict(fresh.state_dict())
+
+
+def test_every_group_is_checked():
+    w = torch.zeros(4, 3, requires_grad=True)
+    for shape in ((3,), (2, 3, 4), (2, 3, 4, 5), ()):
+        bad = torch.zeros(shape, requires_grad=True)
+        with pytest.raises(ValueError):
+            dense.Muon([w, bad])
+        opt = dense.Muon([w])
+        with pytest.raises(ValueError):
+            opt.add_param_group({"params": [torch.zeros(2, 2, requires_grad=True), bad]})
+        assert len(opt.param_groups) == 1
+    for kw in (dict(lr=-1.0), dict(momentum=1.0), dict(momentum=-0.1), dict(weight_decay=-1.0), dict(steps=-1),
+               dict(steps=1.5), dict(coefficients=(1.0, 2.0)), dict(work_dtype=torch.float64), dict(state_dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            dense.Muon([w], **kw)
+        with pytest.raises(ValueError):
+            dense.Muon([{"params": [w], **kw}])
+        opt = dense.Muon([w])
+        with pytest.raises(ValueError):
+            opt.add_param_group({"params": [torch.zeros(2, 2, requires_grad=True)], **kw})
+        assert len(opt.param_groups) == 1
+    opt.add_param_group({"params": torch.zeros(2, 2, requires_grad=True), "lr": 0.5})
+    assert opt.param_groups[1]["lr"] == 0.5 and opt.param_groups[1]["steps"] == 5
