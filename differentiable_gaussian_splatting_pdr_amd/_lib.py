@@ -127,7 +127,8 @@ pdr_orthogonalize_args = _struct("pdr_orthogonalize_args", """
     ptr x
     len ldx, batch_x
     int steps
-    float a, b, c, eps""")
+    float a, b, c, eps
+    int g_f32""")
 
 
 class PdrError(RuntimeError):

@@ -662,12 +662,14 @@ void gated_backward(Walk &w, const pdr_gated_mlp &p) {
 
 // ------------------------------------------------------------ orthogonalize
 
+int g_fmt(const pdr_orthogonalize_args &p) { return p.g_f32 ? kF32 : p.fmt; }
+
 int check_ortho(const pdr_orthogonalize_args *p) {
   if (!p || !good_fmt(p->fmt) || p->steps < 0) return PDR_ERR_INVALID_ARG;
   if (!good_len(p->batch) || p->batch > 65535 || !good_len(p->m) || !good_len(p->n)) return PDR_ERR_INVALID_ARG;
   if (round8(p->m) > kMaxLd || round8(p->n) > kMaxLd) return PDR_ERR_INVALID_ARG;
   const long long rows = p->batch ? p->m : 0;
-  if (!good_mat(p->g, p->ldg, rows, p->n, p->fmt) || !good_mat(p->x, p->ldx, rows, p->n, p->fmt))
+  if (!good_mat(p->g, p->ldg, rows, p->n, g_fmt(*p)) || !good_mat(p->x, p->ldx, rows, p->n, p->fmt))
     return PDR_ERR_INVALID_ARG;
   if (!isfinite(p->a) || !isfinite(p->b) || !isfinite(p->c) || !isfinite(p->eps) || p->eps < 0.f)
     return PDR_ERR_INVALID_ARG;
@@ -692,7 +694,7 @@ void orthogonalize(Walk &w, const pdr_orthogonalize_args &p) {
                        long long cols, int vec) {
     if (!w.go()) return;
     hipLaunchKernelGGL(k_squares, dim3((unsigned)parts, (unsigned)p.batch), dim3(kThreads), 0, w.st,
-                       p.g, p.fmt, p.ldg, p.batch_g, (int)p.m, (int)p.n, vec_g,
+                       p.g, g_fmt(p), p.ldg, p.batch_g, (int)p.m, (int)p.n, vec_g,
                        make_fastdiv((uint32_t)((p.n + 7) / 8)), part);
     NormaliseArgs a = {};
     a.g = p.g;
@@ -703,7 +705,7 @@ void orthogonalize(Walk &w, const pdr_orthogonalize_args &p) {
     a.batch_g = p.batch_g;
     a.ldx = ldx;
     a.batch_x = batch_x;
-    a.fmt = p.fmt;
+    a.fmt = g_fmt(p);
     a.fmt_out = fmt;
     a.parts = parts;
     a.m = (int)p.m;

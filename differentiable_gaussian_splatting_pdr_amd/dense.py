@@ -311,31 +311,36 @@ def _check_steps(steps, coefficients):
 
 @torch.no_grad()
 def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=MUON_COEFFICIENTS,
-                  eps: float = 1e-7) -> torch.Tensor:
+                  eps: float = 1e-7, dtype: torch.dtype | None = None) -> torch.Tensor:
     """Bring the singular values of g [..., m, n] near one, by `steps` of
     X <- a X + (b A + c A^2) X with A = X X^T, from X = g / (|g|_F + eps).
 
-    A step of an optimiser: the result is no function of g to autograd."""
+    dtype: the result's type; g's, or with a float32 g any, which is normalised
+    before it is rounded.  A step of an optimiser: the result is no function of g to autograd."""
     _check("g", g)
     if _has_tangent(g):
         raise NotImplementedError("orthogonalize has no forward-mode derivative")
     if g.dim() < 2:
         raise ValueError("g must be [..., m, n]")
     _check_steps(steps, coefficients)
+    dtype = dtype or g.dtype
+    if dtype not in _FMT or dtype != g.dtype != torch.float32:
+        raise ValueError("dtype must be g's type, or g float32 and dtype float16 or bfloat16")
     m, n = g.shape[-2:]
     flat = g if g.dim() == 2 else g.reshape((g.shape[:-2].numel(), m, n))
     if g.numel() and (flat.stride(-1) != 1 and n > 1
                       or m > 1 and not n <= flat.stride(-2) <= _MAX_LD):
         flat = flat.contiguous()
-    out = torch.empty(g.shape, dtype=g.dtype, device=g.device)
+    out = torch.empty(g.shape, dtype=dtype, device=g.device)
     a = _lib.pdr_orthogonalize_args()
-    a.fmt, a.batch, a.m, a.n = _FMT[g.dtype], 1 if g.dim() == 2 else flat.shape[0], m, n
+    a.fmt, a.batch, a.m, a.n = _FMT[dtype], 1 if g.dim() == 2 else flat.shape[0], m, n
     a.g, a.ldg = flat.data_ptr(), flat.stride(-2) if m > 1 else max(n, 1)
     a.batch_g = flat.stride(0) if g.dim() > 2 else 0
     a.x, a.ldx, a.batch_x = out.data_ptr(), max(n, 1), m * n
     a.steps = int(steps)
     a.a, a.b, a.c = (float(v) for v in coefficients)
     a.eps = float(eps)
+    a.g_f32 = dtype != g.dtype
     _call("pdr_orthogonalize", a, g.device)
     return out
 
@@ -419,12 +424,15 @@ class Muon(torch.optim.Optimizer):
                 grad = p.grad.to(buf.dtype)
                 buf.mul_(group["momentum"]).add_(grad)
                 u = grad.add(buf, alpha=group["momentum"]) if group["nesterov"] else buf
-                u = u.to(group["work_dtype"] or p.dtype)
+                work = group["work_dtype"] or p.dtype
+                # fp16 holds the orthogonalisation's values, not a gradient's range
+                u = u.to(torch.float32 if work == torch.float16 else work)
                 alike.setdefault((p.shape, p.dtype, p.device), []).append((p, u))
             for (shape, _, _), pairs in alike.items():
                 scale = max(1.0, shape[0] / max(1, shape[1])) ** 0.5
                 updates = orthogonalize(torch.stack([u for _, u in pairs]), group["steps"],
-                                        group["coefficients"], group["eps"])
+                                        group["coefficients"], group["eps"],
+                                        dtype=group["work_dtype"] or pairs[0][0].dtype)
                 for (p, _), u in zip(pairs, updates):
                     p.mul_(1 - group["lr"] * group["weight_decay"])
                     p.add_(u.to(p.dtype), alpha=-group["lr"] * scale)

@@ -137,6 +137,8 @@ typedef struct {
     void *x; long long ldx, batch_x;  /* may not alias g */
     int steps;
     float a, b, c, eps;
+    int g_f32;                        /* not 0: g is PDR_FMT_F32, only x has format fmt: values that
+                                         fmt's range does not hold before they are normalised */
 } pdr_orthogonalize_args;
 
 long long pdr_orthogonalize_workspace_bytes(const pdr_orthogonalize_args *p);
