@@ -229,14 +229,15 @@ __global__ __launch_bounds__(kThreads) void k_normalise(NormaliseArgs a) {
   for (int i = threadIdx.x; i < a.parts; i += kThreads) s += a.part[blockIdx.y * a.parts + i];
   s = block_sum(s);
   if (!mine) return;
-  // 1 / (|g| + eps) as a value in [1/2, 1) and a power of two: no fp32 input
-  // makes the product with either leave fp32's range on the way
+  // 1 / (|g| + eps) as a power of two and a value in [1/2, 1), in this order: no
+  // fp32 input leaves fp32's range on the way up or loses bits on the way down,
+  // also where its own values are subnormal
   int e;
   const float f = (float)frexp(1.0 / (sqrt(s) + (double)a.eps), &e);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     // a zero matrix with eps = 0 stays zero rather than 0 * inf
-    const float t = v[i] == 0.f ? 0.f : ldexpf(v[i] * f, e + a.shift);
+    const float t = v[i] == 0.f ? 0.f : ldexpf(v[i], e + a.shift) * f;
     v[i] = t;
     lo[i] = t - f16_to_f(f_to_f16(t));
   }

@@ -153,3 +153,16 @@ def test_linear_fp16_rows_of_a_32_bit_gradient_far_apart():
     got = ws.grad.cpu()
     assert past.sum() == 3 and torch.equal(got[past].double(), value[past].sign() * float("inf"))
     ref.within(torch.where(past, torch.zeros_like(got), got), (torch.where(past, torch.zeros_like(value), value), bound), "dw")
+
+
+@pytest.mark.parametrize("dtype", (BF, FP))
+@pytest.mark.parametrize("steps", [0, 5])
+def test_orthogonalize_smallest_values(steps, dtype):
+    # values that are multiples of the type's smallest step, where eps is nothing
+    step = 2.0 ** -133 if dtype == BF else 2.0 ** -149
+    g = (torch.randint(-3, 4, (24, 40), generator=torch.Generator().manual_seed(1)).double() * step).to(dtype)
+    want = ref.orthogonalize(g, steps, NS, 0.0)
+    got = dense().orthogonalize(g.cuda(), steps=steps, eps=0.0).cpu().double()
+    plane = 2.0 ** -12 if dtype == BF else 2.0 ** -21
+    bound = max(steps, 1) * 3 * (plane + 64 * 2.0 ** -24) + ref.U[dtype]
+    assert ((got - want).norm() / want.norm()).item() <= bound
