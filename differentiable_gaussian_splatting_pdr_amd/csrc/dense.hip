@@ -117,6 +117,7 @@ struct DzArgs {
   float *colsum;  // [row block][N], or null
   long long lddy, ld_slope, ld_dz;
   int dy_fmt, slope_fmt, dz_fmt;
+  float slope_down;  // 1 / the scale that the slope is kept under
   int M, N, rows, vec;
 };
 template <int TX, bool SLOPE>
@@ -143,7 +144,7 @@ __global__ __launch_bounds__(kThreads) void k_dz(DzArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           // past N the slope's rows hold nothing that was written
-          if constexpr (SLOPE) v[u][j] = n + j < a.N ? v[u][j] * s[u][j] : 0.f;
+          if constexpr (SLOPE) v[u][j] = n + j < a.N ? v[u][j] * (s[u][j] * a.slope_down) : 0.f;
           sum[j] += v[u][j];
         }
         const long long at = (m + u * TY) * a.ld_dz + n;
@@ -435,7 +436,11 @@ int check_linear(const pdr_linear *p, bool backward) {
   return PDR_OK;
 }
 
+// A bf16 projection's slopes are kept in fp16, under a scale: they lie in
+// (-0.14, 1.14), and those of units that are nearly off (silu at -20: -4e-8)
+// keep fp16's 11 bits down to 2^-29.
 int slope_fmt(int fmt) { return fmt == kBf16 ? kF16 : kF32; }
+float slope_scale(int fmt) { return fmt == kBf16 ? 32768.f : 1.f; }
 
 // Few rows: the kernel for them, which lays nothing out.
 void multiply_few(Walk &w, const void *x, long long ldx, const void *wt, long long ldw,
@@ -458,6 +463,7 @@ void linear_forward(Walk &w, const pdr_linear &p) {
   e.act = p.activation;
   e.slope = p.activation != PDR_ACT_NONE ? p.slope : nullptr;
   e.slope_fmt = slope_fmt(p.fmt);
+  e.slope_scale = slope_scale(p.fmt);
   e.ld_slope = (int)round8(p.N);
   if (p.M <= kSkinnyRows)
     return multiply_few(w, p.x, p.ldx, p.w, p.ldw, 0, p.M, p.N, p.K, e, p.fmt, false);
@@ -502,6 +508,7 @@ void linear_backward(Walk &w, const pdr_linear &p) {
     a.ld_dz = z.ld;
     a.dy_fmt = p.out_fmt;
     a.slope_fmt = slope_fmt(p.fmt);
+    a.slope_down = 1.f / slope_scale(p.fmt);
     a.dz_fmt = in;
     a.M = (int)p.M;
     a.N = (int)p.N;

@@ -32,8 +32,9 @@ struct Epi {
   const void *res;  // format fmt
   int ldr;
   int act;
-  void *slope;  // format slope_fmt, or null
+  void *slope;  // slope_scale times it, format slope_fmt, or null
   int slope_fmt, ld_slope;
+  float slope_scale;
   // kEpiGated: gate and up sums kept for the gradient, fp32 [rows][2][ld_gu] (null: not kept)
   // kEpiGatedGrad: reads them; y = [dg | du], du at column up_at
   float *gu;
@@ -262,6 +263,8 @@ struct Columns<kEpiLinear, W, FLAGS> {
     if (flag<FLAGS>(e, kEpiLinear, kKeeps)) {
       float d[W];
       activate<W>(e.act, v, d);
+#pragma unroll
+      for (int i = 0; i < W; ++i) d[i] *= e.slope_scale;
       store_w<W>(e.slope, e.slope_fmt, place(m, e.ld_slope) + n, d);
     } else {
       activate<W>(e.act, v, nullptr);

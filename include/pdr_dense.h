@@ -57,9 +57,9 @@ long long pdr_dense_kept_ld(long long n);
 /* ------------------------------------------------------------------------ */
 /* Linear: x [M][K], w [N][K], bias [N] or NULL (format fmt); res [M][N] or
  * NULL, y [M][N] (format out_fmt: fmt or PDR_FMT_F32).  slope, if not NULL,
- * receives act'(z) for the backward: [M][kept_ld(N)], fp16 where fmt is bf16
- * (11 bits of a value in (-0.2, 1.2): below bf16's own rounding), else fp32.
- * Not used without an activation. */
+ * receives act'(z) for the backward: [M][kept_ld(N)], 2^15 act'(z) in fp16
+ * where fmt is bf16 (11 bits of a slope down to 2^-29: below bf16's own
+ * rounding), else fp32.  Not used without an activation. */
 typedef struct {
     int fmt, out_fmt, activation;
     long long M, N, K;

@@ -155,6 +155,26 @@ def test_linear_fp16_rows_of_a_32_bit_gradient_far_apart():
     ref.within(torch.where(past, torch.zeros_like(got), got), (torch.where(past, torch.zeros_like(value), value), bound), "dw")
 
 
+@pytest.mark.parametrize("M", [48, 200])
+def test_linear_bf16_gradient_of_units_that_are_nearly_off(M):
+    # silu'(z) is about z e^z for z in -12 .. -22: small, and as exact as any.
+    # Its own evaluation is off by (|z| + 4) 2^-23 of it, z's sum moves it by
+    # less than 2^-14 of it, it is kept to 2^-11 and dz to 2^-8 of itself; the
+    # result is rounded to 2^-8 of itself.
+    K, N = 64, 40
+    x, w = normal(1, M, K, dtype=BF), normal(2, N, K, scale=0.05, dtype=BF)
+    b = -torch.linspace(14, 20, N).to(BF)
+    dy = normal(3, M, N, dtype=BF)
+    X, W = x.double(), w.double()
+    dz = dy.double() * ref.slope("silu", X @ W.t() + b.double())
+    e = 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -13
+    xs, ws, bs = leaf(x), leaf(w), leaf(b)
+    dense().linear(xs, ws, bs, activation="silu").backward(dy.cuda())
+    for k, t, v, mag in (("dw", ws.grad, dz.t() @ X, dz.abs().t() @ X.abs()), ("db", bs.grad, dz.sum(0), dz.abs().sum(0)),
+                         ("dx", xs.grad, dz @ W, dz.abs() @ W.abs())):
+        ref.within(t, (v, e * mag + 2.0 ** -8 * v.abs()), k)
+
+
 @pytest.mark.parametrize("dtype", (BF, FP))
 @pytest.mark.parametrize("steps", [0, 5])
 def test_orthogonalize_smallest_values(steps, dtype):
