@@ -672,6 +672,39 @@ void gated_backward(Walk &w, const pdr_gated_mlp &p) {
 
 int g_fmt(const pdr_orthogonalize_args &p) { return p.g_f32 ? kF32 : p.fmt; }
 
+// Powers of two that keep the iterates' entries well inside fp16's normal
+// range: X's entries are at most a singular value and about 1/sqrt(n), those
+// of A and B = b A + c A^2 at most theirs and about 1/n.
+constexpr int kShiftX = 12, kShiftA = 10;
+constexpr double kMostX = 15.0, kMostA = 60.0;  // times the shifts: below 65504, with room for roundings
+
+// The largest of |f| over [0, most], at its ends or where its slope is zero.
+template <class F>
+double largest(F f, double most, double at0, double at1) {
+  double r = fabs(f(most));
+  for (double t : {at0, at1})
+    if (t > 0.0 && t < most) r = fmax(r, fabs(f(t)));
+  return r;
+}
+// Whether the iterates stay in range from singular values in [0, 1] on.
+bool stays_in_range(const pdr_orthogonalize_args &p) {
+  const double a = p.a, b = p.b, c = p.c;
+  double top = 1.0;
+  for (int i = 0; i < p.steps; ++i) {
+    const double t = top * top;
+    auto poly = [&](double x) { return b * x + c * x * x; };
+    if (t > kMostA || !(largest(poly, t, -b / (2.0 * c), 0.0) <= kMostA)) return false;
+    if (i + 1 == p.steps) break;  // the result has its own format
+    auto next = [&](double x) { return sqrt(x) * (a + x * (b + c * x)); };  // of the square
+    const double root = sqrt(9.0 * b * b - 20.0 * a * c);  // NaN: no such place
+    const double at0 = c != 0.0 ? (-3.0 * b + root) / (10.0 * c) : -a / (3.0 * b);
+    const double at1 = c != 0.0 ? (-3.0 * b - root) / (10.0 * c) : 0.0;
+    top = largest(next, t, at0, at1);
+    if (!(top <= kMostX)) return false;
+  }
+  return true;
+}
+
 int check_ortho(const pdr_orthogonalize_args *p) {
   if (!p || !good_fmt(p->fmt) || p->steps < 0) return PDR_ERR_INVALID_ARG;
   if (!good_len(p->batch) || p->batch > 65535 || !good_len(p->m) || !good_len(p->n)) return PDR_ERR_INVALID_ARG;
@@ -681,13 +714,9 @@ int check_ortho(const pdr_orthogonalize_args *p) {
     return PDR_ERR_INVALID_ARG;
   if (!isfinite(p->a) || !isfinite(p->b) || !isfinite(p->c) || !isfinite(p->eps) || p->eps < 0.f)
     return PDR_ERR_INVALID_ARG;
+  if (!stays_in_range(*p)) return PDR_ERR_INVALID_ARG;
   return PDR_OK;
 }
-
-// Powers of two that keep the iterates' entries well inside fp16's normal
-// range: X's entries are at most a singular value (< 8) and about 1/sqrt(n),
-// those of A and B at most (b + c) and about 1/n.
-constexpr int kShiftX = 12, kShiftA = 10;
 
 void orthogonalize(Walk &w, const pdr_orthogonalize_args &p) {
   const bool two = p.fmt != kBf16, tall = p.m > p.n;

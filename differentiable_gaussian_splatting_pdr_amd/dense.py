@@ -315,6 +315,8 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=MUON_COEFFICIENT
     """Bring the singular values of g [..., m, n] near one, by `steps` of
     X <- a X + (b A + c A^2) X with A = X X^T, from X = g / (|g|_F + eps).
 
+    coefficients: (a, b, c); those under which singular values from [0, 1] run
+    away from 1 leave the iterates' range and are refused (PdrError).
     dtype: the result's type; g's, or with a float32 g any, which is normalised
     before it is rounded.  A step of an optimiser: the result is no function of g to autograd."""
     _check("g", g)

@@ -127,9 +127,11 @@ int pdr_gated_mlp_backward(const pdr_gated_mlp *p, void *workspace, size_t works
  *   X <- a X + (b A + c A^2) X
  * The iterates are held in fp16 under a power-of-two scale (singular values
  * stay near 1, so 11 bits serve a bf16 result where bf16's 8 would not), in
- * two planes (22 bits) for fp16 and fp32 results.  The polynomial must keep
- * the iterates' singular values below 8, as Muon's (3.4445, -4.775, 2.0315)
- * does.  steps >= 0; with 0 the result is G / (|G|_F + eps). */
+ * two planes (22 bits) for fp16 and fp32 results.  Coefficients that take
+ * singular values s from [0, 1] on to s > 7.7, or to |b s^2 + c s^4| > 60, in
+ * what a step starts from are refused: the planes would not hold them (Muon's
+ * (3.4445, -4.775, 2.0315) reach 1.21 and 2.81).  steps >= 0; with 0 the result
+ * is G / (|G|_F + eps). */
 typedef struct {
     int fmt;                          /* of g and x */
     long long batch, m, n;

@@ -205,3 +205,19 @@ def test_gated_kept_values_beyond_the_passes_index_are_refused(name, M, F):
     assert size(ctypes.byref(gated(fmt=0, **sizes))) == -1
     assert size(ctypes.byref(gated(fmt=2, **sizes))) >= 0
     assert size(ctypes.byref(gated(fmt=0, **{**sizes, "M": M // 2}))) >= 0
+
+
+# What the iterates reach from singular values in [0, 1], and whether fp16 holds it under the fixed scales.
+COEFFICIENTS = [((3.4445, -4.7750, 2.0315), 5, True), ((3.4445, -4.7750, 2.0315), 100, True), ((2.0, -1.5, 0.5), 12, True),
+                ((15 / 8, -10 / 8, 3 / 8), 30, True), ((1.5, -0.5, 0.0), 30, True), ((1.0, 0.0, 0.0), 9, True),
+                ((0.0, 30.0, 25.0), 1, True), ((0.0, 40.0, 40.0), 1, False), ((0.0, -80.0, 80.0), 1, True),
+                ((0.0, -300.0, 300.0), 1, False), ((100.0, 0.0, 0.0), 1, True), ((100.0, 0.0, 0.0), 2, False),
+                ((1.1, 0.0, 0.0), 21, True), ((1.1, 0.0, 0.0), 40, False), ((2.0, 1.0, 1.0), 2, False), ((1e30, 0.0, 0.0), 1, True),
+                ((1e30, 1e30, 1e30), 0, True), ((7.0, 0.0, 0.0), 2, True), ((0.0, 0.0, 3e38), 1, False)]
+
+
+@pytest.mark.parametrize("c,steps,held", COEFFICIENTS)
+def test_coefficients_that_leave_the_iterates_range_are_refused(c, steps, held):
+    a = ortho(steps=steps, a=c[0], b=c[1], c=c[2])
+    size = _lib.lib().pdr_orthogonalize_workspace_bytes(ctypes.byref(a))
+    assert size > 0 if held else size == -1
