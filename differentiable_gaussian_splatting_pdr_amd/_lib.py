@@ -3,8 +3,10 @@ and ``include/pdr_dense.h``).
 
 Argument marshalling only: every function here forwards to the entry point of
 the same name and turns a negative status into :class:`PdrError`.  Pointers
-are passed as integers (device addresses, ``hipStream_t`` handles).  There is
-no fallback: if the library is not built, loading it raises.
+are passed as integers (device addresses, ``hipStream_t`` handles).  The dense
+operators' calls take a struct each (the classes below) and are made on
+:func:`lib` itself, with their status looked at by the caller.  There is no
+fallback: if the library is not built, loading it raises.
 """
 from __future__ import annotations
 
@@ -397,48 +399,3 @@ PDR_ACT_NONE, PDR_ACT_RELU, PDR_ACT_SILU, PDR_ACT_GELU = 0, 1, 2, 3
 
 def pdr_dense_kept_ld(n) -> int:
     return _raise(lib().pdr_dense_kept_ld(int(n)), "pdr_dense_kept_ld")
-
-
-def pdr_linear_forward_workspace_bytes(args) -> int:
-    return _raise(lib().pdr_linear_forward_workspace_bytes(args), "pdr_linear_forward")
-
-
-def pdr_linear_forward(args, workspace, workspace_bytes, stream):
-    return _raise(lib().pdr_linear_forward(args, workspace, workspace_bytes, stream),
-                  "pdr_linear_forward")
-
-
-def pdr_linear_backward_workspace_bytes(args) -> int:
-    return _raise(lib().pdr_linear_backward_workspace_bytes(args), "pdr_linear_backward")
-
-
-def pdr_linear_backward(args, workspace, workspace_bytes, stream):
-    return _raise(lib().pdr_linear_backward(args, workspace, workspace_bytes, stream),
-                  "pdr_linear_backward")
-
-
-def pdr_gated_mlp_forward_workspace_bytes(args) -> int:
-    return _raise(lib().pdr_gated_mlp_forward_workspace_bytes(args), "pdr_gated_mlp_forward")
-
-
-def pdr_gated_mlp_forward(args, workspace, workspace_bytes, stream):
-    return _raise(lib().pdr_gated_mlp_forward(args, workspace, workspace_bytes, stream),
-                  "pdr_gated_mlp_forward")
-
-
-def pdr_gated_mlp_backward_workspace_bytes(args) -> int:
-    return _raise(lib().pdr_gated_mlp_backward_workspace_bytes(args), "pdr_gated_mlp_backward")
-
-
-def pdr_gated_mlp_backward(args, workspace, workspace_bytes, stream):
-    return _raise(lib().pdr_gated_mlp_backward(args, workspace, workspace_bytes, stream),
-                  "pdr_gated_mlp_backward")
-
-
-def pdr_orthogonalize_workspace_bytes(args) -> int:
-    return _raise(lib().pdr_orthogonalize_workspace_bytes(args), "pdr_orthogonalize")
-
-
-def pdr_orthogonalize(args, workspace, workspace_bytes, stream):
-    return _raise(lib().pdr_orthogonalize(args, workspace, workspace_bytes, stream),
-                  "pdr_orthogonalize")

@@ -64,3 +64,9 @@ def test_inputs_without_elements_keep_their_gradient(no_launch, shape):
     r = torch.zeros(*shape[:-1], 4, requires_grad=True)
     y = dense.linear(x.detach(), torch.ones(4, n), residual=r)
     assert y.requires_grad and torch.autograd.grad(y.sum(), r)[0].shape == r.shape
+
+
+def test_kept_rows_are_as_far_apart_as_the_library_says():
+    from differentiable_gaussian_splatting_pdr_amd import _lib
+    for n in (0, 1, 7, 8, 9, 1000, 1 << 22):
+        assert dense._kept_ld(n) == _lib.pdr_dense_kept_ld(n)
