@@ -64,6 +64,9 @@ EXPORTED_DENSE = (
     "pdr_gated_mlp_backward",
     "pdr_orthogonalize_workspace_bytes",
     "pdr_orthogonalize",
+    "pdr_linear_products",
+    "pdr_gated_mlp_products",
+    "pdr_orthogonalize_products",
 )
 
 KERNEL_COUNT = 14
@@ -131,6 +134,10 @@ pdr_orthogonalize_args = _struct("pdr_orthogonalize_args", """
     int steps
     float a, b, c, eps
     int g_f32""")
+
+pdr_dense_product = _struct("pdr_dense_product", """
+    len M, N, K
+    int fmt, a_mc, b_mc, epilogue, batch, tile, groups, parts, lower""")
 
 
 class PdrError(RuntimeError):
@@ -223,6 +230,11 @@ def lib() -> ctypes.CDLL:
             size, call = getattr(L, name + "_workspace_bytes"), getattr(L, name)
             size.argtypes, size.restype = [ctypes.POINTER(args)], ll
             call.argtypes, call.restype = [ctypes.POINTER(args), vp, sz, vp], i
+        out = ctypes.POINTER(pdr_dense_product)
+        for name, args in (("pdr_linear_products", pdr_linear), ("pdr_gated_mlp_products", pdr_gated_mlp)):
+            getattr(L, name).argtypes, getattr(L, name).restype = [ctypes.POINTER(args), i, out, i], i
+        L.pdr_orthogonalize_products.argtypes = [ctypes.POINTER(pdr_orthogonalize_args), out, i]
+        L.pdr_orthogonalize_products.restype = i
         _lib = L
     return _lib
 
@@ -399,3 +411,16 @@ PDR_ACT_NONE, PDR_ACT_RELU, PDR_ACT_SILU, PDR_ACT_GELU = 0, 1, 2, 3
 
 def pdr_dense_kept_ld(n) -> int:
     return _raise(lib().pdr_dense_kept_ld(int(n)), "pdr_dense_kept_ld")
+
+
+def dense_products(args, backward=False):
+    """The products that a call with these arguments makes: pdr_*_products."""
+    L = lib()
+    if isinstance(args, pdr_orthogonalize_args):
+        name, extra = "pdr_orthogonalize_products", ()
+    else:
+        name, extra = type(args).__name__ + "_products", (int(backward),)
+    n = _raise(getattr(L, name)(args, *extra, None, 0), name)
+    out = (pdr_dense_product * n)()
+    _raise(getattr(L, name)(args, *extra, out, n), name)
+    return list(out)

@@ -273,6 +273,8 @@ struct Walk {
   bool run = false;
   hipError_t err = hipSuccess;
   PrepBatch repack = {}, split = {};  // laid out by flush(), before the next product
+  pdr_dense_product *out = nullptr;   // if asked for: the first `most` products
+  int most = 0, products = 0;
 
   void *take(size_t bytes) {
     void *p = base + at;
@@ -284,6 +286,10 @@ struct Walk {
     if (err == hipSuccess) err = e;
   }
   bool go() const { return run && err == hipSuccess; }
+  void note(const pdr_dense_product &p) {
+    if (products < most) out[products] = p;
+    ++products;
+  }
   void add(PrepBatch &b, const Prep &p) {
     if (b.count == kMaxPrep) flush();
     b.item[b.count++] = p;
@@ -398,6 +404,11 @@ GemmArgs product(long long M, long long N, long long K) {
 
 void multiply(Walk &w, const GemmArgs &g, int fmt, bool a_mc, bool b_mc, EpiKind kind) {
   w.flush();
+  if (w.out) {
+    const TilePlan t = plan_tiles(g, kind);
+    w.note({g.M, g.N, (long long)g.K * g.segs, product_fmt(fmt), a_mc, b_mc, kind, g.batches, t.tile,
+            t.groups, t.splits, t.lower});
+  }
   const size_t keep = w.at;
   void *ws = w.take(gemm_scratch_bytes(g, kind));
   if (w.go())
@@ -446,6 +457,7 @@ float slope_scale(int fmt) { return fmt == kBf16 ? 32768.f : 1.f; }
 void multiply_few(Walk &w, const void *x, long long ldx, const void *wt, long long ldw,
                   long long up_at, long long M, long long N, long long K, const Epi &epi, int fmt,
                   bool gated) {
+  if (w.out) w.note({M, N, K, fmt, 0, 0, gated ? kEpiGated : kEpiLinear, 1, 0, 1, 1, 0});
   if (!w.go()) return;
   SkinnyArgs a = {x, wt, ldx, ldw, up_at, (int)M, (int)N, (int)K, epi};
   w.done(launch_skinny(a, fmt, gated, w.st));
@@ -846,6 +858,17 @@ long long bytes_of(const Desc &d, Op op) {
 }
 
 template <class Desc, class Op>
+int products_of(const Desc &d, Op op, pdr_dense_product *out, int most) {
+  if (most < 0 || (most > 0 && !out)) return PDR_ERR_INVALID_ARG;
+  pdr_dense_product none;
+  Walk w;
+  w.out = out ? out : &none;
+  w.most = most;
+  op(w, d);
+  return w.products;
+}
+
+template <class Desc, class Op>
 int run_in(const Desc &d, Op op, void *workspace, size_t bytes, void *stream) {
   const long long need = bytes_of(d, op);
   if (need > 0 && (!workspace || ((uintptr_t)workspace & 255u) || bytes < (size_t)need))
@@ -908,6 +931,19 @@ int pdr_orthogonalize(const pdr_orthogonalize_args *p, void *workspace, size_t w
                       void *stream) {
   const int rc = check_ortho(p);
   return rc != PDR_OK ? rc : run_in(*p, orthogonalize, workspace, workspace_bytes, stream);
+}
+
+int pdr_linear_products(const pdr_linear *p, int backward, pdr_dense_product *out, int most) {
+  const int rc = check_linear(p, backward != 0);
+  return rc != PDR_OK ? rc : products_of(*p, backward ? linear_backward : linear_forward, out, most);
+}
+int pdr_gated_mlp_products(const pdr_gated_mlp *p, int backward, pdr_dense_product *out, int most) {
+  const int rc = check_gated(p, backward != 0);
+  return rc != PDR_OK ? rc : products_of(*p, backward ? gated_backward : gated_forward, out, most);
+}
+int pdr_orthogonalize_products(const pdr_orthogonalize_args *p, pdr_dense_product *out, int most) {
+  const int rc = check_ortho(p);
+  return rc != PDR_OK ? rc : products_of(*p, orthogonalize, out, most);
 }
 
 }  // extern "C"

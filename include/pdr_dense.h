@@ -147,6 +147,26 @@ long long pdr_orthogonalize_workspace_bytes(const pdr_orthogonalize_args *p);
 int pdr_orthogonalize(const pdr_orthogonalize_args *p, void *workspace, size_t workspace_bytes,
                       void *stream);
 
+/* ------------------------------------------------------------------------ */
+/* The products that a call makes, in order, and the kernels that they run in:
+ * for tests and tuning.  Returns their number (the first `most` are written to
+ * `out`) or a negative pdr_status.  Nothing is enqueued. */
+typedef struct {
+    long long M, N, K;   /* results, and what one of them sums over (in all segments) */
+    int fmt;             /* of the operands' planes */
+    int a_mc, b_mc;      /* operands read transposed */
+    int epilogue;        /* 0 linear, 1 gated, 2 its gradient, 3 a step's polynomial */
+    int batch;
+    int tile;            /* rows and columns of a workgroup's tile; 0: the kernel for few rows */
+    int groups;          /* of waves that share a tile's sums */
+    int parts;           /* that the sums are cut into, joined by a second kernel */
+    int lower;           /* only a symmetric result's lower tiles are computed */
+} pdr_dense_product;
+
+int pdr_linear_products(const pdr_linear *p, int backward, pdr_dense_product *out, int most);
+int pdr_gated_mlp_products(const pdr_gated_mlp *p, int backward, pdr_dense_product *out, int most);
+int pdr_orthogonalize_products(const pdr_orthogonalize_args *p, pdr_dense_product *out, int most);
+
 #ifdef __cplusplus
 }
 #endif

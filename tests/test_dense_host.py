@@ -221,3 +221,72 @@ def test_coefficients_that_leave_the_iterates_range_are_refused(c, steps, held):
     a = ortho(steps=steps, a=c[0], b=c[1], c=c[2])
     size = _lib.lib().pdr_orthogonalize_workspace_bytes(ctypes.byref(a))
     assert size > 0 if held else size == -1
+
+
+FMT = {"torch.float32": 0, "torch.float16": 1, "torch.bfloat16": 2}
+ACT = {"none": 0, "silu": 2, "gelu": 3}
+TILES = [(64, 1), (64, 4), (128, 1), (128, 2), (256, 1)]
+
+
+def test_struct_layout_of_a_product_matches_the_header(tmp_path):
+    src, exe = tmp_path / "layout.c", tmp_path / "layout"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "pdr_dense.h"\nint main(void) {\n'
+                   'printf("%zu", sizeof(pdr_dense_product));\n'
+                   + "\n".join('printf(" %%zu", offsetof(pdr_dense_product, %s));' % f
+                               for f, _ in _lib.pdr_dense_product._fields_) + "\nreturn 0; }\n")
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)],
+                   check=True)
+    said = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
+    assert [int(v) for v in said] == [ctypes.sizeof(_lib.pdr_dense_product)] + [
+        getattr(_lib.pdr_dense_product, f).offset for f, _ in _lib.pdr_dense_product._fields_]
+
+
+def test_sizes_take_every_product_kernel():
+    """The sizes of test_gpu_dense_tiles reach each kernel that a product may run in."""
+    import dense_sizes as sizes
+    kernels, epilogues, cut = set(), set(), set()
+
+    def note(p, columns):
+        whole = columns is None or columns % 8 == 0   # rows that begin on 16 bytes
+        kernels.add((p.fmt, p.a_mc, p.b_mc, p.epilogue, p.tile, p.groups, whole))
+        cut.add((p.a_mc, p.b_mc, p.epilogue, p.parts > 1, whole))
+
+    for dtype, out, M, K, N, act, residual in sizes.LINEAR:
+        c = dict(fmt=FMT[str(dtype)], out_fmt=FMT[str(out)], activation=ACT[act], M=M, N=N, K=K, ldx=K, ldw=K, bias=FAKE,
+                 ldy=N, slope=FAKE, lddy=N, dx=FAKE, lddx=K, dw=FAKE, lddw=K, dbias=FAKE)
+        forward, = _lib.dense_products(linear(res=FAKE if residual else None, ldr=N, **c))
+        dx, dw = _lib.dense_products(linear(**c), True)
+        for p, n in ((forward, N), (dx, K), (dw, K)):
+            note(p, n)
+        epilogues.add((forward.tile, forward.groups, act != "none", residual, str(out) == "torch.float32", N % 8 == 0))
+    for dtype, M, D, F, O in sizes.GATED:
+        c = dict(fmt=FMT[str(dtype)], M=M, D=D, F=F, O=O, ldx=D, ld_in=D, ld_out=F, ldy=O, lddy=O, lddx=D, dw_in=FAKE,
+                 ldd_in=D, dw_out=FAKE, ldd_out=F)
+        both, down = _lib.dense_products(gated(res=FAKE, ldr=O, **c))
+        dwo, dgu, dx, dwi = _lib.dense_products(gated(**c), True)
+        for p, n in ((both, None), (down, O), (dwo, F), (dgu, None), (dx, D), (dwi, D)):
+            note(p, n)
+    for fmt in (1, 2):
+        for a_mc, b_mc, epilogue in ((0, 0, 0), (0, 1, 0), (1, 1, 0), (0, 0, 1), (0, 1, 2)):
+            for tile, groups in TILES:
+                for whole in (True, False) if epilogue == 0 else (True,):
+                    assert (fmt, a_mc, b_mc, epilogue, tile, groups, whole) in kernels
+    for tile, groups in TILES:
+        for key in [(act, res, wide, whole) for act in (0, 1) for res in (0, 1) for wide in (0, 1) for whole in (0, 1)]:
+            assert (tile, groups, *map(bool, key)) in epilogues
+    for a_mc, b_mc, epilogue, whole in ((0, 0, 0, 0), (0, 0, 0, 1), (0, 1, 0, 0), (0, 1, 0, 1), (1, 1, 0, 0), (1, 1, 0, 1),
+                                        (0, 1, 2, 1)):
+        for parts in (True, False):
+            assert (a_mc, b_mc, epilogue, parts, bool(whole)) in cut
+
+    steps, last = set(), set()
+    for dtype, batch, m, n in sizes.ORTHOGONALIZE:
+        fmt = FMT[str(dtype)]
+        made = _lib.dense_products(ortho(fmt=fmt, batch=batch, m=m, n=n, ldg=n, batch_g=m * n, ldx=n, batch_x=m * n, steps=2))
+        assert len(made) == 6
+        steps.update((p.a_mc, p.b_mc, p.tile, p.groups, p.lower) for p in made)
+        last.add((made[5].b_mc, made[5].tile, fmt, n % 8 == 0))
+    for tile, groups in TILES:
+        for a_mc, b_mc, lower in ((0, 0, 0), (0, 0, 1), (0, 1, 0), (1, 1, 0), (1, 1, 1)):
+            assert (a_mc, b_mc, tile, groups, lower) in steps
+    assert {(b, f, w) for b, _, f, w in last} == {(b, f, w) for b in (0, 1) for f in (0, 1, 2) for w in (True, False)}
