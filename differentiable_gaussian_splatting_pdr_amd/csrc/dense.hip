@@ -1024,9 +1024,11 @@ TilePlan plan_tiles(const GemmArgs &g, EpiKind kind) {
     for (int lower = 0; lower <= (g.symmetric ? 1 : 0); ++lower) {
       p.lower = lower != 0;
       p.tiles = lower ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * p.tiles_n;
+      if ((long long)p.tiles * 256 * p.groups >= 1LL << 32) continue;  // more threads than a launch holds
       // storing a tile on both sides
       const double mirror = lower ? bm == 256 ? 14.0 : bm == 128 ? 4.0 : 2.0 : 0.0;
       for (p.splits = 1; p.splits <= most; ++p.splits) {
+        if (p.splits > 1 && (long long)g.M * g.epi.store_n >= 1LL << 31) break;  // nor would the second kernel's
         double us = tiles_us(c, batches * p.tiles * p.splits,
                              (double)((steps + p.splits - 1) / p.splits),
                              mirror + (p.splits > 1 ? 0.0 : slow));

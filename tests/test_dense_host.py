@@ -290,3 +290,19 @@ def test_sizes_take_every_product_kernel():
         for a_mc, b_mc, lower in ((0, 0, 0), (0, 0, 1), (0, 1, 0), (1, 1, 0), (1, 1, 1)):
             assert (a_mc, b_mc, tile, groups, lower) in steps
     assert {(b, f, w) for b, _, f, w in last} == {(b, f, w) for b in (0, 1) for f in (0, 1, 2) for w in (True, False)}
+
+
+@pytest.mark.parametrize("M,N,K", [(2 ** 31 - 257, 1, 8), (2 ** 30 + 100001, 1, 8), (2 ** 31 - 257, 8, 8), (2 ** 31 - 257, 7, 8),
+                                   (8, 8, 2 ** 31 - 257), (1 << 22, 4088, 8), (4096, 1 << 21, 8)])
+def test_launches_hold_their_threads(M, N, K):
+    """A launch has fewer than 2^32 threads along its first axis."""
+    # dw of (N x K outputs) sums over M rows: the third length is the sum's in one direction or the other
+    for act, fmt in ((0, 2), (3, 2), (0, 0)):
+        if K < 1 << 22:
+            made = _lib.dense_products(linear(fmt=fmt, out_fmt=fmt, activation=act, M=M, N=N, K=K, ldx=K, ldw=K, ldy=N))
+        else:
+            made = _lib.dense_products(linear(fmt=fmt, out_fmt=fmt, M=K, N=N, K=M, ldx=M, ldw=M, lddy=N, dw=FAKE, lddw=M), True)
+        for p in made:
+            tiles = ((p.M + p.tile - 1) // p.tile) * ((p.N + p.tile - 1) // p.tile)
+            assert tiles * 256 * p.groups < 2 ** 32 and p.parts < 65536
+            assert p.parts == 1 or p.M * p.N < 2 ** 31

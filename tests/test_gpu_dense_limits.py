@@ -67,3 +67,16 @@ def test_coefficients_at_the_end_of_the_iterates_range(c, steps, dtype):
     for bad, n in (((0.0, 40.0, 40.0), 1), ((100.0, 0.0, 0.0), 2), ((2.0, 1.0, 1.0), 3)):
         with pytest.raises(PdrError):
             dense.orthogonalize(g, n, bad)
+
+
+def test_more_rows_than_a_launch_of_small_tiles_holds():
+    from differentiable_gaussian_splatting_pdr_amd import dense
+    M = 2 ** 30 + 100001
+    x = torch.zeros(M, 8, dtype=torch.bfloat16, device="cuda")
+    w = torch.arange(1, 9, dtype=torch.bfloat16, device="cuda")[None]
+    at = torch.tensor([0, 1, 63, 64, 2 ** 30 - 1, 2 ** 30, 2 ** 30 + 65536, M - 129, M - 2, M - 1], device="cuda")
+    x[at] = torch.arange(1, 11, dtype=torch.bfloat16, device="cuda")[:, None]
+    y = dense.linear(x, w)
+    # 36 times the row's value, rounded to bf16
+    assert torch.equal(y[at, 0], (36.0 * torch.arange(1, 11, device="cuda")).to(torch.bfloat16))
+    assert y.count_nonzero() == 10
