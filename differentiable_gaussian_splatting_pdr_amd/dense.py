@@ -318,7 +318,8 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=MUON_COEFFICIENT
     coefficients: (a, b, c); those under which singular values from [0, 1] run
     away from 1 leave the iterates' range and are refused (PdrError).
     dtype: the result's type; g's, or with a float32 g any, which is normalised
-    before it is rounded.  A step of an optimiser: the result is no function of g to autograd."""
+    before it is rounded.  bfloat16 results come from iterates of 11 bits (up to
+    twice as far off as their own rounding), others from 22 bits.  A step of an optimiser: the result is no function of g to autograd."""
     _check("g", g)
     if _has_tangent(g):
         raise NotImplementedError("orthogonalize has no forward-mode derivative")
@@ -354,7 +355,8 @@ class Muon(torch.optim.Optimizer):
     p <- p (1 - lr weight_decay) - lr max(1, m / n)^(1/2) orthogonalize(u).
     The momentum is kept in `state_dtype` (float32 by default).  Weights of one
     shape and type are orthogonalised in one batch, in `work_dtype` (their own
-    type by default; bfloat16 takes a third of the products of float32).
+    type by default; bfloat16 takes a third of the products of float32 and
+    float16, which start from the update in float32).
     """
 
     def __init__(self, params, lr: float = 0.02, momentum: float = 0.95, nesterov: bool = True,

@@ -125,9 +125,12 @@ int pdr_gated_mlp_backward(const pdr_gated_mlp *p, void *workspace, size_t works
 /* Newton-Schulz orthogonalisation of each [m][n] matrix of a batch:
  *   X = G / (|G|_F + eps);  `steps` times: A = X X^T (X^T X where m > n),
  *   X <- a X + (b A + c A^2) X
- * The iterates are held in fp16 under a power-of-two scale (singular values
- * stay near 1, so 11 bits serve a bf16 result where bf16's 8 would not), in
- * two planes (22 bits) for fp16 and fp32 results.  Coefficients that take
+ * For fp16 and fp32 results the iterates are held in two fp16 planes (22 bits)
+ * under a power-of-two scale.  For bf16 results they have one (11 bits: every
+ * step's rounding of X, A and B is carried on, so that a result is 2.0e-3 to
+ * 2.5e-3 off after five steps and 2.3e-3 to 3.0e-3 after six, the more the
+ * longer its rows, where rounding it once to bf16 costs 1.7e-3); a caller who
+ * wants the 22 bits asks for an fp16 or fp32 result.  Coefficients that take
  * singular values s from [0, 1] on to s > 7.7, or to |b s^2 + c s^4| > 60, in
  * what a step starts from are refused: the planes would not hold them (Muon's
  * (3.4445, -4.775, 2.0315) reach 1.21 and 2.81).  steps >= 0; with 0 the result

@@ -80,3 +80,61 @@ def test_more_rows_than_a_launch_of_small_tiles_holds():
     # 36 times the row's value, rounded to bf16
     assert torch.equal(y[at, 0], (36.0 * torch.arange(1, 11, device="cuda")).to(torch.bfloat16))
     assert y.count_nonzero() == 10
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gated_offsets_beyond_31_bits(dtype):
+    # 2.3e9 gate and up sums, 1.15e9 values of h: the last rows, and their gradients
+    import dense_ref as ref
+    from differentiable_gaussian_splatting_pdr_amd import dense
+    from test_gpu_dense_range import plain_product
+    M, D, F, O = 280_003, 16, 4104, 8
+    gen = torch.Generator("cuda").manual_seed(1)
+    x, wi, wo = (torch.randn(*s, device="cuda", generator=gen).mul_(k).to(dtype).requires_grad_()
+                 for s, k in (((M, D), 1.0), ((2 * F, D), D ** -0.5), ((O, F), F ** -0.5)))
+    y = dense.gated_mlp(x, wi, wo)
+    at = torch.tensor([0, 1, 131071, 131072, 261633, 261634, 262143, 262144, M - 130, M - 2, M - 1], device="cuda")
+    dy = torch.zeros_like(y)
+    dy[at] = torch.randn(len(at), O, device="cuda", generator=gen).to(dtype)
+    gx, gi, go = torch.autograd.grad(y, (x, wi, wo), dy)
+    keep = ref.product
+    try:
+        ref.product = plain_product if dtype == torch.float32 else keep
+        want = ref.gated(*(t.detach() for t in (x[at], wi, wo)), None, "silu", dy[at])
+    finally:
+        ref.product = keep
+    # the weights' gradients sum 280000 rows, all but eleven of them zero
+    for k, t in (("y", y[at]), ("dx", gx[at]), ("dw_in", gi), ("dw_out", go)):
+        value, bound = want[k]
+        assert ((t.double() - value).abs() <= bound).all(), k
+    others = torch.ones(M, dtype=torch.bool, device="cuda")
+    others[at] = False
+    assert not gx[others].any()
+
+
+def test_fp32_offsets_beyond_31_bits():
+    # planes of 2.25e9 values each
+    import dense_ref as ref
+    from differentiable_gaussian_splatting_pdr_amd import dense
+    from test_gpu_dense_range import plain_product
+    M, K, N = 1_100_003, 2048, 16
+    gen = torch.Generator("cuda").manual_seed(2)
+    x = torch.randn(M, K, device="cuda", generator=gen).requires_grad_()
+    w = (torch.randn(N, K, device="cuda", generator=gen) * K ** -0.5).requires_grad_()
+    y = dense.linear(x, w)
+    at = torch.tensor([0, 1, 524287, 524288, 1048575, 1048576, M - 130, M - 2, M - 1], device="cuda")
+    dy = torch.zeros_like(y)
+    dy[at] = torch.randn(len(at), N, device="cuda", generator=gen)
+    gx, gw = torch.autograd.grad(y, (x, w), dy)
+    keep = ref.product
+    try:
+        ref.product = plain_product
+        want = ref.linear(x.detach()[at], w.detach(), None, None, "none", dy[at], torch.float32)
+    finally:
+        ref.product = keep
+    for k, t in (("y", y[at]), ("dx", gx[at]), ("dw", gw)):
+        value, bound = want[k]
+        assert ((t.double() - value).abs() <= bound).all(), k
+    others = torch.ones(M, dtype=torch.bool, device="cuda")
+    others[at] = False
+    assert not gx[others].any()

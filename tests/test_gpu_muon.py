@@ -103,3 +103,31 @@ def test_orthogonalize_of_fp32_to_another_type(shape, dtype):
         for to in (torch.float32, torch.float64, torch.bfloat16 if bad.dtype == HF else HF):
             with pytest.raises(ValueError):
                 d.orthogonalize(bad, dtype=to)
+
+
+@pytest.mark.parametrize("steps", [5, 6])
+@pytest.mark.parametrize("m,n", [(300, 2000), (336, 7000), (1024, 1024), (2000, 300)])
+def test_bf16_orthogonalisation_is_as_exact_as_its_roundings(m, n, steps):
+    # The error is that of rounding X, A and B once each step to fp16 under the
+    # documented scales, and the result to bf16, in an fp64 chain; sums in fp32
+    # add about (m + n)^(1/2) 2^-24 a step, their roundings' signs being
+    # independent.  Which way a value rounds where sums differ moves the error
+    # of a matrix by a few parts in a hundred: 1.1 times.
+    a, b, c = NS
+    g = torch.randn(m, n, device="cuda", generator=torch.Generator("cuda").manual_seed(m + n)).to(BF)
+    want = ref.orthogonalize(g, steps, NS, 1e-7)
+
+    def rounded(v, shift):
+        return (v * 2.0 ** shift).to(HF).double() * 2.0 ** -shift
+    x = g.double().t() if m > n else g.double()
+    x = rounded(x / (x.pow(2).sum().sqrt() + 1e-7), 12)
+    for k in range(steps):
+        p = rounded(x @ x.t(), 10)
+        x = a * x + rounded(b * p + c * (p @ p), 10) @ x
+        x = rounded(x, 12) if k + 1 < steps else x.to(BF).double()
+    x = x.t() if m > n else x
+    norm = want.norm()
+    allowed = 1.1 * ((x - want).norm() / norm) + steps * (m + n) ** 0.5 * 2.0 ** -24
+    off = (dense().orthogonalize(g, steps=steps).double() - want).norm() / norm
+    print("%dx%d, %d steps: %.2e, allowed %.2e" % (m, n, steps, off, allowed))
+    assert off <= allowed
