@@ -37,8 +37,9 @@ __device__ __forceinline__ double block_sum(double v) {
 }
 
 // Values as sums of bf16 values, each the rest's nearest: two hold fp16's 11
-// bits (and 16 of an fp32 value), three hold 24 bits, over fp32's own range (a rest below bf16's smallest step, 2^-133, is
-// lost: the last bits of values below 2^-110).
+// bits (and 16 of an fp32 value), three hold 24 bits, over fp32's own range (a
+// rest below bf16's smallest step, 2^-133, is lost: the last bits of values
+// below 2^-110).
 constexpr int kMaxPlanes = 3;
 __device__ __forceinline__ void store_planes(uint16_t *const *plane, int planes, long long at,
                                              float v[8]) {

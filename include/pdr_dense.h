@@ -17,8 +17,8 @@
  *    range (of values below 2^-110, the bits above 2^-133), and multiplied as
  *    the six products of those parts that matter: what is left out of a term
  *    is at most 2^-22 of it, whatever the other terms are.  An infinity in an
- *    fp32 operand makes the results it reaches not finite, as NaN or as an
- *    infinity.  (Forward products of at most 64 rows use the fp32 matrix
+ *    operand that is split makes the results it reaches not finite, as NaN or
+ *    as an infinity.  (Forward products of at most 64 rows use the fp32 matrix
  *    instruction instead.)
  *  - Matrices are row-major; ld* is the distance between rows in elements
  *    (>= the row's length, <= 2^22).  Rows that begin on 16 bytes (and, where
