@@ -321,7 +321,9 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=MUON_COEFFICIENT
     away from 1 leave the iterates' range and are refused (PdrError).
     dtype: the result's type; g's, or with a float32 g any, which is normalised
     before it is rounded.  bfloat16 results come from iterates of 11 bits (up to
-    twice as far off as their own rounding), others from 22 bits.  A step of an optimiser: the result is no function of g to autograd."""
+    twice as far off as their own rounding), others from 22 bits.
+    A step of an optimiser: the result is no function of g to autograd.
+    """
     _check("g", g)
     if _has_tangent(g):
         raise NotImplementedError("orthogonalize has no forward-mode derivative")
