@@ -8,7 +8,8 @@ gfx950 behind the C ABI of ``include/pdr_splat.h``; this package is the
 Python binding (``_lib``: ctypes, same names as the C entry points;
 ``splat``: PyTorch tensors, workspace handling, autograd).  ``dense`` holds the
 operators of the network in front of the layer and of its optimiser
-(``include/pdr_dense.h``).
+(``include/pdr_dense.h``), ``blocks`` those that make a transformer block of them
+(``include/pdr_blocks.h``).
 """
 from ._lib import (  # noqa: F401
     LIB_PATH,

@@ -1,10 +1,10 @@
-"""ctypes binding of ``libpdrsplat.so`` (the C ABI in ``include/pdr_splat.h``
-and ``include/pdr_dense.h``).
+"""ctypes binding of ``libpdrsplat.so`` (the C ABI in ``include/pdr_splat.h``,
+``include/pdr_dense.h`` and ``include/pdr_blocks.h``).
 
 Argument marshalling only: every function here forwards to the entry point of
 the same name and turns a negative status into :class:`PdrError`.  Pointers
 are passed as integers (device addresses, ``hipStream_t`` handles).  The dense
-operators' calls take a struct each (the classes below) and are made on
+operators' and the blocks' calls take a struct each (the classes below) and are made on
 :func:`lib` itself, with their status looked at by the caller.  There is no
 fallback: if the library is not built, loading it raises.
 """
@@ -69,13 +69,26 @@ EXPORTED_DENSE = (
     "pdr_orthogonalize_products",
 )
 
+EXPORTED_BLOCKS = (
+    "pdr_attention_forward_workspace_bytes",
+    "pdr_attention_forward",
+    "pdr_attention_backward_workspace_bytes",
+    "pdr_attention_backward",
+    "pdr_layer_norm_forward_workspace_bytes",
+    "pdr_layer_norm_forward",
+    "pdr_layer_norm_backward_workspace_bytes",
+    "pdr_layer_norm_backward",
+    "pdr_dropout_workspace_bytes",
+    "pdr_dropout",
+)
+
 KERNEL_COUNT = 14
 
 
 def _struct(name, spec):
-    """A C struct from "type name" lines (the layouts of pdr_dense.h)."""
+    """A C struct from "type name" lines (the layouts of pdr_dense.h and pdr_blocks.h)."""
     kinds = {"int": ctypes.c_int, "len": ctypes.c_longlong, "ptr": ctypes.c_void_p,
-             "float": ctypes.c_float}
+             "float": ctypes.c_float, "double": ctypes.c_double, "word": ctypes.c_ulonglong}
     fields = []
     for line in spec.strip().splitlines():
         kind, names = line.split(None, 1)
@@ -138,6 +151,42 @@ pdr_orthogonalize_args = _struct("pdr_orthogonalize_args", """
 pdr_dense_product = _struct("pdr_dense_product", """
     len M, N, K
     int fmt, a_mc, b_mc, epilogue, batch, tile, groups, parts, lower""")
+
+
+pdr_attention = _struct("pdr_attention", """
+    int fmt, causal
+    len batch, heads, kv_heads, dim
+    len q_rows, k_rows
+    ptr q_offsets, k_offsets, key_lengths
+    float scale
+""" + "".join("ptr %s\nlen %s_row, %s_head, %s_batch\n" % (t, t, t, t) + ("ptr lse\n" if t == "o" else "")
+              for t in ("q", "k", "v", "o", "dy", "dq", "dk", "dv")))
+
+pdr_layer_norm = _struct("pdr_layer_norm", """
+    int fmt
+    len rows, cols
+    float eps
+    ptr x
+    len ldx
+    ptr weight, bias, y
+    len ldy
+    ptr stats, dy
+    len lddy
+    ptr dx
+    len lddx
+    ptr dweight, dbias""")
+
+pdr_dropout_args = _struct("pdr_dropout_args", """
+    int fmt
+    len rows, cols
+    double p
+    word seed, offset
+    ptr seed_at, x
+    len ldx
+    ptr res
+    len ldr
+    ptr y
+    len ldy""")
 
 
 class PdrError(RuntimeError):
@@ -226,7 +275,12 @@ def lib() -> ctypes.CDLL:
         for name, args in (("pdr_linear_forward", pdr_linear), ("pdr_linear_backward", pdr_linear),
                            ("pdr_gated_mlp_forward", pdr_gated_mlp),
                            ("pdr_gated_mlp_backward", pdr_gated_mlp),
-                           ("pdr_orthogonalize", pdr_orthogonalize_args)):
+                           ("pdr_orthogonalize", pdr_orthogonalize_args),
+                           ("pdr_attention_forward", pdr_attention),
+                           ("pdr_attention_backward", pdr_attention),
+                           ("pdr_layer_norm_forward", pdr_layer_norm),
+                           ("pdr_layer_norm_backward", pdr_layer_norm),
+                           ("pdr_dropout", pdr_dropout_args)):
             size, call = getattr(L, name + "_workspace_bytes"), getattr(L, name)
             size.argtypes, size.restype = [ctypes.POINTER(args)], ll
             call.argtypes, call.restype = [ctypes.POINTER(args), vp, sz, vp], i

@@ -1,0 +1,348 @@
+"""The operators that make a transformer block of the dense ones (:mod:`.dense`):
+
+  attention    softmax(scale q k^T) v over whole, packed or cached sequences, differentiable
+  layer_norm   (x - mean) / sqrt(var + eps) * weight + bias of rows, differentiable
+  dropout      kept values / (1 - p) + residual, with a mask that is never stored, differentiable
+
+PyTorch provides device memory and the current HIP stream; the computation
+runs in the library's kernels through :mod:`._lib`.  Tensors live on one ROCm
+device and are float32, float16 or bfloat16, all of one type.  The last
+dimension is packed (anything else is copied first).
+"""
+from __future__ import annotations
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _lib
+from .dense import _call, _check, _differentiated, _ld, _rows
+from .splat import _FMT
+
+# ---------------------------------------------------------------- attention
+
+MAX_HEAD_DIM = 128
+_MAX_ROW, _MAX_HEAD, _MAX_HEADS = 1 << 22, 1 << 24, 1 << 28   # the kernels' largest strides
+
+
+def _heads(t: torch.Tensor) -> torch.Tensor:
+    """t [..., heads, D] as the kernels read it: rows of whole 16 bytes that begin on
+    16 bytes.  The tensor itself where it is so; else a copy, with zeros up to a
+    multiple."""
+    per = 16 // t.element_size()
+    d, strides = t.shape[-1], t.stride()
+    if d % per:
+        return torch.nn.functional.pad(t, (0, -d % per))
+    if t.numel() and (strides[-1] != 1 or any(s % per for s in strides[:-1]) or t.data_ptr() % 16
+                      or strides[-3] > _MAX_ROW or strides[-2] > _MAX_HEAD
+                      or strides[-2] * (t.shape[-2] - 1) > _MAX_HEADS):
+        return t.clone(memory_format=torch.contiguous_format)
+    return t
+
+
+def _place(a, name: str, t: torch.Tensor):
+    """The fields of a tensor [batch, tokens, heads, D] or [tokens, heads, D]."""
+    strides = t.stride()
+    setattr(a, name, t.data_ptr())
+    setattr(a, name + "_row", strides[-3])
+    setattr(a, name + "_head", strides[-2])
+    setattr(a, name + "_batch", strides[0] if t.dim() == 4 else 0)
+
+
+def _attention_args(q, k, v, causal, scale, offsets, key_offsets, key_lengths):
+    a = _lib.pdr_attention()
+    a.fmt, a.causal, a.scale = _FMT[q.dtype], causal, scale
+    a.heads, a.kv_heads, a.dim = q.shape[-2], k.shape[-2], q.shape[-1]
+    a.q_rows, a.k_rows = q.shape[-3], k.shape[-3]
+    if offsets is None:
+        a.batch = q.shape[0]
+        if key_lengths is not None:
+            a.key_lengths = key_lengths.data_ptr()
+    else:
+        a.batch = offsets.shape[0] - 1
+        a.q_offsets, a.k_offsets = offsets.data_ptr(), key_offsets.data_ptr()
+    _place(a, "q", q)
+    _place(a, "k", k)
+    _place(a, "v", v)
+    return a
+
+
+def _attention_forward(q, k, v, causal, scale, offsets, key_offsets, key_lengths, keep):
+    """(o, lse) of tensors that _heads has seen; lse only with `keep`."""
+    a = _attention_args(q, k, v, causal, scale, offsets, key_offsets, key_lengths)
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _place(a, "o", o)
+    lse = None
+    if keep:
+        lse = torch.empty((a.kv_heads, q.shape[:-2].numel(), a.heads // a.kv_heads),
+                          dtype=torch.float32, device=q.device)
+        a.lse = lse.data_ptr()
+    _call("pdr_attention_forward", a, q.device)
+    return o, lse
+
+
+def _to_dim(t, d):
+    return t if t.shape[-1] == d else t[..., :d].contiguous()
+
+
+class Attention(torch.autograd.Function):
+    """Attention of whole, packed or cached sequences; keeps the result and each
+    row's log of the sum of exponentials for the backward."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, causal, scale, offsets, key_offsets, key_lengths):
+        d = q.shape[-1]
+        q, k, v = _heads(q), _heads(k), _heads(v)
+        o, lse = _attention_forward(q, k, v, causal, scale, offsets, key_offsets, key_lengths, True)
+        ctx.save_for_backward(q, k, v, o, lse, offsets, key_offsets, key_lengths)
+        ctx.meta = (causal, scale, d)
+        return _to_dim(o, d)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        q, k, v, o, lse, offsets, key_offsets, key_lengths = ctx.saved_tensors
+        causal, scale, d = ctx.meta
+        a = _attention_args(q, k, v, causal, scale, offsets, key_offsets, key_lengths)
+        dy = _heads(dy)
+        _place(a, "o", o)
+        _place(a, "dy", dy)
+        a.lse = lse.data_ptr()
+        dq = dk = dv = None
+        if ctx.needs_input_grad[0]:
+            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            _place(a, "dq", dq)
+        if ctx.needs_input_grad[1] or ctx.needs_input_grad[2]:
+            dk, dv = (torch.empty(k.shape, dtype=k.dtype, device=k.device) for _ in range(2))
+            _place(a, "dk", dk)
+            _place(a, "dv", dv)
+        _call("pdr_attention_backward", a, q.device)
+        need = ctx.needs_input_grad
+        return (*(_to_dim(g, d) if n else None for g, n in zip((dq, dk, dv), need)),
+                None, None, None, None, None)
+
+
+def _check_index(name: str, t, like, length=None):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1:
+        raise ValueError("%s must be an int32 tensor of one dimension" % name)
+    if t.device != like.device:
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, like.device))
+    if length is not None and t.shape[0] != length:
+        raise ValueError("%s must be [%d]" % (name, length))
+    return t.contiguous()
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = False,
+              scale: float | None = None, offsets: torch.Tensor | None = None,
+              key_offsets: torch.Tensor | None = None,
+              key_lengths: torch.Tensor | None = None) -> torch.Tensor:
+    """softmax(scale q k^T) v for each sequence and head; q's shape.
+
+    Sequences of one length: q [B, Sq, Hq, D], k and v [B, Sk, Hk, D]; Hq is a
+    multiple of Hk, and query head h reads key head h // (Hq // Hk).
+    key_lengths (int32 [B], on the device): how many of its Sk keys each sequence
+    has, as for a cache that is being filled.
+    Packed sequences: q [T, Hq, D], k and v [Tk, Hk, D] with offsets (int32
+    [n + 1], on the device, not descending): sequence b has the queries
+    offsets[b] .. offsets[b + 1] - 1, and the same keys or those of key_offsets.
+    Tokens outside of all sequences get zeros.
+    causal: a query sees the keys up to its own, the last query being at the last
+    key: j <= i + (keys - queries).  A query that sees no key gets zeros.
+    scale: positive; D ** -0.5 by default.  D is at most 128.
+    """
+    _check("q", q)
+    _check("k", k, q.dtype, q.device)
+    _check("v", v, q.dtype, q.device)
+    dim = 4 if offsets is None else 3
+    if q.dim() != dim or k.dim() != dim:
+        raise ValueError("q and k must be [B, S, H, D], or with offsets [T, H, D]")
+    if k.shape != v.shape or q.shape[-1] != k.shape[-1] or dim == 4 and q.shape[0] != k.shape[0]:
+        raise ValueError("q, k and v disagree: %s, %s, %s" % (tuple(q.shape), tuple(k.shape), tuple(v.shape)))
+    heads, kv_heads, d = q.shape[-2], k.shape[-2], q.shape[-1]
+    if not 0 < d <= MAX_HEAD_DIM:
+        raise ValueError("heads must have 1 to %d values" % MAX_HEAD_DIM)
+    if kv_heads < 1 or heads < 1 or heads % kv_heads:
+        raise ValueError("q's heads must be a multiple of k's: %d, %d" % (heads, kv_heads))
+    scale = d ** -0.5 if scale is None else float(scale)
+    if not 0 < scale < float("inf"):
+        raise ValueError("scale must be positive and finite")
+    if offsets is None:
+        if key_offsets is not None:
+            raise ValueError("key_offsets needs offsets")
+        if key_lengths is not None:
+            key_lengths = _check_index("key_lengths", key_lengths, q, q.shape[0])
+    else:
+        if key_lengths is not None:
+            raise ValueError("key_lengths is for sequences without offsets")
+        offsets = _check_index("offsets", offsets, q)
+        if offsets.shape[0] < 1:
+            raise ValueError("offsets must have a value more than there are sequences")
+        key_offsets = (offsets if key_offsets is None
+                       else _check_index("key_offsets", key_offsets, q, offsets.shape[0]))
+    rest = (bool(causal), scale, offsets, key_offsets, key_lengths)
+    if _differentiated(q, k, v):
+        return Attention.apply(q, k, v, *rest)
+    return _to_dim(_attention_forward(_heads(q), _heads(k), _heads(v), *rest, False)[0], d)
+
+
+# --------------------------------------------------------------- layer norm
+
+def _norm_args(x, weight, eps):
+    a = _lib.pdr_layer_norm()
+    a.fmt, a.eps = _FMT[x.dtype], eps
+    a.rows, a.cols = x.shape
+    a.x, a.ldx = x.data_ptr(), _ld(x)
+    if weight is not None:
+        a.weight = weight.data_ptr()
+    return a
+
+
+def _norm_forward(x, weight, bias, eps, keep):
+    """(y, stats); stats only with `keep`."""
+    a = _norm_args(x, weight, eps)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    a.y, a.ldy = y.data_ptr(), max(a.cols, 1)
+    if bias is not None:
+        a.bias = bias.data_ptr()
+    stats = None
+    if keep:
+        stats = torch.empty((a.rows, 2), dtype=torch.float32, device=x.device)
+        a.stats = stats.data_ptr()
+    _call("pdr_layer_norm_forward", a, x.device)
+    return y, stats
+
+
+class LayerNorm(torch.autograd.Function):
+    """Layer norm of rows; keeps each row's mean and inverse deviation."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        y, stats = _norm_forward(x, weight, bias, eps, True)
+        ctx.save_for_backward(x, weight, stats)
+        ctx.eps = eps
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, stats = ctx.saved_tensors
+        a = _norm_args(x, weight, ctx.eps)
+        rows = _rows(dy)
+        a.dy, a.lddy = rows.data_ptr(), _ld(rows)
+        a.stats = stats.data_ptr()
+        need = ctx.needs_input_grad
+        dx = dw = db = None
+        if need[0]:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            a.dx, a.lddx = dx.data_ptr(), max(a.cols, 1)
+        if need[1]:
+            dw = torch.empty((a.cols,), dtype=x.dtype, device=x.device)
+            a.dweight = dw.data_ptr()
+        if need[2]:
+            db = torch.empty((a.cols,), dtype=x.dtype, device=x.device)
+            a.dbias = db.data_ptr()
+        _call("pdr_layer_norm_backward", a, x.device)
+        return dx, dw, db, None
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
+               bias: torch.Tensor | None = None, eps: float = 1e-5) -> torch.Tensor:
+    """(x - mean) / sqrt(var + eps) * weight + bias over the last dimension of x
+    [..., N]; weight and bias [N], or None for one and zero.
+
+    The squares of centred values are summed in fp32 and have to be in its range.
+    """
+    _check("x", x)
+    if x.dim() < 1:
+        raise ValueError("x must be [..., N]")
+    n = x.shape[-1]
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _check(name, t, x.dtype, x.device, 1)
+            if t.shape[0] != n:
+                raise ValueError("%s must be [%d]" % (name, n))
+    eps = float(eps)
+    if not 0 <= eps < float("inf"):
+        raise ValueError("eps must be finite and not negative")
+    args = (_rows(x), None if weight is None else weight.contiguous(),
+            None if bias is None else bias.contiguous(), eps)
+    y = LayerNorm.apply(*args) if _differentiated(x, weight, bias) else _norm_forward(*args, False)[0]
+    return y if x.dim() == 2 else y.view(x.shape)
+
+
+# ------------------------------------------------------------------ dropout
+
+def _dropout(x, residual, p, seed, offset):
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    a = _lib.pdr_dropout_args()
+    a.fmt, a.p, a.offset = _FMT[x.dtype], p, offset
+    a.rows, a.cols = x.shape
+    if isinstance(seed, torch.Tensor):
+        a.seed_at = seed.data_ptr()
+    else:
+        a.seed = seed
+    a.x, a.ldx = x.data_ptr(), _ld(x)
+    a.y, a.ldy = y.data_ptr(), max(a.cols, 1)
+    if residual is not None:
+        a.res, a.ldr = residual.data_ptr(), _ld(residual)
+    _call("pdr_dropout", a, x.device)
+    return y
+
+
+class Dropout(torch.autograd.Function):
+    """Dropout of rows; the backward draws the same bits again."""
+
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, offset):
+        if isinstance(seed, torch.Tensor):
+            ctx.save_for_backward(seed)
+            ctx.seed = None
+        else:
+            ctx.seed = seed
+        ctx.meta = (p, offset)
+        return _dropout(x, residual, p, seed, offset)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        seed = ctx.saved_tensors[0] if ctx.seed is None else ctx.seed
+        p, offset = ctx.meta
+        dx = _dropout(_rows(dy), None, p, seed, offset) if ctx.needs_input_grad[0] else None
+        return dx, dy if ctx.needs_input_grad[1] else None, None, None, None
+
+
+def dropout(x: torch.Tensor, p: float, seed, offset: int = 0,
+            residual: torch.Tensor | None = None) -> torch.Tensor:
+    """x / (1 - p) where an element is kept, 0 elsewhere, + residual (x's shape).
+
+    Which elements are kept is a function of (seed, offset, element) alone: 16 bits
+    of Philox 4x32-10 each, compared with p 2^16 (p is taken to a multiple of 2^-16).
+    seed: a whole number below 2^64, or an int64 tensor of one element on x's
+    device, which is read when the kernels run, so that replays of a captured
+    graph may draw anew; it may not change between a forward and its backward.
+    offset: a whole number below 2^64, such as a layer's and a step's, for masks
+    under one seed.
+    """
+    _check("x", x)
+    p = float(p)
+    if not 0 <= p <= 1:
+        raise ValueError("p must be in [0, 1]")
+    if isinstance(seed, torch.Tensor):
+        if seed.dtype != torch.int64 or seed.numel() != 1 or seed.device != x.device:
+            raise ValueError("seed must be a whole number, or an int64 tensor of one element on %s" % x.device)
+    elif int(seed) != seed or not 0 <= seed < 1 << 64:
+        raise ValueError("seed must be a whole number in [0, 2^64)")
+    else:
+        seed = int(seed)
+    if int(offset) != offset or not 0 <= offset < 1 << 64:
+        raise ValueError("offset must be a whole number in [0, 2^64)")
+    if residual is not None:
+        _check("residual", residual, x.dtype, x.device)
+        if residual.shape != x.shape:
+            raise ValueError("residual must be %s" % (tuple(x.shape),))
+    flat = x if x.dim() else x.view(1)
+    rest = None
+    if residual is not None:
+        rest = _rows(residual if residual.dim() else residual.view(1))
+    args = (_rows(flat), rest, p, seed, int(offset))
+    y = Dropout.apply(*args) if _differentiated(x, residual) else _dropout(*args)
+    return y if x.dim() == 2 else y.view(x.shape)

@@ -1,0 +1,384 @@
+// attention.hpp -- what the attention kernels share: where a workgroup's rows
+// and keys lie, tiles of rows in LDS, and the two kinds of matrix product.
+//
+// Rows.  A key head is read by G = heads / kv_heads query heads.  Their queries
+// are taken together: row r of a sequence and key head is head r % G of token
+// r / G.  One pass over the keys then serves the whole group, a single token's
+// heads share one tile, and the gradients of shared heads are sums over rows
+// like any other.
+//
+// Products.  Both kinds are 32x32 matrix instructions whose result has 32 tile
+// rows in registers and one column per lane (lane % 32): register r of half
+// h = lane / 32 holds row 8 (r / 4) + 4 h + r % 4.
+//   along()  c[row][col] += sum_d tile[row][d] reg[col][d]: scores, from rows
+//            of an LDS tile and rows that the lanes keep in registers;
+//   across() c[d][col] += sum_row tile[row][d] p[row][col]: sums over rows,
+//            whose weights p are just what along() left in the registers: the
+//            sum's order over rows is free, so register r, half h stands for
+//            the same row in both operands and nothing moves between lanes.
+// A softmax over rows is then a sum over a lane's registers and its other half.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dense_epilogue.hpp"
+#include "pdr_blocks.h"
+#include "pdr_common.hpp"
+
+namespace pdr {
+namespace attend {
+
+using dense::bf16_to_f;
+using dense::f16_to_f;
+using dense::kBf16;
+using dense::kF16;
+using dense::kF32;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr uint32_t kOutside = 0x80000000u;  // a byte offset beyond every buffer's bound
+constexpr long long kMaxRow = 1 << 22, kMaxHead = 1 << 24, kMaxHeads = 1 << 28;  // elements
+
+struct Mat {
+  char *p;
+  long long row, head, batch;  // elements
+};
+
+struct Args {
+  Mat q, k, v, o, dy, dq, dk, dv;
+  const int *q_offsets, *k_offsets, *key_lengths;
+  float *lse, *delta;
+  float *part_o, *part_ml;  // few queries: the splits' sums, and their maxima and weights
+  float scale, scale2;      // scale, and scale log2(e)
+  int causal, batch, kv_heads, dim, q_rows, k_rows;
+  int q_tiles, k_tiles;     // of a sequence; with offsets, of all
+  int splits;
+  FastDiv group;            // by G
+  FastDiv heads;            // by kv_heads
+  FastDiv per_seq;          // by the tiles of a sequence (no offsets)
+};
+
+// ------------------------------------------------------------ where things lie
+
+// A workgroup's tile: the sequence, its queries and keys, the tile in it.
+struct Place {
+  int seq, nq, nk;   // tokens
+  int q0, k0;        // first token in the tensor (offsets), or 0
+  int stored;        // keys that the tensor has from k0 on and that belong to this sequence
+  int tile;          // -1: nothing to do
+};
+
+__device__ __forceinline__ int bound_at(const int *off, int n, int total, int i) {
+  if (i <= 0) return 0;
+  if (i > n + 1) return total;
+  const int v = off[i - 1];
+  return v < 0 ? 0 : v > total ? total : v;
+}
+
+// Tiles of packed sequences.  Bounds 0, off[0], .., off[n], total cut the tokens
+// into n + 2 sequences, of which the first and last hold what no sequence has.
+// Sequence i's tiles begin at floor(bound_i G / 2^LOG) + i, which leaves room for
+// all of them whatever their lengths: no list has to be made first, and at most
+// one workgroup a sequence has nothing to do.  The search looks at 64 bounds at
+// a time.
+template <int LOG>
+__device__ __forceinline__ int find_sequence(const int *off, int n, int total, int g, int t) {
+  int lo = 0, count = n + 2;
+  const int lane = threadIdx.x & 63;
+  while (count > 1) {
+    const int step = (count + 63) >> 6;
+    const int i = lo + lane * step;
+    const bool in = lane * step < count &&
+                    (int)(((long long)bound_at(off, n, total, i) * g) >> LOG) + i <= t;
+    const uint64_t no = ~__ballot(in);
+    int k = no ? __ffsll((unsigned long long)no) - 2 : 63;
+    k = __builtin_amdgcn_readfirstlane(k < 0 ? 0 : k);
+    lo += k * step;
+    count = count - k * step < step ? count - k * step : step;
+  }
+  return lo;
+}
+
+// BY_KEYS: t counts tiles of 2^LOG keys; else of 2^LOG rows (g to a token).
+template <int LOG, bool BY_KEYS>
+__device__ __forceinline__ Place place(const Args &a, int t) {
+  Place p;
+  const int g = BY_KEYS ? 1 : (int)a.group.d;
+  if (!a.q_offsets) {
+    p.seq = (int)fdiv((uint32_t)t, a.per_seq);
+    p.tile = t - p.seq * (int)a.per_seq.d;
+    p.nq = a.q_rows;
+    p.nk = a.k_rows;
+    if (a.key_lengths) {
+      const int len = a.key_lengths[p.seq];
+      p.nk = len < 0 ? 0 : len > a.k_rows ? a.k_rows : len;
+    }
+    p.q0 = p.k0 = 0;
+    p.stored = a.k_rows;
+    return p;
+  }
+  const int *off = BY_KEYS ? a.k_offsets : a.q_offsets;
+  const int total = BY_KEYS ? a.k_rows : a.q_rows;
+  const int i = find_sequence<LOG>(off, a.batch, total, g, t);
+  const int begin = bound_at(off, a.batch, total, i);
+  int end = bound_at(off, a.batch, total, i + 1);
+  if (end < begin) end = begin;
+  p.seq = 0;
+  p.tile = t - ((int)(((long long)begin * g) >> LOG) + i);
+  const bool real = i >= 1 && i <= a.batch;
+  // the other side's tokens; the first and last sequence have none
+  const int *off2 = BY_KEYS ? a.q_offsets : a.k_offsets;
+  const int total2 = BY_KEYS ? a.q_rows : a.k_rows;
+  const int begin2 = real ? bound_at(off2, a.batch, total2, i) : 0;
+  int end2 = real ? bound_at(off2, a.batch, total2, i + 1) : 0;
+  if (end2 < begin2) end2 = begin2;
+  p.q0 = BY_KEYS ? begin2 : begin;
+  p.nq = BY_KEYS ? end2 - begin2 : end - begin;
+  p.k0 = BY_KEYS ? begin : begin2;
+  p.nk = BY_KEYS ? end - begin : end2 - begin2;
+  p.stored = p.nk;
+  return p;
+}
+
+// First element of a sequence's tokens at a head.
+__device__ __forceinline__ long long first_of(const Mat &m, const Place &p, int token0, int head) {
+  return p.seq * m.batch + token0 * m.row + head * m.head;
+}
+
+// -------------------------------------------------------------- element types
+
+template <int FMT, int DP>  // DP: values a row has in LDS and registers (dim, rounded up)
+struct Core {
+  static constexpr int kSize = FMT == kF32 ? 4 : 2;
+  static constexpr int kPer = 16 / kSize;             // values of a 16-byte chunk
+  static constexpr int kChunks = DP / kPer;           // of a row
+  static constexpr int kSteps = kChunks / 2;          // of along()
+  static constexpr int kRowBytes = DP * kSize;
+  static constexpr int kBlocks = DP / 32;             // of 32 d
+
+  // LDS: chunk c of row r is stored at chunk c ^ swizzle(r).  Eight rows' equal
+  // chunks fall on different banks (along), and so do the 32 bytes that each of
+  // four rows gives to a transposing read (across).
+  static __device__ __forceinline__ int swizzle(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+
+  static __device__ __forceinline__ f32x16 go(i32x4 a, i32x4 b, f32x16 c) {
+    if constexpr (FMT == kBf16) {
+      return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                     __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    } else if constexpr (FMT == kF16) {
+      return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                    __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        c = __builtin_amdgcn_mfma_f32_32x32x2f32(__int_as_float(a[i]), __int_as_float(b[i]), c, 0, 0,
+                                                 0);
+      return c;
+    }
+  }
+
+  // A lane's chunks of a row in memory, as along() wants them; zeros past dim.
+  static __device__ __forceinline__ void fetch_row(i32x4 (&f)[kSteps], const char *row, int dim,
+                                                   int half, bool there) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int c = 2 * s + half;
+      f[s] = i32x4{0, 0, 0, 0};
+      if (there && c * kPer < dim) f[s] = *(const i32x4 *)(row + c * 16);
+    }
+  }
+
+  static __device__ __forceinline__ void along(f32x16 &c, const char *tile, int row0,
+                                               const i32x4 (&reg)[kSteps], int lane) {
+    const int r = row0 + (lane & 31), half = lane >> 5, sw = swizzle(r);
+    const lds_char *p = (const lds_char *)tile + r * kRowBytes;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const i32x4 a =
+          *(const __attribute__((address_space(3))) i32x4 *)(p + (((2 * s + half) ^ sw) << 4));
+      c = go(a, reg[s], c);
+    }
+  }
+
+  // Sixteen rows from row0 on, whose weights are 8 registers of an along().
+  static __device__ __forceinline__ void across(f32x16 (&c)[kBlocks], const char *tile, int row0,
+                                                const float *p, int lane) {
+    const int half = lane >> 5;
+    if constexpr (FMT != kF32) {
+      typedef float f32x2 __attribute__((ext_vector_type(2)));
+      typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+      typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+      i32x4 w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x2 two = {p[2 * i], p[2 * i + 1]};
+        w[i] = FMT == kBf16 ? __builtin_bit_cast(int, __builtin_convertvector(two, b2))
+                            : __builtin_bit_cast(int, __builtin_convertvector(two, h2));
+      }
+      const int t = lane & 15, r = row0 + 4 * half + (t >> 2);
+      const int c0 = ((lane >> 4) & 1) * 2 + ((t & 3) >> 1), byte = (t & 1) * 8;
+      const lds_char *lo = (const lds_char *)tile + r * kRowBytes + byte;
+      const lds_char *hi = lo + 8 * kRowBytes;
+      const int sl = swizzle(r), sh = swizzle(r + 8);
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        const s16x4 x = transposed((lds_s16x4 *)(lo + (((b * 4 + c0) ^ sl) << 4)));
+        const s16x4 y = transposed((lds_s16x4 *)(hi + (((b * 4 + c0) ^ sh) << 4)));
+        const s16x8 f = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+        c[b] = go(__builtin_bit_cast(i32x4, f), w, c[b]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int r = row0 + 8 * (e >> 2) + 4 * half + (e & 3);
+        const int d = lane & 31;
+        const lds_char *at = (const lds_char *)tile + r * kRowBytes + (d & 3) * 4;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+          const float f = *(const __attribute__((address_space(3))) float *)(
+              at + (((b * 8 + (d >> 2)) ^ swizzle(r)) << 4));
+          c[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(f, p[e], c[b], 0, 0, 0);
+        }
+      }
+    }
+  }
+  // ds_read_b64_tr_b16: of each 16 lanes' 4 rows of 16 values (a row is four
+  // lanes' 8 bytes), lane t receives column t.  The restrict pointer tells the
+  // compiler that the read does not wait for loads to LDS in flight.
+  static __device__ __forceinline__ s16x4 transposed(lds_s16x4 *__restrict p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+  }
+};
+
+// Copies tiles of ROWS rows to LDS (loads straight to LDS, zeros for rows that
+// do not exist and past dim), by NW waves.  Rows are keys (row apart), or the
+// rows of a group of heads.
+template <class C, int ROWS, int NW>
+struct Loader {
+  static constexpr int kBytes = ROWS * C::kRowBytes;
+  static constexpr int kIssues = kBytes / (NW * 1024);
+  static constexpr int kRowsEach = 1024 / C::kRowBytes;  // rows of one wave's load
+  static_assert(kBytes % (NW * 1024) == 0 && kRowsEach * C::kRowBytes == 1024, "whole loads");
+  const char *base;   // first token of the sequence, this head
+  uint32_t row, head; // bytes
+  int chunk[kIssues]; // byte of this lane's chunk in its row, or kOutside
+  int wave, lane;
+
+  __device__ __forceinline__ void init(const Mat &m, long long first, int dim, int wave_, int lane_) {
+    wave = wave_;
+    lane = lane_;
+    base = m.p + first * C::kSize;
+    row = (uint32_t)(m.row * C::kSize);
+    head = (uint32_t)(m.head * C::kSize);
+#pragma unroll
+    for (int i = 0; i < kIssues; ++i) {
+      const int c = (lane % C::kChunks) ^ C::swizzle(row_of(i));
+      chunk[i] = c * C::kPer < dim ? c * 16 : (int)kOutside;
+    }
+  }
+  __device__ __forceinline__ int row_of(int i) const {
+    return (i * NW + wave) * kRowsEach + lane / C::kChunks;
+  }
+  __device__ __forceinline__ void issue(const char *from, uint32_t off, char *lds, int i) const {
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc((void *)from, 0, (int)kOutside, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(lds + (i * NW + wave) * 1024), 16,
+                                             (int)off, 0, 0, 0);
+  }
+  // Rows [first, first + ROWS) of `rows`.
+  __device__ __forceinline__ void tokens(int first, int rows, char *lds) const {
+    const char *from = base + (long long)first * row;
+#pragma unroll
+    for (int i = 0; i < kIssues; ++i) {
+      const int r = row_of(i);
+      const bool in = first + r < rows && chunk[i] >= 0;
+      issue(from, in ? (uint32_t)r * row + (uint32_t)chunk[i] : kOutside, lds, i);
+    }
+  }
+  // The same of rows in groups.
+  __device__ __forceinline__ void grouped(int first, int rows, const FastDiv &group, char *lds) const {
+    const int token0 = (int)fdiv((uint32_t)first, group);
+    const char *from = base + (long long)token0 * row;
+#pragma unroll
+    for (int i = 0; i < kIssues; ++i) {
+      const int r = first + row_of(i);
+      const int token = (int)fdiv((uint32_t)r, group), g = r - token * (int)group.d;
+      const bool in = r < rows && chunk[i] >= 0;
+      issue(from,
+            in ? (uint32_t)(token - token0) * row + (uint32_t)g * head + (uint32_t)chunk[i] : kOutside,
+            lds, i);
+    }
+  }
+};
+
+// Loads to LDS have landed, but for the wave's last LEFT; its LDS reads are done.
+template <int LEFT>
+__device__ __forceinline__ void landed() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LEFT) : "memory");
+}
+// ... and every wave's.
+template <int LEFT>
+__device__ __forceinline__ void all_landed() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+}
+
+// The value of the lane 32 further on (or back).
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+
+// Row of a result's register r in this half.
+__device__ __forceinline__ int row_in(int r, int half) { return 8 * (r >> 2) + 4 * half + (r & 3); }
+
+__device__ __forceinline__ float exp2_(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// Four consecutive values of a row.
+template <int FMT>
+__device__ __forceinline__ void store4(char *p, const float v[4]) {
+  if constexpr (FMT == kF32) {
+    *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    uint16_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = FMT == kBf16 ? dense::f_to_bf16(v[i]) : dense::f_to_f16(v[i]);
+    *(uint2 *)p = make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
+  }
+}
+
+// Columns of across() to memory: this lane's column is the row at `p`.
+template <class C, int FMT>
+__device__ __forceinline__ void store_columns(const f32x16 (&c)[C::kBlocks], char *p, int dim, int half,
+                                              float by) {
+#pragma unroll
+  for (int b = 0; b < C::kBlocks; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+      const int d = b * 32 + row_in(r, half);
+      const float v[4] = {c[b][r] * by, c[b][r + 1] * by, c[b][r + 2] * by, c[b][r + 3] * by};
+      if (d < dim) store4<FMT>(p + d * C::kSize, v);
+    }
+}
+
+__device__ __forceinline__ void clear(f32x16 &c) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) c[i] = 0.f;
+}
+
+// Launchers (attention_forward.hip, attention_backward.hip).
+constexpr int kLogWide = 7;  // 128 rows, or keys, to a workgroup
+constexpr int kLogFew = 5;   // 32
+hipError_t launch_forward(const Args &a, int fmt, hipStream_t st);
+hipError_t launch_forward_few(const Args &a, int fmt, hipStream_t st);
+hipError_t launch_delta(const Args &a, int fmt, long long tokens, int heads, hipStream_t st);
+hipError_t launch_backward_q(const Args &a, int fmt, hipStream_t st);
+hipError_t launch_backward_kv(const Args &a, int fmt, hipStream_t st);
+
+}  // namespace attend
+}  // namespace pdr

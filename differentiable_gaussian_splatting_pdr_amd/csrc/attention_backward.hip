@@ -1,0 +1,349 @@
+// attention_backward.hip -- the gradients of attention.
+//
+// Two kernels instead of one: the queries' gradients sum over keys, the keys'
+// over queries, and with a workgroup for each result nothing is added by
+// atomics, so a result does not depend on the run.  That costs seven products
+// where five would do.
+#include "attention.hpp"
+
+namespace pdr {
+namespace attend {
+
+namespace {
+
+// delta = dy . o of each row: 16 lanes to a row, 16 bytes each at a time.
+template <int FMT>
+__global__ __launch_bounds__(256) void k_delta(Args a, FastDiv heads, long long total) {
+  constexpr int kSize = FMT == kF32 ? 4 : 2, kPer = 16 / kSize;
+  const long long at = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int lane = threadIdx.x & 15;
+  if (at >= total) return;
+  const uint32_t token = fdiv((uint32_t)at, heads), head = (uint32_t)at - token * heads.d;
+  long long seq = 0, i = token;
+  if (!a.q_offsets) {
+    seq = token / (uint32_t)a.q_rows;
+    i = token - seq * a.q_rows;
+  }
+  const char *o = a.o.p + (seq * a.o.batch + i * a.o.row + head * a.o.head) * kSize;
+  const char *dy = a.dy.p + (seq * a.dy.batch + i * a.dy.row + head * a.dy.head) * kSize;
+  float s = 0.f;
+  for (int d = lane * kPer; d < a.dim; d += 16 * kPer) {
+    const i32x4 x = *(const i32x4 *)(o + d * kSize), y = *(const i32x4 *)(dy + d * kSize);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (FMT == kF32) {
+        s = fmaf(__int_as_float(x[j]), __int_as_float(y[j]), s);
+      } else {
+        s = fmaf(dense::to_f<FMT>((uint16_t)x[j]), dense::to_f<FMT>((uint16_t)y[j]), s);
+        s = fmaf(dense::to_f<FMT>((uint16_t)((uint32_t)x[j] >> 16)),
+                 dense::to_f<FMT>((uint16_t)((uint32_t)y[j] >> 16)), s);
+      }
+    }
+  }
+#pragma unroll
+  for (int w = 8; w > 0; w >>= 1) s += __shfl_xor(s, w);
+  const uint32_t kv = fdiv(head, a.group), g = head - kv * a.group.d;
+  const long long tokens = total / heads.d;
+  if (lane == 0) a.delta[(kv * tokens + token) * a.group.d + g] = s;
+}
+
+// Weights and score gradients enter the products in the operands' type.  In fp16
+// they would leave its range: p is taken times 2^15, and ds under a power of two
+// for each column of the result, found from the largest value that the column
+// has met (both are taken out of the sums again).
+template <class C, int FMT>
+struct Scaled {
+  int e;  // ds is taken times 2^e
+  __device__ __forceinline__ void init() { e = 100; }
+  __device__ __forceinline__ void hold(f32x16 &ds, f32x16 (&sums)[C::kBlocks]) {
+    if constexpr (FMT == kF16) {
+      float m = 0.f;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) m = fmaxf(m, fabsf(ds[r]));
+      m = fmaxf(m, other_half(m));
+      // m 2^e < 2^15 is held
+      const int most = m > 0.f ? 15 - __builtin_amdgcn_frexp_expf(m) : 100;
+      if (__any(most < e)) {
+        // leave room for four times as much
+        int to = most - 2 < -120 ? -120 : most - 2;
+        if (most >= e) to = e;
+        const float by = ldexpf(1.f, to - e < -250 ? -250 : to - e);
+#pragma unroll
+        for (int b = 0; b < C::kBlocks; ++b)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) sums[b][r] *= by;
+        e = to;
+      }
+      const float by = ldexpf(1.f, e);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) ds[r] *= by;
+    }
+  }
+  // What the sums are to be multiplied by.
+  __device__ __forceinline__ float out() const { return FMT == kF16 ? ldexpf(1.f, -e) : 1.f; }
+};
+
+template <class C>
+__device__ __forceinline__ void across32(f32x16 (&c)[C::kBlocks], const char *tile, int row0,
+                                         const f32x16 &w, int lane) {
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    float p[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) p[r] = w[x * 8 + r];
+    C::across(c, tile, row0 + x * 16, p, lane);
+  }
+}
+
+// dq: 128 rows to a workgroup, 32 to a wave, as in the forward.
+template <int FMT, int DP>
+__global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  using C = Core<FMT, DP>;
+  constexpr int kKeys = 64;
+  using L = Loader<C, kKeys, 4>;
+  __shared__ __align__(1024) char smem[4 * L::kBytes];
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int unit = (int)fdiv(blockIdx.x, a.heads), head = blockIdx.x - unit * a.kv_heads;
+  const Place at = place<kLogWide, false>(a, a.causal ? a.q_tiles - 1 - unit : unit);
+  const int group = (int)a.group.d, rows = at.nq * group;
+  const int row0 = at.tile << kLogWide;
+  if (at.tile < 0 || row0 >= rows) return;
+  const int row = row0 + wave * 32 + (lane & 31);
+  const bool there = row < rows;
+  const int token = (int)fdiv((uint32_t)(there ? row : rows - 1), a.group);
+  const int in_group = there ? row - token * group : 0;
+  const int ahead = at.nk - at.nq;
+  const int seen = !a.causal ? at.nk : token + ahead + 1 < at.nk ? token + ahead + 1 : at.nk;
+  int keys = at.nk;
+  if (a.causal) {
+    const int last = row0 + 127 < rows ? row0 + 127 : rows - 1;
+    const int k = (int)fdiv((uint32_t)last, a.group) + ahead + 1;
+    keys = k < 0 ? 0 : k;
+  }
+  const int first_row = row0 + wave * 32 < rows ? row0 + wave * 32 : rows - 1;
+  const int plain = !a.causal ? at.nk : (int)fdiv((uint32_t)first_row, a.group) + ahead + 1;
+
+  i32x4 q[C::kSteps], dy[C::kSteps];
+  C::fetch_row(q, a.q.p + (first_of(a.q, at, at.q0 + token, head * group) + in_group * a.q.head) * C::kSize,
+               a.dim, half, there);
+  C::fetch_row(dy, a.dy.p + (first_of(a.dy, at, at.q0 + token, head * group) + in_group * a.dy.head) * C::kSize,
+               a.dim, half, there);
+  float lse = INFINITY, delta = 0.f;
+  if (there) {
+    const long long tokens = a.q_offsets ? a.q_rows : (long long)a.batch * a.q_rows;
+    const long long i =
+        (head * tokens + (a.q_offsets ? 0 : (long long)at.seq * a.q_rows) + at.q0) * group + row;
+    lse = a.lse[i];
+    delta = a.delta[i];
+  }
+  f32x16 sums[C::kBlocks];
+#pragma unroll
+  for (int b = 0; b < C::kBlocks; ++b) clear(sums[b]);
+  Scaled<C, FMT> scaled;
+  scaled.init();
+  L lk, lv;
+  lk.init(a.k, first_of(a.k, at, at.k0, head), a.dim, wave, lane);
+  lv.init(a.v, first_of(a.v, at, at.k0, head), a.dim, wave, lane);
+  const int tiles = (keys + kKeys - 1) / kKeys;
+  if (tiles > 0) {
+    lk.tokens(0, at.nk, smem);
+    lv.tokens(0, at.nk, smem + L::kBytes);
+  }
+  for (int t = 0; t < tiles; ++t) {
+    char *const sk = smem + (t & 1) * (2 * L::kBytes), *const sv = sk + L::kBytes;
+    all_landed<0>();
+    if (t + 1 < tiles) {
+      char *const next = smem + ((t + 1) & 1) * (2 * L::kBytes);
+      lk.tokens((t + 1) * kKeys, at.nk, next);
+      lv.tokens((t + 1) * kKeys, at.nk, next + L::kBytes);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      f32x16 s, dp;
+      clear(s);
+      clear(dp);
+      C::along(s, sk, u * 32, q, lane);
+      C::along(dp, sv, u * 32, dy, lane);
+      const int key0 = t * kKeys + u * 32;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float p = exp2_(fmaf(s[r], a.scale2, -lse));
+        s[r] = p * (dp[r] - delta);
+      }
+      if (key0 + 32 > plain) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (key0 + row_in(r, half) >= seen) s[r] = 0.f;
+      }
+      scaled.hold(s, sums);
+      across32<C>(sums, sk, u * 32, s, lane);
+    }
+  }
+  if (!there) return;
+  store_columns<C, FMT>(sums,
+                        a.dq.p + (first_of(a.dq, at, at.q0 + token, head * group) + in_group * a.dq.head) * C::kSize,
+                        a.dim, half, lse == INFINITY ? 0.f : a.scale * scaled.out());
+#endif
+}
+
+// dk and dv: 128 keys to a workgroup, 32 to a wave; the waves share tiles of
+// rows (of all heads that read these keys), and of their lse and delta.
+template <int FMT, int DP>
+__global__ __launch_bounds__(256, 1) void k_backward_kv(Args a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  using C = Core<FMT, DP>;
+  constexpr int kRows = 64;
+  using L = Loader<C, kRows, 4>;
+  constexpr int kStage = 2 * L::kBytes + 2 * kRows * 4;
+  __shared__ __align__(1024) char smem[2 * kStage];
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int unit = (int)fdiv(blockIdx.x, a.heads), head = blockIdx.x - unit * a.kv_heads;
+  const Place at = place<kLogWide, true>(a, unit);
+  const int group = (int)a.group.d, rows = at.nq * group;
+  const int key0 = at.tile << kLogWide;
+  if (at.tile < 0 || key0 >= at.stored) return;
+  const int key = key0 + wave * 32 + (lane & 31);
+  const bool there = key < at.nk;
+  const int ahead = at.nk - at.nq;
+  // the first row that sees a key; none sees what is no key
+  auto first_row = [&](int k) {
+    if (k >= at.nk) return rows;
+    const long long r = a.causal ? (long long)(k - ahead) * group : 0;
+    return r < 0 ? 0 : r > rows ? rows : (int)r;
+  };
+  const int from = first_row(key);
+  const int plain = first_row(key0 + wave * 32 + 31);  // from here on the wave needs no mask
+  const int end = key0 < at.nk ? (rows + kRows - 1) / kRows : 0;
+  const int begin = first_row(key0) / kRows;
+
+  i32x4 k[C::kSteps], v[C::kSteps];
+  C::fetch_row(k, a.k.p + first_of(a.k, at, at.k0 + (there ? key : 0), head) * C::kSize, a.dim, half, there);
+  C::fetch_row(v, a.v.p + first_of(a.v, at, at.k0 + (there ? key : 0), head) * C::kSize, a.dim, half, there);
+  f32x16 dk[C::kBlocks], dv[C::kBlocks];
+#pragma unroll
+  for (int b = 0; b < C::kBlocks; ++b) {
+    clear(dk[b]);
+    clear(dv[b]);
+  }
+  Scaled<C, FMT> scaled;
+  scaled.init();
+  L lq, ly;
+  lq.init(a.q, first_of(a.q, at, at.q0, head * group), a.dim, wave, lane);
+  ly.init(a.dy, first_of(a.dy, at, at.q0, head * group), a.dim, wave, lane);
+  const long long tokens = a.q_offsets ? a.q_rows : (long long)a.batch * a.q_rows;
+  const long long first =
+      (head * tokens + (a.q_offsets ? 0 : (long long)at.seq * a.q_rows) + at.q0) * group;
+  auto load = [&](int t, char *stage) {
+    lq.grouped(t * kRows, rows, a.group, stage);
+    ly.grouped(t * kRows, rows, a.group, stage + L::kBytes);
+    const float *src = wave == 0 ? a.lse : a.delta;  // one wave each
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc((void *)(src + first + t * kRows), 0, kRows * 4, 0x00020000);
+    if (wave < 2)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, (lds_void *)(stage + 2 * L::kBytes + wave * (kRows * 4)), 4,
+          t * kRows + lane < rows ? lane * 4 : (int)kOutside, 0, 0, 0);
+  };
+  if (begin < end) load(begin, smem);
+  for (int t = begin; t < end; ++t) {
+    char *const sq = smem + ((t - begin) & 1) * kStage, *const sy = sq + L::kBytes;
+    const float *const stats = (const float *)(sq + 2 * L::kBytes);
+    all_landed<0>();
+    if (t + 1 < end) load(t + 1, smem + ((t + 1 - begin) & 1) * kStage);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      f32x16 s, dp;
+      clear(s);
+      clear(dp);
+      C::along(s, sq, u * 32, k, lane);
+      C::along(dp, sy, u * 32, v, lane);
+      const int r0 = t * kRows + u * 32;
+      const bool masked = r0 < plain || r0 + 32 > rows;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int i = u * 32 + row_in(r, half);
+        float p = exp2_(fmaf(s[r], a.scale2, -stats[i]));
+        float ds = p * (dp[r] - stats[kRows + i]);
+        if (masked) {
+          const int n = t * kRows + i;
+          const bool in = n >= from && n < rows;
+          p = in ? p : 0.f;
+          ds = in ? ds : 0.f;
+        }
+        s[r] = FMT == kF16 ? p * 32768.f : p;
+        dp[r] = ds;
+      }
+      across32<C>(dv, sy, u * 32, s, lane);
+      scaled.hold(dp, dk);
+      across32<C>(dk, sq, u * 32, dp, lane);
+    }
+  }
+  if (key >= at.stored) return;
+  const long long where = at.k0 + key;
+  store_columns<C, FMT>(dk, a.dk.p + (at.seq * a.dk.batch + where * a.dk.row + head * a.dk.head) * C::kSize,
+                        a.dim, half, there ? a.scale * scaled.out() : 0.f);
+  store_columns<C, FMT>(dv, a.dv.p + (at.seq * a.dv.batch + where * a.dv.row + head * a.dv.head) * C::kSize,
+                        a.dim, half, there ? (FMT == kF16 ? 1.f / 32768.f : 1.f) : 0.f);
+#endif
+}
+
+template <int FMT>
+void go_q(const Args &a, hipStream_t st) {
+  const dim3 grid((unsigned)a.q_tiles * a.kv_heads);
+  if (a.dim <= 64)
+    hipLaunchKernelGGL((k_backward_q<FMT, 64>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_backward_q<FMT, 128>), grid, dim3(256), 0, st, a);
+}
+template <int FMT>
+void go_kv(const Args &a, hipStream_t st) {
+  const dim3 grid((unsigned)a.k_tiles * a.kv_heads);
+  if (a.dim <= 64)
+    hipLaunchKernelGGL((k_backward_kv<FMT, 64>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_backward_kv<FMT, 128>), grid, dim3(256), 0, st, a);
+}
+
+}  // namespace
+
+hipError_t launch_delta(const Args &a, int fmt, long long tokens, int heads, hipStream_t st) {
+  const long long total = tokens * heads;
+  if (!total) return hipSuccess;
+  const dim3 grid((unsigned)((total + 15) / 16));
+  const FastDiv div = make_fastdiv((uint32_t)heads);
+  if (fmt == kBf16)
+    hipLaunchKernelGGL(k_delta<kBf16>, grid, dim3(256), 0, st, a, div, total);
+  else if (fmt == kF16)
+    hipLaunchKernelGGL(k_delta<kF16>, grid, dim3(256), 0, st, a, div, total);
+  else
+    hipLaunchKernelGGL(k_delta<kF32>, grid, dim3(256), 0, st, a, div, total);
+  return hipGetLastError();
+}
+
+hipError_t launch_backward_q(const Args &a, int fmt, hipStream_t st) {
+  if (!a.q_tiles || !a.kv_heads) return hipSuccess;
+  if (fmt == kBf16)
+    go_q<kBf16>(a, st);
+  else if (fmt == kF16)
+    go_q<kF16>(a, st);
+  else
+    go_q<kF32>(a, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_backward_kv(const Args &a, int fmt, hipStream_t st) {
+  if (!a.k_tiles || !a.kv_heads) return hipSuccess;
+  if (fmt == kBf16)
+    go_kv<kBf16>(a, st);
+  else if (fmt == kF16)
+    go_kv<kF16>(a, st);
+  else
+    go_kv<kF32>(a, st);
+  return hipGetLastError();
+}
+
+}  // namespace attend
+}  // namespace pdr
