@@ -56,7 +56,8 @@ struct Mat {
 struct Args {
   Mat q, k, v, o, dy, dq, dk, dv;
   const int *q_offsets, *k_offsets, *key_lengths;
-  float *lse, *delta;
+  float *lse;
+  float *start_s, *start_dp;  // backward: what scores and their gradients' products start from, as lse
   float *part_o, *part_ml;  // few queries: the splits' sums, and their maxima and weights
   float scale, scale2;      // scale, and scale log2(e)
   int causal, batch, kv_heads, dim, q_rows, k_rows;
@@ -197,58 +198,88 @@ struct Core {
     }
   }
 
-  static __device__ __forceinline__ void along(f32x16 &c, const char *tile, int row0,
-                                               const i32x4 (&reg)[kSteps], int lane) {
-    const int r = row0 + (lane & 31), half = lane >> 5, sw = swizzle(r);
-    const lds_char *p = (const lds_char *)tile + r * kRowBytes;
+  // Where a lane reads in a tile whose first row is a multiple of 16 of LDS rows.
+  // A chunk's low three bits are turned by the swizzle, and the rest of its place
+  // is the same for all lanes: few addresses serve all of a tile's reads, with
+  // offsets known when the kernel is compiled.
+  static constexpr int kAcross = FMT == kF32 ? 4 : 2;
+  struct Lane {
+    int rows[4];            // along(): of steps s % 4
+    int columns[kAcross];   // across(): of blocks b % 2, or rows e % 4
+    __device__ __forceinline__ void init(int lane) {
+      const int half = lane >> 5, r = lane & 31;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) rows[s] = r * kRowBytes + (((2 * s + half) ^ swizzle(r)) << 4);
+      if constexpr (FMT != kF32) {
+        const int t = lane & 15, k = 4 * half + (t >> 2);
+        const int c = ((lane >> 4) & 1) * 2 + ((t & 3) >> 1);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          columns[b] = k * kRowBytes + (((b * 4 + c) ^ swizzle(k)) << 4) + (t & 1) * 8;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = 4 * half + e;
+          columns[e] = k * kRowBytes + (((r >> 2) ^ swizzle(k)) << 4) + (r & 3) * 4;
+        }
+      }
+    }
+  };
+
+  // Rows 32 U .. 32 U + 31 of the tile.
+  static __device__ __forceinline__ void along(f32x16 &c, const char *tile, int u,
+                                               const i32x4 (&reg)[kSteps], const Lane &at) {
+    const lds_char *p = (const lds_char *)tile;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      const i32x4 a =
-          *(const __attribute__((address_space(3))) i32x4 *)(p + (((2 * s + half) ^ sw) << 4));
+      const i32x4 a = *(const __attribute__((address_space(3))) i32x4 *)(p + at.rows[s & 3] + (s >> 2) * 128 +
+                                                                         u * 32 * kRowBytes);
       c = go(a, reg[s], c);
     }
   }
 
-  // Sixteen rows from row0 on, whose weights are 8 registers of an along().
-  static __device__ __forceinline__ void across(f32x16 (&c)[kBlocks], const char *tile, int row0,
-                                                const float *p, int lane) {
-    const int half = lane >> 5;
-    if constexpr (FMT != kF32) {
-      typedef float f32x2 __attribute__((ext_vector_type(2)));
-      typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-      typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-      i32x4 w;
+  // Eight registers of an along() as the second operand of across().
+  struct Weights {
+    i32x4 w[FMT == kF32 ? 2 : 1];
+  };
+  static __device__ __forceinline__ Weights pack(const f32x16 &v, int first) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    Weights o;
+    if constexpr (FMT == kF32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o.w[i >> 2][i & 3] = __float_as_int(v[first + i]);
+    } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const f32x2 two = {p[2 * i], p[2 * i + 1]};
-        w[i] = FMT == kBf16 ? __builtin_bit_cast(int, __builtin_convertvector(two, b2))
-                            : __builtin_bit_cast(int, __builtin_convertvector(two, h2));
+        const f32x2 two = {v[first + 2 * i], v[first + 2 * i + 1]};
+        o.w[0][i] = FMT == kBf16 ? __builtin_bit_cast(int, __builtin_convertvector(two, b2))
+                                 : __builtin_bit_cast(int, __builtin_convertvector(two, h2));
       }
-      const int t = lane & 15, r = row0 + 4 * half + (t >> 2);
-      const int c0 = ((lane >> 4) & 1) * 2 + ((t & 3) >> 1), byte = (t & 1) * 8;
-      const lds_char *lo = (const lds_char *)tile + r * kRowBytes + byte;
-      const lds_char *hi = lo + 8 * kRowBytes;
-      const int sl = swizzle(r), sh = swizzle(r + 8);
+    }
+    return o;
+  }
+  // Rows 16 X .. 16 X + 15 of the tile under these weights.
+  static __device__ __forceinline__ void across(f32x16 (&c)[kBlocks], const char *tile, int x,
+                                                const Weights &p, const Lane &at) {
+    const lds_char *first = (const lds_char *)tile + x * 16 * kRowBytes;
+    if constexpr (FMT != kF32) {
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
-        const s16x4 x = transposed((lds_s16x4 *)(lo + (((b * 4 + c0) ^ sl) << 4)));
-        const s16x4 y = transposed((lds_s16x4 *)(hi + (((b * 4 + c0) ^ sh) << 4)));
-        const s16x8 f = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-        c[b] = go(__builtin_bit_cast(i32x4, f), w, c[b]);
+        const lds_char *lo = first + at.columns[b & 1] + (b >> 1) * 128;
+        const s16x4 y = transposed((lds_s16x4 *)lo), z = transposed((lds_s16x4 *)(lo + 8 * kRowBytes));
+        c[b] = go(__builtin_bit_cast(i32x4, __builtin_shufflevector(y, z, 0, 1, 2, 3, 4, 5, 6, 7)), p.w[0], c[b]);
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int r = row0 + 8 * (e >> 2) + 4 * half + (e & 3);
-        const int d = lane & 31;
-        const lds_char *at = (const lds_char *)tile + r * kRowBytes + (d & 3) * 4;
+      for (int e = 0; e < 8; ++e)
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
           const float f = *(const __attribute__((address_space(3))) float *)(
-              at + (((b * 8 + (d >> 2)) ^ swizzle(r)) << 4));
-          c[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(f, p[e], c[b], 0, 0, 0);
+              first + at.columns[e & 3] + (e >> 2) * 8 * kRowBytes + b * 128);
+          c[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(f, __int_as_float(p.w[e >> 2][e & 3]), c[b], 0, 0, 0);
         }
-      }
     }
   }
   // ds_read_b64_tr_b16: of each 16 lanes' 4 rows of 16 values (a row is four
@@ -260,33 +291,34 @@ struct Core {
 };
 
 // Copies tiles of ROWS rows to LDS (loads straight to LDS, zeros for rows that
-// do not exist and past dim), by NW waves.  Rows are keys (row apart), or the
-// rows of a group of heads.
+// do not exist and past dim), by NW waves.
+struct Source {
+  const char *base;    // first token of the sequence, this head
+  uint32_t row, head;  // bytes
+  __device__ __forceinline__ Source(const Mat &m, long long first, int size)
+      : base(m.p + first * size), row((uint32_t)(m.row * size)), head((uint32_t)(m.head * size)) {}
+};
 template <class C, int ROWS, int NW>
 struct Loader {
   static constexpr int kBytes = ROWS * C::kRowBytes;
   static constexpr int kIssues = kBytes / (NW * 1024);
   static constexpr int kRowsEach = 1024 / C::kRowBytes;  // rows of one wave's load
   static_assert(kBytes % (NW * 1024) == 0 && kRowsEach * C::kRowBytes == 1024, "whole loads");
-  const char *base;   // first token of the sequence, this head
-  uint32_t row, head; // bytes
-  int chunk[kIssues]; // byte of this lane's chunk in its row, or kOutside
-  int wave, lane;
+  int wave, dim;
+  int row0, chunk0;  // this lane's row and chunk in the first load
 
-  __device__ __forceinline__ void init(const Mat &m, long long first, int dim, int wave_, int lane_) {
+  __device__ __forceinline__ void init(int dim_, int wave_, int lane) {
     wave = wave_;
-    lane = lane_;
-    base = m.p + first * C::kSize;
-    row = (uint32_t)(m.row * C::kSize);
-    head = (uint32_t)(m.head * C::kSize);
-#pragma unroll
-    for (int i = 0; i < kIssues; ++i) {
-      const int c = (lane % C::kChunks) ^ C::swizzle(row_of(i));
-      chunk[i] = c * C::kPer < dim ? c * 16 : (int)kOutside;
-    }
+    dim = dim_;
+    row0 = wave * kRowsEach + lane / C::kChunks;
+    chunk0 = (lane % C::kChunks) ^ C::swizzle(row0);
   }
-  __device__ __forceinline__ int row_of(int i) const {
-    return (i * NW + wave) * kRowsEach + lane / C::kChunks;
+  // The i-th load's row, and its byte in the row or kOutside.  The rows between
+  // two loads are a power of two that row0 stays below, so their swizzles add up.
+  __device__ __forceinline__ int row_of(int i) const { return row0 + i * NW * kRowsEach; }
+  __device__ __forceinline__ uint32_t byte_of(int i) const {
+    const int c = chunk0 ^ C::swizzle(i * NW * kRowsEach);
+    return c * C::kPer < dim ? (uint32_t)c * 16u : kOutside;
   }
   __device__ __forceinline__ void issue(const char *from, uint32_t off, char *lds, int i) const {
     const __amdgpu_buffer_rsrc_t rsrc =
@@ -294,28 +326,31 @@ struct Loader {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(lds + (i * NW + wave) * 1024), 16,
                                              (int)off, 0, 0, 0);
   }
-  // Rows [first, first + ROWS) of `rows`.
-  __device__ __forceinline__ void tokens(int first, int rows, char *lds) const {
-    const char *from = base + (long long)first * row;
+  // Rows [first, first + ROWS) of `rows`, of two tensors.
+  __device__ __forceinline__ void tokens(const Source &x, const Source &y, int first, int rows, char *lds) const {
+    const char *const from_x = x.base + (long long)first * x.row;
+    const char *const from_y = y.base + (long long)first * y.row;
 #pragma unroll
     for (int i = 0; i < kIssues; ++i) {
-      const int r = row_of(i);
-      const bool in = first + r < rows && chunk[i] >= 0;
-      issue(from, in ? (uint32_t)r * row + (uint32_t)chunk[i] : kOutside, lds, i);
+      const uint32_t r = (uint32_t)row_of(i), c = byte_of(i);
+      const bool in = first + (int)r < rows && c != kOutside;
+      issue(from_x, in ? r * x.row + c : kOutside, lds, i);
+      issue(from_y, in ? r * y.row + c : kOutside, lds + kBytes, i);
     }
   }
-  // The same of rows in groups.
-  __device__ __forceinline__ void grouped(int first, int rows, const FastDiv &group, char *lds) const {
+  // The same of a group's rows.
+  __device__ __forceinline__ void grouped(const Source &x, const Source &y, int first, int rows,
+                                          const FastDiv &group, char *lds) const {
     const int token0 = (int)fdiv((uint32_t)first, group);
-    const char *from = base + (long long)token0 * row;
+    const char *const from_x = x.base + (long long)token0 * x.row;
+    const char *const from_y = y.base + (long long)token0 * y.row;
 #pragma unroll
     for (int i = 0; i < kIssues; ++i) {
       const int r = first + row_of(i);
-      const int token = (int)fdiv((uint32_t)r, group), g = r - token * (int)group.d;
-      const bool in = r < rows && chunk[i] >= 0;
-      issue(from,
-            in ? (uint32_t)(token - token0) * row + (uint32_t)g * head + (uint32_t)chunk[i] : kOutside,
-            lds, i);
+      const uint32_t c = byte_of(i), token = fdiv((uint32_t)r, group), g = (uint32_t)r - token * group.d;
+      const bool in = r < rows && c != kOutside;
+      issue(from_x, in ? (token - token0) * x.row + g * x.head + c : kOutside, lds, i);
+      issue(from_y, in ? (token - token0) * y.row + g * y.head + c : kOutside, lds + kBytes, i);
     }
   }
 };
@@ -333,6 +368,13 @@ __device__ __forceinline__ void all_landed() {
 
 // The value of the lane 32 further on (or back).
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+
+// The same value, in a branch that few tiles take: what follows from it is not
+// worked out before the branch, where every tile would pay for it.
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
 
 // Row of a result's register r in this half.
 __device__ __forceinline__ int row_in(int r, int half) { return 8 * (r >> 2) + 4 * half + (r & 3); }
@@ -366,17 +408,18 @@ __device__ __forceinline__ void store_columns(const f32x16 (&c)[C::kBlocks], cha
     }
 }
 
-__device__ __forceinline__ void clear(f32x16 &c) {
+__device__ __forceinline__ void fill(f32x16 &c, float v) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) c[i] = 0.f;
+  for (int i = 0; i < 16; ++i) c[i] = v;
 }
+__device__ __forceinline__ void clear(f32x16 &c) { fill(c, 0.f); }
 
 // Launchers (attention_forward.hip, attention_backward.hip).
 constexpr int kLogWide = 7;  // 128 rows, or keys, to a workgroup
 constexpr int kLogFew = 5;   // 32
 hipError_t launch_forward(const Args &a, int fmt, hipStream_t st);
 hipError_t launch_forward_few(const Args &a, int fmt, hipStream_t st);
-hipError_t launch_delta(const Args &a, int fmt, long long tokens, int heads, hipStream_t st);
+hipError_t launch_starts(const Args &a, int fmt, long long tokens, int heads, hipStream_t st);
 hipError_t launch_backward_q(const Args &a, int fmt, hipStream_t st);
 hipError_t launch_backward_kv(const Args &a, int fmt, hipStream_t st);
 

@@ -11,9 +11,19 @@ namespace attend {
 
 namespace {
 
-// delta = dy . o of each row: 16 lanes to a row, 16 bytes each at a time.
+// Weights and score gradients.  With sums that start from
+//   start_s = -lse / scale2,  start_dp = -(dy . o)
+// the products leave s - lse and dp - delta, and
+//   p = exp2(scale2 s),  ds = p dp
+// are an exponential and two products a pair.  fp32 scores start from 0, and take
+// lse in the exponent: what rounding at lse's magnitude costs them shows (2e-6
+// instead of 8e-7 of a gradient).  In fp16 p is taken times 2^15, which keeps
+// long rows' weights in the type's range.
+constexpr int kShift = 15;
+
+// The starts of each row: 16 lanes to a row, 16 bytes each at a time.
 template <int FMT>
-__global__ __launch_bounds__(256) void k_delta(Args a, FastDiv heads, long long total) {
+__global__ __launch_bounds__(256) void k_starts(Args a, FastDiv heads, long long total) {
   constexpr int kSize = FMT == kF32 ? 4 : 2, kPer = 16 / kSize;
   const long long at = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
   const int lane = threadIdx.x & 15;
@@ -44,13 +54,25 @@ __global__ __launch_bounds__(256) void k_delta(Args a, FastDiv heads, long long 
   for (int w = 8; w > 0; w >>= 1) s += __shfl_xor(s, w);
   const uint32_t kv = fdiv(head, a.group), g = head - kv * a.group.d;
   const long long tokens = total / heads.d;
-  if (lane == 0) a.delta[(kv * tokens + token) * a.group.d + g] = s;
+  if (lane == 0) {
+    const long long to = (kv * tokens + token) * a.group.d + g;
+    const float lse = a.lse[to];
+    a.start_dp[to] = -s;
+    a.start_s[to] = FMT == kF32 ? -lse : ((FMT == kF16 ? kShift : 0) - lse) / a.scale2;
+  }
 }
 
-// Weights and score gradients enter the products in the operands' type.  In fp16
-// they would leave its range: p is taken times 2^15, and ds under a power of two
-// for each column of the result, found from the largest value that the column
-// has met (both are taken out of the sums again).
+// A tile's weights from its scores, and their gradients, in place.  `start`: of the
+// scores in fp32.
+template <int FMT>
+__device__ __forceinline__ void weigh(float &s, float &dp, float start, float scale2) {
+  s = exp2_(FMT == kF32 ? fmaf(s, scale2, start) : s * scale2);
+  dp *= s;
+}
+
+// ds enters the products in the operands' type.  In fp16 it would leave its range:
+// it is taken times a power of two for each column of the result, found from the
+// largest value that the column has met.
 template <class C, int FMT>
 struct Scaled {
   int e;  // ds is taken times 2^e
@@ -80,19 +102,14 @@ struct Scaled {
     }
   }
   // What the sums are to be multiplied by.
-  __device__ __forceinline__ float out() const { return FMT == kF16 ? ldexpf(1.f, -e) : 1.f; }
+  __device__ __forceinline__ float out() const { return FMT == kF16 ? ldexpf(1.f, -e - kShift) : 1.f; }
 };
 
 template <class C>
-__device__ __forceinline__ void across32(f32x16 (&c)[C::kBlocks], const char *tile, int row0,
-                                         const f32x16 &w, int lane) {
+__device__ __forceinline__ void across32(f32x16 (&c)[C::kBlocks], const char *tile, int u,
+                                         const f32x16 &w, const typename C::Lane &at) {
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    float p[8];
-#pragma unroll
-    for (int r = 0; r < 8; ++r) p[r] = w[x * 8 + r];
-    C::across(c, tile, row0 + x * 16, p, lane);
-  }
+  for (int x = 0; x < 2; ++x) C::across(c, tile, 2 * u + x, C::pack(w, 8 * x), at);
 }
 
 // dq: 128 rows to a workgroup, 32 to a wave, as in the forward.
@@ -130,68 +147,70 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
                a.dim, half, there);
   C::fetch_row(dy, a.dy.p + (first_of(a.dy, at, at.q0 + token, head * group) + in_group * a.dy.head) * C::kSize,
                a.dim, half, there);
-  float lse = INFINITY, delta = 0.f;
+  float start_s = 0.f, start_dp = 0.f;
   if (there) {
     const long long tokens = a.q_offsets ? a.q_rows : (long long)a.batch * a.q_rows;
     const long long i =
         (head * tokens + (a.q_offsets ? 0 : (long long)at.seq * a.q_rows) + at.q0) * group + row;
-    lse = a.lse[i];
-    delta = a.delta[i];
+    start_s = a.start_s[i];
+    start_dp = a.start_dp[i];
   }
   f32x16 sums[C::kBlocks];
 #pragma unroll
   for (int b = 0; b < C::kBlocks; ++b) clear(sums[b]);
+  typename C::Lane lanes;
+  lanes.init(lane);
   Scaled<C, FMT> scaled;
   scaled.init();
-  L lk, lv;
-  lk.init(a.k, first_of(a.k, at, at.k0, head), a.dim, wave, lane);
-  lv.init(a.v, first_of(a.v, at, at.k0, head), a.dim, wave, lane);
+  const Source k(a.k, first_of(a.k, at, at.k0, head), C::kSize), v(a.v, first_of(a.v, at, at.k0, head), C::kSize);
+  L load;
+  load.init(a.dim, wave, lane);
   const int tiles = (keys + kKeys - 1) / kKeys;
   if (tiles > 0) {
-    lk.tokens(0, at.nk, smem);
-    lv.tokens(0, at.nk, smem + L::kBytes);
+    load.tokens(k, v, 0, at.nk, smem);
   }
   for (int t = 0; t < tiles; ++t) {
     char *const sk = smem + (t & 1) * (2 * L::kBytes), *const sv = sk + L::kBytes;
     all_landed<0>();
     if (t + 1 < tiles) {
       char *const next = smem + ((t + 1) & 1) * (2 * L::kBytes);
-      lk.tokens((t + 1) * kKeys, at.nk, next);
-      lv.tokens((t + 1) * kKeys, at.nk, next + L::kBytes);
+      load.tokens(k, v, (t + 1) * kKeys, at.nk, next);
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       f32x16 s, dp;
-      clear(s);
-      clear(dp);
-      C::along(s, sk, u * 32, q, lane);
-      C::along(dp, sv, u * 32, dy, lane);
+      fill(s, FMT == kF32 ? 0.f : start_s);
+      fill(dp, start_dp);
+      C::along(s, sk, u, q, lanes);
+      C::along(dp, sv, u, dy, lanes);
       const int key0 = t * kKeys + u * 32;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const float p = exp2_(fmaf(s[r], a.scale2, -lse));
-        s[r] = p * (dp[r] - delta);
+        float p = s[r], ds = dp[r];
+        weigh<FMT>(p, ds, start_s, a.scale2);
+        s[r] = ds;
       }
       if (key0 + 32 > plain) {
+        const int last = here(seen - key0 - 4 * half);
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          if (key0 + row_in(r, half) >= seen) s[r] = 0.f;
+          if (row_in(r, 0) >= last) s[r] = 0.f;
       }
       scaled.hold(s, sums);
-      across32<C>(sums, sk, u * 32, s, lane);
+      across32<C>(sums, sk, u, s, lanes);
     }
   }
   if (!there) return;
   store_columns<C, FMT>(sums,
                         a.dq.p + (first_of(a.dq, at, at.q0 + token, head * group) + in_group * a.dq.head) * C::kSize,
-                        a.dim, half, lse == INFINITY ? 0.f : a.scale * scaled.out());
+                        a.dim, half, a.scale * scaled.out());
 #endif
 }
 
 // dk and dv: 128 keys to a workgroup, 32 to a wave; the waves share tiles of
-// rows (of all heads that read these keys), and of their lse and delta.
+// rows (of all heads that read these keys), and of their starts.
 template <int FMT, int DP>
-__global__ __launch_bounds__(256, 1) void k_backward_kv(Args a) {
+__global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_kv(Args a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using C = Core<FMT, DP>;
   constexpr int kRows = 64;
@@ -228,18 +247,20 @@ __global__ __launch_bounds__(256, 1) void k_backward_kv(Args a) {
     clear(dk[b]);
     clear(dv[b]);
   }
+  typename C::Lane lanes;
+  lanes.init(lane);
   Scaled<C, FMT> scaled;
   scaled.init();
-  L lq, ly;
-  lq.init(a.q, first_of(a.q, at, at.q0, head * group), a.dim, wave, lane);
-  ly.init(a.dy, first_of(a.dy, at, at.q0, head * group), a.dim, wave, lane);
+  const Source from_q(a.q, first_of(a.q, at, at.q0, head * group), C::kSize);
+  const Source from_dy(a.dy, first_of(a.dy, at, at.q0, head * group), C::kSize);
+  L loader;
+  loader.init(a.dim, wave, lane);
   const long long tokens = a.q_offsets ? a.q_rows : (long long)a.batch * a.q_rows;
   const long long first =
       (head * tokens + (a.q_offsets ? 0 : (long long)at.seq * a.q_rows) + at.q0) * group;
   auto load = [&](int t, char *stage) {
-    lq.grouped(t * kRows, rows, a.group, stage);
-    ly.grouped(t * kRows, rows, a.group, stage + L::kBytes);
-    const float *src = wave == 0 ? a.lse : a.delta;  // one wave each
+    loader.grouped(from_q, from_dy, t * kRows, rows, a.group, stage);
+    const float *src = wave == 0 ? a.start_s : a.start_dp;  // one wave each
     const __amdgpu_buffer_rsrc_t rsrc =
         __builtin_amdgcn_make_buffer_rsrc((void *)(src + first + t * kRows), 0, kRows * 4, 0x00020000);
     if (wave < 2)
@@ -256,29 +277,32 @@ __global__ __launch_bounds__(256, 1) void k_backward_kv(Args a) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       f32x16 s, dp;
-      clear(s);
-      clear(dp);
-      C::along(s, sq, u * 32, k, lane);
-      C::along(dp, sy, u * 32, v, lane);
-      const int r0 = t * kRows + u * 32;
-      const bool masked = r0 < plain || r0 + 32 > rows;
+      float start[16];
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int i = u * 32 + row_in(r, half);
-        float p = exp2_(fmaf(s[r], a.scale2, -stats[i]));
-        float ds = p * (dp[r] - stats[kRows + i]);
-        if (masked) {
-          const int n = t * kRows + i;
-          const bool in = n >= from && n < rows;
-          p = in ? p : 0.f;
-          ds = in ? ds : 0.f;
-        }
-        s[r] = FMT == kF16 ? p * 32768.f : p;
+        start[r] = stats[u * 32 + row_in(r, half)];
+        s[r] = FMT == kF32 ? 0.f : start[r];
+        dp[r] = stats[kRows + u * 32 + row_in(r, half)];
+      }
+      C::along(s, sq, u, k, lanes);
+      C::along(dp, sy, u, v, lanes);
+      const int r0 = t * kRows + u * 32;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        float p = s[r], ds = dp[r];
+        weigh<FMT>(p, ds, start[r], a.scale2);
+        s[r] = p;
         dp[r] = ds;
       }
-      across32<C>(dv, sy, u * 32, s, lane);
+      if (r0 < plain || r0 + 32 > rows) {
+        const int first = here(from - r0 - 4 * half), last = here(rows - r0 - 4 * half);
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (row_in(r, 0) < first || row_in(r, 0) >= last) s[r] = dp[r] = 0.f;
+      }
+      across32<C>(dv, sy, u, s, lanes);
       scaled.hold(dp, dk);
-      across32<C>(dk, sq, u * 32, dp, lane);
+      across32<C>(dk, sq, u, dp, lanes);
     }
   }
   if (key >= at.stored) return;
@@ -286,7 +310,7 @@ __global__ __launch_bounds__(256, 1) void k_backward_kv(Args a) {
   store_columns<C, FMT>(dk, a.dk.p + (at.seq * a.dk.batch + where * a.dk.row + head * a.dk.head) * C::kSize,
                         a.dim, half, there ? a.scale * scaled.out() : 0.f);
   store_columns<C, FMT>(dv, a.dv.p + (at.seq * a.dv.batch + where * a.dv.row + head * a.dv.head) * C::kSize,
-                        a.dim, half, there ? (FMT == kF16 ? 1.f / 32768.f : 1.f) : 0.f);
+                        a.dim, half, there ? (FMT == kF16 ? ldexpf(1.f, -kShift) : 1.f) : 0.f);
 #endif
 }
 
@@ -309,17 +333,17 @@ void go_kv(const Args &a, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_delta(const Args &a, int fmt, long long tokens, int heads, hipStream_t st) {
+hipError_t launch_starts(const Args &a, int fmt, long long tokens, int heads, hipStream_t st) {
   const long long total = tokens * heads;
   if (!total) return hipSuccess;
   const dim3 grid((unsigned)((total + 15) / 16));
   const FastDiv div = make_fastdiv((uint32_t)heads);
   if (fmt == kBf16)
-    hipLaunchKernelGGL(k_delta<kBf16>, grid, dim3(256), 0, st, a, div, total);
+    hipLaunchKernelGGL(k_starts<kBf16>, grid, dim3(256), 0, st, a, div, total);
   else if (fmt == kF16)
-    hipLaunchKernelGGL(k_delta<kF16>, grid, dim3(256), 0, st, a, div, total);
+    hipLaunchKernelGGL(k_starts<kF16>, grid, dim3(256), 0, st, a, div, total);
   else
-    hipLaunchKernelGGL(k_delta<kF32>, grid, dim3(256), 0, st, a, div, total);
+    hipLaunchKernelGGL(k_starts<kF32>, grid, dim3(256), 0, st, a, div, total);
   return hipGetLastError();
 }
 

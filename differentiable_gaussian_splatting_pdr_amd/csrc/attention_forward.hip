@@ -50,14 +50,9 @@ struct Query {
   }
   // 32 N keys' values under these weights.
   template <int N>
-  __device__ __forceinline__ void take(const char *values, const f32x16 (&s)[N], int lane) {
+  __device__ __forceinline__ void take(const char *values, const f32x16 (&s)[N], const typename C::Lane &at) {
 #pragma unroll
-    for (int x = 0; x < 2 * N; ++x) {
-      float p[8];
-#pragma unroll
-      for (int r = 0; r < 8; ++r) p[r] = s[x >> 1][(x & 1) * 8 + r];
-      C::across(out, values, x * 16, p, lane);
-    }
+    for (int x = 0; x < 2 * N; ++x) C::across(out, values, x, C::pack(s[x >> 1], (x & 1) * 8), at);
   }
 };
 
@@ -70,11 +65,12 @@ __device__ __forceinline__ float lse_of(float most, float sum) {
   return most == -INFINITY && sum == 0.f ? INFINITY : most + __log2f(sum);
 }
 
-// Scores of keys that the lane's query does not see.
-__device__ __forceinline__ void mask(f32x16 &s, int key0, int half, int seen) {
+// Scores of keys that the lane's query does not see; `seen` counts from the tile's
+// first key of this half.
+__device__ __forceinline__ void mask(f32x16 &s, int key0, int seen) {
 #pragma unroll
   for (int r = 0; r < 16; ++r)
-    if (key0 + row_in(r, half) >= seen) s[r] = -INFINITY;
+    if (key0 + row_in(r, 0) >= seen) s[r] = -INFINITY;
 }
 
 // What a lane needs to know of its row.
@@ -130,36 +126,37 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_forward(Args a) {
 
   i32x4 q[C::kSteps];
   C::fetch_row(q, row_at(a.q, at, row, head, group, C::kSize), a.dim, half, row.there);
+  typename C::Lane lanes;
+  lanes.init(lane);
   Query<C> query;
   query.init();
-  L lk, lv;
-  lk.init(a.k, first_of(a.k, at, at.k0, head), a.dim, wave, lane);
-  lv.init(a.v, first_of(a.v, at, at.k0, head), a.dim, wave, lane);
+  const Source k(a.k, first_of(a.k, at, at.k0, head), C::kSize), v(a.v, first_of(a.v, at, at.k0, head), C::kSize);
+  L load;
+  load.init(a.dim, wave, lane);
   const int tiles = (keys + kKeys - 1) / kKeys;
   if (tiles > 0) {
-    lk.tokens(0, at.nk, smem);
-    lv.tokens(0, at.nk, smem + L::kBytes);
+    load.tokens(k, v, 0, at.nk, smem);
   }
   for (int t = 0; t < tiles; ++t) {
     char *const sk = smem + (t & 1) * (2 * L::kBytes), *const sv = sk + L::kBytes;
     all_landed<0>();
     if (t + 1 < tiles) {
       char *const next = smem + ((t + 1) & 1) * (2 * L::kBytes);
-      lk.tokens((t + 1) * kKeys, at.nk, next);
-      lv.tokens((t + 1) * kKeys, at.nk, next + L::kBytes);
+      load.tokens(k, v, (t + 1) * kKeys, at.nk, next);
     }
     f32x16 s[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       clear(s[u]);
-      C::along(s[u], sk, u * 32, q, lane);
+      C::along(s[u], sk, u, q, lanes);
     }
     if ((t + 1) * kKeys > plain) {
+      const int seen = here(row.seen - t * kKeys - 4 * half);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) mask(s[u], t * kKeys + u * 32, half, row.seen);
+      for (int u = 0; u < 2; ++u) mask(s[u], u * 32, seen);
     }
     query.template weigh<2>(s, a.scale2);
-    query.template take<2>(sv, s, lane);
+    query.template take<2>(sv, s, lanes);
   }
   const float sum = query.sum + other_half(query.sum);
   if (!row.there) return;
@@ -194,11 +191,13 @@ __global__ __launch_bounds__(64 * NW) void k_forward_few(Args a) {
 
   i32x4 q[C::kSteps];
   C::fetch_row(q, row_at(a.q, at, row, head, group, C::kSize), a.dim, half, row.there);
+  typename C::Lane lanes;
+  lanes.init(lane);
   Query<C> query;
   query.init();
-  L lk, lv;
-  lk.init(a.k, first_of(a.k, at, at.k0, head), a.dim, 0, lane);
-  lv.init(a.v, first_of(a.v, at, at.k0, head), a.dim, 0, lane);
+  const Source k(a.k, first_of(a.k, at, at.k0, head), C::kSize), v(a.v, first_of(a.v, at, at.k0, head), C::kSize);
+  L load;
+  load.init(a.dim, 0, lane);
   char *const ring = smem + wave * 4 * L::kBytes;
   // this wave's tiles
   const int all = (keys + kKeys - 1) / kKeys, parts = a.splits * NW;
@@ -206,26 +205,26 @@ __global__ __launch_bounds__(64 * NW) void k_forward_few(Args a) {
   const int begin = part * each < all ? part * each : all;
   const int end = begin + each < all ? begin + each : all;
   if (begin < end) {
-    lk.tokens(begin * kKeys, at.nk, ring);
-    lv.tokens(begin * kKeys, at.nk, ring + L::kBytes);
+    load.tokens(k, v, begin * kKeys, at.nk, ring);
   }
   for (int t = begin; t < end; ++t) {
     char *const sk = ring + ((t - begin) & 1) * (2 * L::kBytes), *const sv = sk + L::kBytes;
     if (t + 1 < end) {
       char *const next = ring + ((t + 1 - begin) & 1) * (2 * L::kBytes);
       landed<2 * L::kIssues>();  // what is there of the last tile's reads is done
-      lk.tokens((t + 1) * kKeys, at.nk, next);
-      lv.tokens((t + 1) * kKeys, at.nk, next + L::kBytes);
+      load.tokens(k, v, (t + 1) * kKeys, at.nk, next);
       landed<2 * L::kIssues>();
     } else {
       landed<0>();
     }
     f32x16 s[1];
     clear(s[0]);
-    C::along(s[0], sk, 0, q, lane);
-    if ((t + 1) * kKeys > plain) mask(s[0], t * kKeys, half, row.seen);
+    C::along(s[0], sk, 0, q, lanes);
+    if ((t + 1) * kKeys > plain) {
+      mask(s[0], 0, here(row.seen - t * kKeys - 4 * half));
+    }
     query.template weigh<1>(s, a.scale2);
-    query.template take<1>(sv, s, lane);
+    query.template take<1>(sv, s, lanes);
   }
   const float sum = query.sum + other_half(query.sum);
   __syncthreads();

@@ -143,6 +143,8 @@ Plan plan_of(const pdr_attention &p) {
 }
 
 long long tokens_of(const pdr_attention &p) { return (p.q_offsets ? 1 : p.batch) * p.q_rows; }
+// Bytes of a value for each query and head.
+size_t row_values(const pdr_attention &p) { return round256((size_t)tokens_of(p) * p.heads * 4); }
 
 // ------------------------------------------------------- layer norm, dropout
 
@@ -240,7 +242,7 @@ int pdr_attention_forward(const pdr_attention *p, void *workspace, size_t worksp
 
 long long pdr_attention_backward_workspace_bytes(const pdr_attention *p) {
   const int rc = check_attention(p, true);
-  return rc != PDR_OK ? rc : (long long)round256((size_t)tokens_of(*p) * p->heads * 4);
+  return rc != PDR_OK ? rc : (long long)(2 * row_values(*p));
 }
 int pdr_attention_backward(const pdr_attention *p, void *workspace, size_t workspace_bytes, void *stream) {
   const long long need = pdr_attention_backward_workspace_bytes(p);
@@ -249,8 +251,9 @@ int pdr_attention_backward(const pdr_attention *p, void *workspace, size_t works
   if (rc != PDR_OK) return rc;
   const hipStream_t st = (hipStream_t)stream;
   Args a = args_of(*p);
-  a.delta = (float *)workspace;
-  hipError_t e = attend::launch_delta(a, p->fmt, tokens_of(*p), (int)p->heads, st);
+  a.start_s = (float *)workspace;
+  a.start_dp = (float *)((char *)workspace + row_values(*p));
+  hipError_t e = attend::launch_starts(a, p->fmt, tokens_of(*p), (int)p->heads, st);
   if (e == hipSuccess && p->dk) {
     a.k_tiles = tiles_of(*p, p->k_rows, 1, attend::kLogWide, &a.per_seq);
     e = attend::launch_backward_kv(a, p->fmt, st);

@@ -131,9 +131,9 @@ def test_null_structs_and_workspaces():
 
 
 def test_workspace_bytes():
-    # many queries keep nothing; a row's delta in the backward
+    # many queries keep nothing; two values a row in the backward
     assert size("pdr_attention_forward", attention()) == 0
-    assert size("pdr_attention_backward", attention()) == 2 * 100 * 8 * 4
+    assert size("pdr_attention_backward", attention()) == 2 * (2 * 100 * 8 * 4)
     assert size("pdr_layer_norm_forward", norm()) == 0
     assert size("pdr_layer_norm_backward", norm(dweight=None, dbias=None)) == 0
     assert size("pdr_dropout", dropout()) == 0
