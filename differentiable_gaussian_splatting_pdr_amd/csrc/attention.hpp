@@ -59,13 +59,15 @@ struct Args {
   float *lse;
   float *start_s, *start_dp;  // backward: what scores and their gradients' products start from, as lse
   float *part_o, *part_ml;  // few queries: the splits' sums, and their maxima and weights
+  float *part_k;            // dk and dv: the parts' sums
   float scale, scale2;      // scale, and scale log2(e)
   int causal, batch, kv_heads, dim, q_rows, k_rows;
   int q_tiles, k_tiles;     // of a sequence; with offsets, of all
   int splits;
+  int waves;                // few queries: of a workgroup
   FastDiv group;            // by G
   FastDiv heads;            // by kv_heads
-  FastDiv per_seq;          // by the tiles of a sequence (no offsets)
+  FastDiv per_tile;         // by the sequences (no offsets)
 };
 
 // ------------------------------------------------------------ where things lie
@@ -115,8 +117,10 @@ __device__ __forceinline__ Place place(const Args &a, int t) {
   Place p;
   const int g = BY_KEYS ? 1 : (int)a.group.d;
   if (!a.q_offsets) {
-    p.seq = (int)fdiv((uint32_t)t, a.per_seq);
-    p.tile = t - p.seq * (int)a.per_seq.d;
+    // equal tiles of all sequences follow one another, so that where queries see
+    // what is before them work is handed out by its length
+    p.tile = (int)fdiv((uint32_t)t, a.per_tile);
+    p.seq = t - p.tile * a.batch;
     p.nq = a.q_rows;
     p.nk = a.k_rows;
     if (a.key_lengths) {
@@ -157,6 +161,13 @@ __device__ __forceinline__ long long first_of(const Mat &m, const Place &p, int 
 
 // -------------------------------------------------------------- element types
 
+// The same value; what follows from it is not worked out earlier: in a branch that
+// few tiles take, or to hold few registers.
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 template <int FMT, int DP>  // DP: values a row has in LDS and registers (dim, rounded up)
 struct Core {
   static constexpr int kSize = FMT == kF32 ? 4 : 2;
@@ -166,10 +177,13 @@ struct Core {
   static constexpr int kRowBytes = DP * kSize;
   static constexpr int kBlocks = DP / 32;             // of 32 d
 
-  // LDS: chunk c of row r is stored at chunk c ^ swizzle(r).  Eight rows' equal
-  // chunks fall on different banks (along), and so do the 32 bytes that each of
-  // four rows gives to a transposing read (across).
-  static __device__ __forceinline__ int swizzle(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+  // LDS: chunk c of row r is stored at chunk c ^ swizzle(r), so that the 256 bytes
+  // that are read at a time fall on different banks: eight rows' equal chunks
+  // (along), and four neighbouring chunks of each of four rows (across, whose
+  // transposing read takes 32 bytes of a row to 16 lanes).
+  static __device__ __forceinline__ constexpr int swizzle(int r) {
+    return kChunks > 8 ? (r & 3) << 2 | ((r >> 2) & 1) : ((r >> 1) & 1) << 2 | (r & 1) << 1 | ((r >> 2) & 1);
+  }
 
   static __device__ __forceinline__ f32x16 go(i32x4 a, i32x4 b, f32x16 c) {
     if constexpr (FMT == kBf16) {
@@ -198,43 +212,55 @@ struct Core {
     }
   }
 
-  // Where a lane reads in a tile whose first row is a multiple of 16 of LDS rows.
-  // A chunk's low three bits are turned by the swizzle, and the rest of its place
-  // is the same for all lanes: few addresses serve all of a tile's reads, with
-  // offsets known when the kernel is compiled.
-  static constexpr int kAcross = FMT == kF32 ? 4 : 2;
+  // The same of rows [first, first + 32) of `rows`, one to a lane and its other half.
+  template <class Source>
+  static __device__ __forceinline__ void fetch_rows(i32x4 (&f)[kSteps], const Source &from, int first, int rows,
+                                                    int dim, int lane) {
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(from.base + (long long)first * from.row), 0, (int)kOutside, 0x00020000);
+    const uint32_t r = lane & 31, half = lane >> 5;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const uint32_t c = 2 * s + half;
+      const bool in = first + (int)r < rows && (int)c * kPer < dim;
+      f[s] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                           rsrc, (int)(in ? r * from.row + c * 16 : kOutside), 0, 0));
+    }
+  }
+
+  // Where a lane reads in a tile that begins on 256 bytes.  What the swizzle turns
+  // of a chunk's place is turned again for each step or block, by a constant; the
+  // rest is the same for all lanes, an offset known when the kernel is compiled.
+  // The lane keeps one address of each kind: registers are what these kernels run
+  // out of, so the turned ones are made where they are used (here()).
   struct Lane {
-    int rows[4];            // along(): of steps s % 4
-    int columns[kAcross];   // across(): of blocks b % 2, or rows e % 4
+    int row, column;
     __device__ __forceinline__ void init(int lane) {
       const int half = lane >> 5, r = lane & 31;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) rows[s] = r * kRowBytes + (((2 * s + half) ^ swizzle(r)) << 4);
+      row = r * kRowBytes + ((half ^ swizzle(r)) << 4);
       if constexpr (FMT != kF32) {
-        const int t = lane & 15, k = 4 * half + (t >> 2);
-        const int c = ((lane >> 4) & 1) * 2 + ((t & 3) >> 1);
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-          columns[b] = k * kRowBytes + (((b * 4 + c) ^ swizzle(k)) << 4) + (t & 1) * 8;
+        const int t = lane & 15, k = 4 * half + (t >> 2), c = ((lane >> 4) & 1) * 2 + ((t & 3) >> 1);
+        column = k * kRowBytes + ((c ^ swizzle(k)) << 4) + (t & 1) * 8;
       } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int k = 4 * half + e;
-          columns[e] = k * kRowBytes + (((r >> 2) ^ swizzle(k)) << 4) + (r & 3) * 4;
-        }
+        column = 4 * half * kRowBytes + (((r >> 2) ^ half) << 4) + (r & 3) * 4;
       }
     }
   };
+  template <class T>
+  static __device__ __forceinline__ T read(int at) {
+    return *(const __attribute__((address_space(3))) T *)(uintptr_t)(uint32_t)at;
+  }
 
-  // Rows 32 U .. 32 U + 31 of the tile.
-  static __device__ __forceinline__ void along(f32x16 &c, const char *tile, int u,
+  // Rows 32 u .. 32 u + 31 of the tile.
+  static __device__ __forceinline__ void along(f32x16 &c, const lds_char *tile, int u,
                                                const i32x4 (&reg)[kSteps], const Lane &at) {
-    const lds_char *p = (const lds_char *)tile;
+    const int first = here((int)(uintptr_t)tile + at.row);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      const i32x4 a = *(const __attribute__((address_space(3))) i32x4 *)(p + at.rows[s & 3] + (s >> 2) * 128 +
-                                                                         u * 32 * kRowBytes);
-      c = go(a, reg[s], c);
+      // chunk 2 s + half: with 8 chunks in a row all of s is turned, else its bits 1 and 2
+      const int turn = kChunks > 8 ? ((s >> 1) & 3) << 6 : s << 5;
+      const int offset = kChunks > 8 ? (s & 1) * 32 + (s >> 3) * 256 : 0;
+      c = go(read<i32x4>((first ^ turn) + offset + u * 32 * kRowBytes), reg[s], c);
     }
   }
 
@@ -261,23 +287,25 @@ struct Core {
     return o;
   }
   // Rows 16 X .. 16 X + 15 of the tile under these weights.
-  static __device__ __forceinline__ void across(f32x16 (&c)[kBlocks], const char *tile, int x,
+  static __device__ __forceinline__ void across(f32x16 (&c)[kBlocks], const lds_char *tile, int x,
                                                 const Weights &p, const Lane &at) {
-    const lds_char *first = (const lds_char *)tile + x * 16 * kRowBytes;
+    const int first = here((int)(uintptr_t)tile + at.column);
     if constexpr (FMT != kF32) {
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
-        const lds_char *lo = first + at.columns[b & 1] + (b >> 1) * 128;
-        const s16x4 y = transposed((lds_s16x4 *)lo), z = transposed((lds_s16x4 *)(lo + 8 * kRowBytes));
+        const int lo = (first ^ b << 6) + x * 16 * kRowBytes;
+        const s16x4 y = transposed((lds_s16x4 *)(uintptr_t)(uint32_t)lo);
+        const s16x4 z = transposed((lds_s16x4 *)(uintptr_t)(uint32_t)(lo + 8 * kRowBytes));
         c[b] = go(__builtin_bit_cast(i32x4, __builtin_shufflevector(y, z, 0, 1, 2, 3, 4, 5, 6, 7)), p.w[0], c[b]);
       }
     } else {
+      // row 8 (e / 4) + 4 half + e % 4: of its swizzle, bits 2 and 3 are e's
 #pragma unroll
       for (int e = 0; e < 8; ++e)
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
-          const float f = *(const __attribute__((address_space(3))) float *)(
-              first + at.columns[e & 3] + (e >> 2) * 8 * kRowBytes + b * 128);
+          const float f = read<float>((first ^ (e & 1) << 6) + (x * 16 + 8 * (e >> 2) + (e & 3)) * kRowBytes +
+                                      (b ^ ((e >> 1) & 1)) * 128);
           c[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(f, __int_as_float(p.w[e >> 2][e & 3]), c[b], 0, 0, 0);
         }
     }
@@ -320,14 +348,23 @@ struct Loader {
     const int c = chunk0 ^ C::swizzle(i * NW * kRowsEach);
     return c * C::kPer < dim ? (uint32_t)c * 16u : kOutside;
   }
-  __device__ __forceinline__ void issue(const char *from, uint32_t off, char *lds, int i) const {
+  __device__ __forceinline__ void issue(const char *from, uint32_t off, lds_char *lds, int i) const {
     const __amdgpu_buffer_rsrc_t rsrc =
         __builtin_amdgcn_make_buffer_rsrc((void *)from, 0, (int)kOutside, 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(lds + (i * NW + wave) * 1024), 16,
                                              (int)off, 0, 0, 0);
   }
-  // Rows [first, first + ROWS) of `rows`, of two tensors.
-  __device__ __forceinline__ void tokens(const Source &x, const Source &y, int first, int rows, char *lds) const {
+  // Rows [first, first + ROWS) of `rows`.
+  __device__ __forceinline__ void tokens(const Source &x, int first, int rows, lds_char *lds) const {
+    const char *const from = x.base + (long long)first * x.row;
+#pragma unroll
+    for (int i = 0; i < kIssues; ++i) {
+      const uint32_t r = (uint32_t)row_of(i), c = byte_of(i);
+      issue(from, first + (int)r < rows && c != kOutside ? r * x.row + c : kOutside, lds, i);
+    }
+  }
+  // The same, of two tensors.
+  __device__ __forceinline__ void tokens(const Source &x, const Source &y, int first, int rows, lds_char *lds) const {
     const char *const from_x = x.base + (long long)first * x.row;
     const char *const from_y = y.base + (long long)first * y.row;
 #pragma unroll
@@ -340,7 +377,7 @@ struct Loader {
   }
   // The same of a group's rows.
   __device__ __forceinline__ void grouped(const Source &x, const Source &y, int first, int rows,
-                                          const FastDiv &group, char *lds) const {
+                                          const FastDiv &group, lds_char *lds) const {
     const int token0 = (int)fdiv((uint32_t)first, group);
     const char *const from_x = x.base + (long long)token0 * x.row;
     const char *const from_y = y.base + (long long)token0 * y.row;
@@ -368,13 +405,6 @@ __device__ __forceinline__ void all_landed() {
 
 // The value of the lane 32 further on (or back).
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
-
-// The same value, in a branch that few tiles take: what follows from it is not
-// worked out before the branch, where every tile would pay for it.
-__device__ __forceinline__ int here(int v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
 
 // Row of a result's register r in this half.
 __device__ __forceinline__ int row_in(int r, int half) { return 8 * (r >> 2) + 4 * half + (r & 3); }

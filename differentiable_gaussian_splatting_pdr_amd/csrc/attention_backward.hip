@@ -21,7 +21,29 @@ namespace {
 // long rows' weights in the type's range.
 constexpr int kShift = 15;
 
-// The starts of each row: 16 lanes to a row, 16 bytes each at a time.
+template <int FMT>
+__device__ __forceinline__ float start_of(float lse, float scale2) {
+  return FMT == kF32 ? -lse : ((FMT == kF16 ? kShift : 0) - lse) / scale2;
+}
+
+// s + x . y of 16 bytes each.
+template <int FMT>
+__device__ __forceinline__ float dot(i32x4 x, i32x4 y, float s) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (FMT == kF32) {
+      s = fmaf(__int_as_float(x[j]), __int_as_float(y[j]), s);
+    } else {
+      s = fmaf(dense::to_f<FMT>((uint16_t)x[j]), dense::to_f<FMT>((uint16_t)y[j]), s);
+      s = fmaf(dense::to_f<FMT>((uint16_t)((uint32_t)x[j] >> 16)),
+               dense::to_f<FMT>((uint16_t)((uint32_t)y[j] >> 16)), s);
+    }
+  }
+  return s;
+}
+
+// The starts of each row, where no dq is wanted (its kernel makes them on the
+// way): 16 lanes to a row, 16 bytes each at a time.
 template <int FMT>
 __global__ __launch_bounds__(256) void k_starts(Args a, FastDiv heads, long long total) {
   constexpr int kSize = FMT == kF32 ? 4 : 2, kPer = 16 / kSize;
@@ -37,28 +59,16 @@ __global__ __launch_bounds__(256) void k_starts(Args a, FastDiv heads, long long
   const char *o = a.o.p + (seq * a.o.batch + i * a.o.row + head * a.o.head) * kSize;
   const char *dy = a.dy.p + (seq * a.dy.batch + i * a.dy.row + head * a.dy.head) * kSize;
   float s = 0.f;
-  for (int d = lane * kPer; d < a.dim; d += 16 * kPer) {
-    const i32x4 x = *(const i32x4 *)(o + d * kSize), y = *(const i32x4 *)(dy + d * kSize);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (FMT == kF32) {
-        s = fmaf(__int_as_float(x[j]), __int_as_float(y[j]), s);
-      } else {
-        s = fmaf(dense::to_f<FMT>((uint16_t)x[j]), dense::to_f<FMT>((uint16_t)y[j]), s);
-        s = fmaf(dense::to_f<FMT>((uint16_t)((uint32_t)x[j] >> 16)),
-                 dense::to_f<FMT>((uint16_t)((uint32_t)y[j] >> 16)), s);
-      }
-    }
-  }
+  for (int d = lane * kPer; d < a.dim; d += 16 * kPer)
+    s = dot<FMT>(*(const i32x4 *)(o + d * kSize), *(const i32x4 *)(dy + d * kSize), s);
 #pragma unroll
   for (int w = 8; w > 0; w >>= 1) s += __shfl_xor(s, w);
   const uint32_t kv = fdiv(head, a.group), g = head - kv * a.group.d;
   const long long tokens = total / heads.d;
   if (lane == 0) {
     const long long to = (kv * tokens + token) * a.group.d + g;
-    const float lse = a.lse[to];
     a.start_dp[to] = -s;
-    a.start_s[to] = FMT == kF32 ? -lse : ((FMT == kF16 ? kShift : 0) - lse) / a.scale2;
+    a.start_s[to] = start_of<FMT>(a.lse[to], a.scale2);
   }
 }
 
@@ -106,20 +116,22 @@ struct Scaled {
 };
 
 template <class C>
-__device__ __forceinline__ void across32(f32x16 (&c)[C::kBlocks], const char *tile, int u,
+__device__ __forceinline__ void across32(f32x16 (&c)[C::kBlocks], const lds_char *tile, int u,
                                          const f32x16 &w, const typename C::Lane &at) {
 #pragma unroll
   for (int x = 0; x < 2; ++x) C::across(c, tile, 2 * u + x, C::pack(w, 8 * x), at);
 }
 
-// dq: 128 rows to a workgroup, 32 to a wave, as in the forward.
+// dq: 128 rows to a workgroup, 32 to a wave, as in the forward; and the rows'
+// starts.
 template <int FMT, int DP>
 __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using C = Core<FMT, DP>;
   constexpr int kKeys = 64;
   using L = Loader<C, kKeys, 4>;
-  __shared__ __align__(1024) char smem[4 * L::kBytes];
+  __shared__ __align__(1024) char shared[4 * L::kBytes];
+  lds_char *const smem = (lds_char *)shared;
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int unit = (int)fdiv(blockIdx.x, a.heads), head = blockIdx.x - unit * a.kv_heads;
@@ -148,12 +160,23 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
   C::fetch_row(dy, a.dy.p + (first_of(a.dy, at, at.q0 + token, head * group) + in_group * a.dy.head) * C::kSize,
                a.dim, half, there);
   float start_s = 0.f, start_dp = 0.f;
+  {
+    i32x4 o[C::kSteps];
+    C::fetch_row(o, a.o.p + (first_of(a.o, at, at.q0 + token, head * group) + in_group * a.o.head) * C::kSize,
+                 a.dim, half, there);
+#pragma unroll
+    for (int i = 0; i < C::kSteps; ++i) start_dp = dot<FMT>(o[i], dy[i], start_dp);
+    start_dp = -(start_dp + other_half(start_dp));
+  }
   if (there) {
     const long long tokens = a.q_offsets ? a.q_rows : (long long)a.batch * a.q_rows;
     const long long i =
         (head * tokens + (a.q_offsets ? 0 : (long long)at.seq * a.q_rows) + at.q0) * group + row;
-    start_s = a.start_s[i];
-    start_dp = a.start_dp[i];
+    start_s = start_of<FMT>(a.lse[i], a.scale2);
+    if (half == 0) {
+      a.start_s[i] = start_s;
+      a.start_dp[i] = start_dp;
+    }
   }
   f32x16 sums[C::kBlocks];
 #pragma unroll
@@ -170,10 +193,10 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
     load.tokens(k, v, 0, at.nk, smem);
   }
   for (int t = 0; t < tiles; ++t) {
-    char *const sk = smem + (t & 1) * (2 * L::kBytes), *const sv = sk + L::kBytes;
+    const lds_char *const sk = smem + (t & 1) * (2 * L::kBytes), *const sv = sk + L::kBytes;
     all_landed<0>();
     if (t + 1 < tiles) {
-      char *const next = smem + ((t + 1) & 1) * (2 * L::kBytes);
+      lds_char *const next = smem + ((t + 1) & 1) * (2 * L::kBytes);
       load.tokens(k, v, (t + 1) * kKeys, at.nk, next);
     }
 #pragma unroll
@@ -216,7 +239,8 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_kv(Args a
   constexpr int kRows = 64;
   using L = Loader<C, kRows, 4>;
   constexpr int kStage = 2 * L::kBytes + 2 * kRows * 4;
-  __shared__ __align__(1024) char smem[2 * kStage];
+  __shared__ __align__(1024) char shared[2 * kStage];
+  lds_char *const smem = (lds_char *)shared;
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int unit = (int)fdiv(blockIdx.x, a.heads), head = blockIdx.x - unit * a.kv_heads;
@@ -233,10 +257,13 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_kv(Args a
     const long long r = a.causal ? (long long)(k - ahead) * group : 0;
     return r < 0 ? 0 : r > rows ? rows : (int)r;
   };
-  const int from = first_row(key);
   const int plain = first_row(key0 + wave * 32 + 31);  // from here on the wave needs no mask
-  const int end = key0 < at.nk ? (rows + kRows - 1) / kRows : 0;
-  const int begin = first_row(key0) / kRows;
+  // this part's tiles of rows
+  int begin = first_row(key0) / kRows;
+  const int last = key0 < at.nk ? (rows + kRows - 1) / kRows : begin;
+  const int each = (last - begin + a.splits - 1) / a.splits;
+  begin += blockIdx.y * each;
+  const int end = begin + each < last ? begin + each : last;
 
   i32x4 k[C::kSteps], v[C::kSteps];
   C::fetch_row(k, a.k.p + first_of(a.k, at, at.k0 + (there ? key : 0), head) * C::kSize, a.dim, half, there);
@@ -258,7 +285,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_kv(Args a
   const long long tokens = a.q_offsets ? a.q_rows : (long long)a.batch * a.q_rows;
   const long long first =
       (head * tokens + (a.q_offsets ? 0 : (long long)at.seq * a.q_rows) + at.q0) * group;
-  auto load = [&](int t, char *stage) {
+  auto load = [&](int t, lds_char *stage) {
     loader.grouped(from_q, from_dy, t * kRows, rows, a.group, stage);
     const float *src = wave == 0 ? a.start_s : a.start_dp;  // one wave each
     const __amdgpu_buffer_rsrc_t rsrc =
@@ -270,8 +297,8 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_kv(Args a
   };
   if (begin < end) load(begin, smem);
   for (int t = begin; t < end; ++t) {
-    char *const sq = smem + ((t - begin) & 1) * kStage, *const sy = sq + L::kBytes;
-    const float *const stats = (const float *)(sq + 2 * L::kBytes);
+    const lds_char *const sq = smem + ((t - begin) & 1) * kStage, *const sy = sq + L::kBytes;
+    const auto *const stats = (const __attribute__((address_space(3))) float *)(sq + 2 * L::kBytes);
     all_landed<0>();
     if (t + 1 < end) load(t + 1, smem + ((t + 1 - begin) & 1) * kStage);
 #pragma unroll
@@ -295,7 +322,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_kv(Args a
         dp[r] = ds;
       }
       if (r0 < plain || r0 + 32 > rows) {
-        const int first = here(from - r0 - 4 * half), last = here(rows - r0 - 4 * half);
+        const int first = here(first_row(key) - r0 - 4 * half), last = here(rows - r0 - 4 * half);
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           if (row_in(r, 0) < first || row_in(r, 0) >= last) s[r] = dp[r] = 0.f;
@@ -306,12 +333,51 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_kv(Args a
     }
   }
   if (key >= at.stored) return;
+  const float by_k = there ? a.scale * scaled.out() : 0.f;
+  const float by_v = there ? (FMT == kF16 ? ldexpf(1.f, -kShift) : 1.f) : 0.f;
   const long long where = at.k0 + key;
+  if (a.splits > 1) {
+    // [part][dk, dv][key head][key][dim]
+    const long long all = (a.q_offsets ? 1LL : a.batch) * a.k_rows;
+    const long long mine = (a.q_offsets ? 0 : (long long)at.seq * a.k_rows) + where;
+    float *const to = a.part_k + ((2LL * blockIdx.y * a.kv_heads + head) * all + mine) * a.dim;
+    using P = Core<kF32, DP>;
+    store_columns<P, kF32>(dk, (char *)to, a.dim, half, by_k);
+    store_columns<P, kF32>(dv, (char *)(to + a.kv_heads * all * a.dim), a.dim, half, by_v);
+    return;
+  }
   store_columns<C, FMT>(dk, a.dk.p + (at.seq * a.dk.batch + where * a.dk.row + head * a.dk.head) * C::kSize,
-                        a.dim, half, there ? a.scale * scaled.out() : 0.f);
+                        a.dim, half, by_k);
   store_columns<C, FMT>(dv, a.dv.p + (at.seq * a.dv.batch + where * a.dv.row + head * a.dv.head) * C::kSize,
-                        a.dim, half, there ? (FMT == kF16 ? ldexpf(1.f, -kShift) : 1.f) : 0.f);
+                        a.dim, half, by_v);
 #endif
+}
+
+// dk (y = 0) and dv: the sums of the parts.  One thread per 4 values.
+template <int FMT>
+__global__ __launch_bounds__(256) void k_join_keys(Args a, FastDiv quads, FastDiv keys, long long rows) {
+  constexpr int kSize = FMT == kF32 ? 4 : 2;
+  const uint32_t x = blockIdx.x * 256u + threadIdx.x, i = fdiv(x, quads);
+  if (i >= rows) return;
+  const int d = (int)(x - i * quads.d) * 4;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const float4 p = *(const float4 *)(a.part_k + ((2LL * s + blockIdx.y) * rows + i) * a.dim + d);
+    v[0] += p.x;
+    v[1] += p.y;
+    v[2] += p.z;
+    v[3] += p.w;
+  }
+  // row i is key n of a head, of all sequences' keys
+  const uint32_t head = fdiv(i, keys), n = i - head * keys.d;
+  long long seq = 0, token = n;
+  if (!a.q_offsets) {
+    seq = n / (uint32_t)a.k_rows;
+    token = n - seq * a.k_rows;
+  }
+  const Mat &to = blockIdx.y ? a.dv : a.dk;
+  store4<FMT>(to.p + (seq * to.batch + token * to.row + head * to.head + d) * kSize, v);
 }
 
 template <int FMT>
@@ -324,11 +390,16 @@ void go_q(const Args &a, hipStream_t st) {
 }
 template <int FMT>
 void go_kv(const Args &a, hipStream_t st) {
-  const dim3 grid((unsigned)a.k_tiles * a.kv_heads);
+  const dim3 grid((unsigned)a.k_tiles * a.kv_heads, (unsigned)a.splits);
   if (a.dim <= 64)
     hipLaunchKernelGGL((k_backward_kv<FMT, 64>), grid, dim3(256), 0, st, a);
   else
     hipLaunchKernelGGL((k_backward_kv<FMT, 128>), grid, dim3(256), 0, st, a);
+  if (a.splits > 1) {
+    const long long keys = (a.q_offsets ? 1LL : a.batch) * a.k_rows, rows = keys * a.kv_heads;
+    hipLaunchKernelGGL(k_join_keys<FMT>, dim3((unsigned)((rows * (a.dim / 4) + 255) / 256), 2), dim3(256), 0, st, a,
+                       make_fastdiv((uint32_t)a.dim / 4), make_fastdiv((uint32_t)keys), rows);
+  }
 }
 
 }  // namespace

@@ -50,7 +50,7 @@ struct Query {
   }
   // 32 N keys' values under these weights.
   template <int N>
-  __device__ __forceinline__ void take(const char *values, const f32x16 (&s)[N], const typename C::Lane &at) {
+  __device__ __forceinline__ void take(const lds_char *values, const f32x16 (&s)[N], const typename C::Lane &at) {
 #pragma unroll
     for (int x = 0; x < 2 * N; ++x) C::across(out, values, x, C::pack(s[x >> 1], (x & 1) * 8), at);
   }
@@ -110,7 +110,8 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_forward(Args a) {
   using C = Core<FMT, DP>;
   constexpr int kKeys = 64;
   using L = Loader<C, kKeys, 4>;
-  __shared__ __align__(1024) char smem[4 * L::kBytes];
+  __shared__ __align__(1024) char shared[4 * L::kBytes];
+  lds_char *const smem = (lds_char *)shared;
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // heads change fastest, so that an XCD's workgroups share few heads' keys;
@@ -138,10 +139,10 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_forward(Args a) {
     load.tokens(k, v, 0, at.nk, smem);
   }
   for (int t = 0; t < tiles; ++t) {
-    char *const sk = smem + (t & 1) * (2 * L::kBytes), *const sv = sk + L::kBytes;
+    const lds_char *const sk = smem + (t & 1) * (2 * L::kBytes), *const sv = sk + L::kBytes;
     all_landed<0>();
     if (t + 1 < tiles) {
-      char *const next = smem + ((t + 1) & 1) * (2 * L::kBytes);
+      lds_char *const next = smem + ((t + 1) & 1) * (2 * L::kBytes);
       load.tokens(k, v, (t + 1) * kKeys, at.nk, next);
     }
     f32x16 s[2];
@@ -168,29 +169,31 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_forward(Args a) {
 }
 
 // Few queries: 32 rows to a workgroup, whose waves take parts of the keys each,
-// in LDS of their own; workgroups along y take further parts, joined below.
+// in LDS of their own; workgroups along y take further parts, joined below.  Keys
+// go straight to registers (a lane's chunks of one row are what along() wants),
+// so that only values take up LDS and two workgroups' loads are in flight on a
+// compute unit.
 template <int FMT, int DP, int NW>
-__global__ __launch_bounds__(64 * NW) void k_forward_few(Args a) {
+__global__ __launch_bounds__(64 * NW, FMT == kF32 ? 1 : 2) void k_forward_few(Args a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using C = Core<FMT, DP>;
   constexpr int kKeys = 32;
   using L = Loader<C, kKeys, 1>;
-  constexpr int kPitch = DP * 4 + 16;  // of a row's sums
-  static_assert(4 * L::kBytes >= 32 * kPitch, "a wave's sums fit where its keys were");
-  __shared__ __align__(1024) char smem[NW * 4 * L::kBytes];
+  constexpr int kRing = 2 * L::kBytes;
+  static_assert(kRing >= 32 * DP * 4, "a wave's sums fit where its values were");
+  __shared__ __align__(1024) char shared[NW * kRing];
+  lds_char *const smem = (lds_char *)shared;
   __shared__ float stats[NW][32][2];
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int unit = (int)fdiv(blockIdx.x, a.heads), head = blockIdx.x - unit * a.kv_heads;
-  const Place at = place<kLogFew, false>(a, unit);
+  const Place at = place<kLogFew, false>(a, a.causal ? a.q_tiles - 1 - unit : unit);
   const int group = (int)a.group.d, rows = at.nq * group;
   const int row0 = at.tile << kLogFew;
   if (at.tile < 0 || row0 >= rows) return;
   const Row row(a, at, row0 + (lane & 31), rows);
   const int keys = keys_of(a, at, row0 + 31, rows), plain = keys_of(a, at, row0, rows);
 
-  i32x4 q[C::kSteps];
-  C::fetch_row(q, row_at(a.q, at, row, head, group, C::kSize), a.dim, half, row.there);
   typename C::Lane lanes;
   lanes.init(lane);
   Query<C> query;
@@ -198,33 +201,37 @@ __global__ __launch_bounds__(64 * NW) void k_forward_few(Args a) {
   const Source k(a.k, first_of(a.k, at, at.k0, head), C::kSize), v(a.v, first_of(a.v, at, at.k0, head), C::kSize);
   L load;
   load.init(a.dim, 0, lane);
-  char *const ring = smem + wave * 4 * L::kBytes;
+  lds_char *const ring = smem + wave * kRing;
   // this wave's tiles
   const int all = (keys + kKeys - 1) / kKeys, parts = a.splits * NW;
   const int each = (all + parts - 1) / parts, part = blockIdx.y * NW + wave;
   const int begin = part * each < all ? part * each : all;
   const int end = begin + each < all ? begin + each : all;
+  i32x4 keys_now[C::kSteps], keys_next[C::kSteps], q[C::kSteps];
   if (begin < end) {
-    load.tokens(k, v, begin * kKeys, at.nk, ring);
+    C::fetch_rows(keys_now, k, begin * kKeys, at.nk, a.dim, lane);
+    load.tokens(v, begin * kKeys, at.nk, ring);
   }
+  C::fetch_row(q, row_at(a.q, at, row, head, group, C::kSize), a.dim, half, row.there);
   for (int t = begin; t < end; ++t) {
-    char *const sk = ring + ((t - begin) & 1) * (2 * L::kBytes), *const sv = sk + L::kBytes;
+    const lds_char *const sv = ring + ((t - begin) & 1) * L::kBytes;
     if (t + 1 < end) {
-      char *const next = ring + ((t + 1 - begin) & 1) * (2 * L::kBytes);
-      landed<2 * L::kIssues>();  // what is there of the last tile's reads is done
-      load.tokens(k, v, (t + 1) * kKeys, at.nk, next);
-      landed<2 * L::kIssues>();
+      landed<C::kSteps + L::kIssues>();  // the last tile's reads of LDS are done
+      C::fetch_rows(keys_next, k, (t + 1) * kKeys, at.nk, a.dim, lane);
+      load.tokens(v, (t + 1) * kKeys, at.nk, ring + ((t + 1 - begin) & 1) * L::kBytes);
+      landed<C::kSteps + L::kIssues>();
     } else {
       landed<0>();
     }
     f32x16 s[1];
     clear(s[0]);
-    C::along(s[0], sk, 0, q, lanes);
-    if ((t + 1) * kKeys > plain) {
-      mask(s[0], 0, here(row.seen - t * kKeys - 4 * half));
-    }
+#pragma unroll
+    for (int i = 0; i < C::kSteps; ++i) s[0] = C::go(keys_now[i], q[i], s[0]);
+    if ((t + 1) * kKeys > plain) mask(s[0], 0, here(row.seen - t * kKeys - 4 * half));
     query.template weigh<1>(s, a.scale2);
     query.template take<1>(sv, s, lanes);
+#pragma unroll
+    for (int i = 0; i < C::kSteps; ++i) keys_now[i] = keys_next[i];
   }
   const float sum = query.sum + other_half(query.sum);
   __syncthreads();
@@ -236,7 +243,7 @@ __global__ __launch_bounds__(64 * NW) void k_forward_few(Args a) {
   for (int b = 0; b < C::kBlocks; ++b)
 #pragma unroll
     for (int r = 0; r < 16; r += 4)
-      *(float4 *)(ring + (lane & 31) * kPitch + (b * 32 + row_in(r, half)) * 4) =
+      *(float4 *)(shared + wave * kRing + (lane & 31) * (DP * 4) + (((b * 32 + row_in(r, half)) / 4 ^ (lane & 7)) * 16)) =
           make_float4(query.out[b][r], query.out[b][r + 1], query.out[b][r + 2], query.out[b][r + 3]);
   __syncthreads();
   constexpr int kQuads = DP / 4;
@@ -252,7 +259,7 @@ __global__ __launch_bounds__(64 * NW) void k_forward_few(Args a) {
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       const float by = exp2_(stats[w][i][0] - from);
-      const float4 o = *(const float4 *)(smem + w * 4 * L::kBytes + i * kPitch + d * 4);
+      const float4 o = *(const float4 *)(shared + w * kRing + i * (DP * 4) + ((d / 4 ^ (i & 7)) * 16));
       total = fmaf(stats[w][i][1], by, total);
       v[0] = fmaf(o.x, by, v[0]);
       v[1] = fmaf(o.y, by, v[1]);
@@ -325,14 +332,23 @@ void go(const Args &a, hipStream_t st) {
   else
     hipLaunchKernelGGL((k_forward<FMT, 128>), grid, dim3(256), 0, st, a);
 }
+template <int FMT, int DP>
+void go_few(const Args &a, hipStream_t st) {
+  const dim3 grid((unsigned)a.q_tiles * a.kv_heads, (unsigned)a.splits);
+  if constexpr (FMT != kF32 || DP == 64) {  // fp32 rows of 128: LDS for four waves
+    if (a.waves == 8) {
+      hipLaunchKernelGGL((k_forward_few<FMT, DP, 8>), grid, dim3(512), 0, st, a);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((k_forward_few<FMT, DP, 4>), grid, dim3(256), 0, st, a);
+}
 template <int FMT>
 void go_few(const Args &a, long long rows, hipStream_t st) {
-  const dim3 grid((unsigned)a.q_tiles * a.kv_heads, (unsigned)a.splits);
-  constexpr int kWide = FMT == kF32 ? 2 : 4;  // fp32 rows of 128: LDS for two waves
   if (a.dim <= 64)
-    hipLaunchKernelGGL((k_forward_few<FMT, 64, 4>), grid, dim3(256), 0, st, a);
+    go_few<FMT, 64>(a, st);
   else
-    hipLaunchKernelGGL((k_forward_few<FMT, 128, kWide>), grid, dim3(64 * kWide), 0, st, a);
+    go_few<FMT, 128>(a, st);
   if (a.splits > 1)
     hipLaunchKernelGGL(k_join<FMT>, dim3((unsigned)((rows * (a.dim / 4) + 255) / 256)), dim3(256), 0, st, a,
                        make_fastdiv((uint32_t)a.dim / 4), make_fastdiv((uint32_t)(rows / a.kv_heads)),

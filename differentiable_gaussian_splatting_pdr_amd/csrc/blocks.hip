@@ -100,38 +100,48 @@ Args args_of(const pdr_attention &p) {
   a.q_rows = (int)p.q_rows;
   a.k_rows = (int)p.k_rows;
   a.splits = 1;
+  a.per_tile = make_fastdiv((uint32_t)(p.batch > 0 ? p.batch : 1));
   a.group = make_fastdiv((uint32_t)(p.heads / p.kv_heads));
   a.heads = make_fastdiv((uint32_t)p.kv_heads);
   return a;
 }
 
-// Tiles of 2^log of a sequence's rows or, with offsets, of all (attention.hpp);
-// the former go into per_seq.
-int tiles_of(const pdr_attention &p, long long tokens, long long each, int log, FastDiv *per_seq) {
+// Tiles of 2^log rows, `each` to a token, of all sequences (attention.hpp).
+int tiles_of(const pdr_attention &p, long long tokens, long long each, int log) {
   if (p.q_offsets) return (int)((tokens * each >> log) + p.batch + 2);
-  const long long t = (tokens * each + (1 << log) - 1) >> log;
-  *per_seq = make_fastdiv((uint32_t)(t > 0 ? t : 1));
-  return (int)(t * p.batch);
+  return (int)(((tokens * each + (1 << log) - 1) >> log) * p.batch);
 }
+
+constexpr long long kFewBelow = 256;   // workgroups of 128 rows
+constexpr long long kFewUnits = 2048;  // workgroups of 32 rows to aim for
+constexpr long long kFewKeys = 256;    // keys of a workgroup, at least
+constexpr long long kAlone = 1024;     // keys that one workgroup takes without a join
 
 struct Plan {
   bool few;
-  int splits;
+  int waves, splits;
   size_t part_o, part_ml;  // bytes
 };
 
-// Few queries: a workgroup of 32 rows whose waves take different keys, and
-// several workgroups over the keys until the card has work.
+// Few queries, or too few workgroups of many: 32 rows to a workgroup whose waves
+// take different keys, and several workgroups over the keys until the card has
+// work.
 Plan plan_of(const pdr_attention &p) {
   const long long group = p.heads / p.kv_heads;
   const long long seqs = p.batch > 0 ? p.batch : 1;
   const long long rows = p.q_offsets ? (p.q_rows * group + seqs - 1) / seqs : p.q_rows * group;
   const long long keys = p.q_offsets ? (p.k_rows + seqs - 1) / seqs : p.k_rows;
-  Plan plan = {rows <= 32, 1, 0, 0};
+  const long long units = (rows + 31) / 32 * seqs * p.kv_heads;
+  Plan plan = {rows <= 32 || (rows + 127) / 128 * seqs * p.kv_heads < kFewBelow, 4, 1, 0, 0};
+  // a launch has fewer than 2^32 threads
+  if ((p.q_offsets ? (p.q_rows * group >> 5) + seqs + 2 : units) * p.kv_heads >= 1 << 22) plan.few = false;
   if (!plan.few || !rows) return plan;
-  const long long units = ((rows + 31) / 32) * seqs * p.kv_heads;
-  long long splits = (512 + units - 1) / units;
-  const long long most = (keys + 255) / 256;
+  if (keys <= kAlone) {
+    if (!(p.fmt == kF32 && p.dim > 64)) plan.waves = 8;
+    return plan;
+  }
+  long long splits = (kFewUnits + units - 1) / units;
+  const long long most = (keys + kFewKeys - 1) / kFewKeys;
   if (splits > most) splits = most;
   plan.splits = (int)(splits < 1 ? 1 : splits);
   if (plan.splits > 1) {
@@ -140,6 +150,24 @@ Plan plan_of(const pdr_attention &p) {
     plan.part_ml = round256(all * 8);
   }
   return plan;
+}
+
+// Parts that the rows are cut into for dk and dv, until the card has work; the
+// bytes of their sums.
+constexpr long long kKeyUnits = 512;  // workgroups of 128 keys to aim for
+constexpr long long kKeyRows = 256;   // rows of a part, at least
+int key_splits(const pdr_attention &p, size_t *bytes) {
+  *bytes = 0;
+  const long long seqs = p.batch > 0 ? p.batch : 1;
+  const long long rows = (p.q_offsets ? (p.q_rows + seqs - 1) / seqs : p.q_rows) * (p.heads / p.kv_heads);
+  const long long keys = p.q_offsets ? (p.k_rows + seqs - 1) / seqs : p.k_rows;
+  const long long units = (keys + 127) / 128 * seqs * p.kv_heads;
+  if (!p.dk || !units) return 1;
+  long long splits = (kKeyUnits + units - 1) / units;
+  if (splits > rows / kKeyRows) splits = rows / kKeyRows;
+  if (splits <= 1) return 1;
+  *bytes = round256((size_t)(p.q_offsets ? 1 : p.batch) * p.k_rows * p.kv_heads * p.dim * splits * 8);
+  return (int)splits;
 }
 
 long long tokens_of(const pdr_attention &p) { return (p.q_offsets ? 1 : p.batch) * p.q_rows; }
@@ -232,9 +260,10 @@ int pdr_attention_forward(const pdr_attention *p, void *workspace, size_t worksp
   if (rc != PDR_OK) return rc;
   if (!tokens_of(*p)) return PDR_OK;
   Args a = args_of(*p);
-  a.q_tiles = tiles_of(*p, p->q_rows, p->heads / p->kv_heads, plan.few ? attend::kLogFew : attend::kLogWide, &a.per_seq);
+  a.q_tiles = tiles_of(*p, p->q_rows, p->heads / p->kv_heads, plan.few ? attend::kLogFew : attend::kLogWide);
   if (!plan.few) return status(attend::launch_forward(a, p->fmt, (hipStream_t)stream));
   a.splits = plan.splits;
+  a.waves = plan.waves;
   a.part_o = (float *)workspace;
   a.part_ml = (float *)((char *)workspace + plan.part_o);
   return status(attend::launch_forward_few(a, p->fmt, (hipStream_t)stream));
@@ -242,7 +271,10 @@ int pdr_attention_forward(const pdr_attention *p, void *workspace, size_t worksp
 
 long long pdr_attention_backward_workspace_bytes(const pdr_attention *p) {
   const int rc = check_attention(p, true);
-  return rc != PDR_OK ? rc : (long long)(2 * row_values(*p));
+  if (rc != PDR_OK) return rc;
+  size_t parts;
+  key_splits(*p, &parts);
+  return (long long)(2 * row_values(*p) + parts);
 }
 int pdr_attention_backward(const pdr_attention *p, void *workspace, size_t workspace_bytes, void *stream) {
   const long long need = pdr_attention_backward_workspace_bytes(p);
@@ -253,14 +285,19 @@ int pdr_attention_backward(const pdr_attention *p, void *workspace, size_t works
   Args a = args_of(*p);
   a.start_s = (float *)workspace;
   a.start_dp = (float *)((char *)workspace + row_values(*p));
-  hipError_t e = attend::launch_starts(a, p->fmt, tokens_of(*p), (int)p->heads, st);
-  if (e == hipSuccess && p->dk) {
-    a.k_tiles = tiles_of(*p, p->k_rows, 1, attend::kLogWide, &a.per_seq);
-    e = attend::launch_backward_kv(a, p->fmt, st);
-  }
-  if (e == hipSuccess && p->dq && tokens_of(*p)) {
-    a.q_tiles = tiles_of(*p, p->q_rows, p->heads / p->kv_heads, attend::kLogWide, &a.per_seq);
+  a.part_k = (float *)((char *)workspace + 2 * row_values(*p));
+  hipError_t e = hipSuccess;
+  if (!p->dq) {
+    e = attend::launch_starts(a, p->fmt, tokens_of(*p), (int)p->heads, st);
+  } else if (tokens_of(*p)) {
+    a.q_tiles = tiles_of(*p, p->q_rows, p->heads / p->kv_heads, attend::kLogWide);
     e = attend::launch_backward_q(a, p->fmt, st);
+  }
+  if (e == hipSuccess && p->dk) {
+    size_t parts;
+    a.splits = key_splits(*p, &parts);
+    a.k_tiles = tiles_of(*p, p->k_rows, 1, attend::kLogWide);
+    e = attend::launch_backward_kv(a, p->fmt, st);
   }
   return status(e);
 }

@@ -134,6 +134,9 @@ def test_workspace_bytes():
     # many queries keep nothing; two values a row in the backward
     assert size("pdr_attention_forward", attention()) == 0
     assert size("pdr_attention_backward", attention()) == 2 * (2 * 100 * 8 * 4)
+    # few keys for many queries: sums of parts
+    assert size("pdr_attention_backward", attention(q_rows=4096)) > 2 * (2 * 4096 * 8 * 4)
+    assert size("pdr_attention_backward", attention(q_rows=4096, dk=None, dv=None)) == 2 * (2 * 4096 * 8 * 4)
     assert size("pdr_layer_norm_forward", norm()) == 0
     assert size("pdr_layer_norm_backward", norm(dweight=None, dbias=None)) == 0
     assert size("pdr_dropout", dropout()) == 0
