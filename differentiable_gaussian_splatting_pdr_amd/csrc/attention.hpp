@@ -35,6 +35,7 @@ using dense::kBf16;
 using dense::kF16;
 using dense::kF32;
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -57,7 +58,7 @@ struct Args {
   Mat q, k, v, o, dy, dq, dk, dv;
   const int *q_offsets, *k_offsets, *key_lengths;
   float *lse;
-  float *start_s, *start_dp;  // backward: what scores and their gradients' products start from, as lse
+  float *starts;            // backward: what scores and their gradients' products start from, pairs laid out as lse
   float *part_o, *part_ml;  // few queries: the splits' sums, and their maxima and weights
   float *part_k;            // dk and dv: the parts' sums
   float scale, scale2;      // scale, and scale log2(e)
@@ -168,6 +169,27 @@ __device__ __forceinline__ int here(int v) {
   return v;
 }
 
+// The lane's number, worked out anew rather than held in a register.
+__device__ __forceinline__ int lane_again() {
+  return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, (uint32_t)here(0)));
+}
+
+// The order that a stretch of products is to run in: AHEAD reads of LDS first, then
+// to each of MFMAS matrix instructions EACH more reads, until there are READS, and
+// VALU other instructions.  Left alone, the compiler reads a fragment, waits for it
+// and uses it, one after another.
+template <int AHEAD, int READS, int EACH, int MFMAS, int VALU = 0>
+__device__ __forceinline__ void interleave() {
+  constexpr int kMfma = 0x8, kRead = 0x100, kValu = 0x2;
+  __builtin_amdgcn_sched_group_barrier(kRead, AHEAD, 0);
+#pragma unroll
+  for (int i = 0; i < MFMAS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+    if (AHEAD + i * EACH < READS) __builtin_amdgcn_sched_group_barrier(kRead, EACH, 0);
+    if (VALU > 0) __builtin_amdgcn_sched_group_barrier(kValu, VALU, 0);
+  }
+}
+
 template <int FMT, int DP>  // DP: values a row has in LDS and registers (dim, rounded up)
 struct Core {
   static constexpr int kSize = FMT == kF32 ? 4 : 2;
@@ -178,11 +200,14 @@ struct Core {
   static constexpr int kBlocks = DP / 32;             // of 32 d
 
   // LDS: chunk c of row r is stored at chunk c ^ swizzle(r), so that the 256 bytes
-  // that are read at a time fall on different banks: eight rows' equal chunks
-  // (along), and four neighbouring chunks of each of four rows (across, whose
-  // transposing read takes 32 bytes of a row to 16 lanes).
+  // that are read at a time fall on different banks: equal chunks of sixteen rows
+  // (along: whichever rows four groups of four lanes hold, for which bit 4 is
+  // folded into bits 2 and 3), and four neighbouring chunks of each of four rows
+  // (across, whose transposing read takes 32 bytes of a row to 16 lanes).  It is
+  // linear: the swizzle of a sum without carries is that of its parts.
   static __device__ __forceinline__ constexpr int swizzle(int r) {
-    return kChunks > 8 ? (r & 3) << 2 | ((r >> 2) & 1) : ((r >> 1) & 1) << 2 | (r & 1) << 1 | ((r >> 2) & 1);
+    const int folded = ((r >> 2) & 3) ^ ((r >> 4) & 1) * 3;
+    return (kChunks > 8 ? (r & 3) << 2 : ((r >> 1) & 1) << 2) | folded;
   }
 
   static __device__ __forceinline__ f32x16 go(i32x4 a, i32x4 b, f32x16 c) {
@@ -246,9 +271,15 @@ struct Core {
       }
     }
   };
+  // Reads of LDS.  The restrict pointers tell the compiler that they do not wait for
+  // loads to LDS in flight.
+  template <class T>
+  static __device__ __forceinline__ T at_pointer(const __attribute__((address_space(3))) T *__restrict p) {
+    return *p;
+  }
   template <class T>
   static __device__ __forceinline__ T read(int at) {
-    return *(const __attribute__((address_space(3))) T *)(uintptr_t)(uint32_t)at;
+    return at_pointer((const __attribute__((address_space(3))) T *)(uintptr_t)(uint32_t)at);
   }
 
   // Rows 32 u .. 32 u + 31 of the tile.
@@ -257,10 +288,36 @@ struct Core {
     const int first = here((int)(uintptr_t)tile + at.row);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      // chunk 2 s + half: with 8 chunks in a row all of s is turned, else its bits 1 and 2
-      const int turn = kChunks > 8 ? ((s >> 1) & 3) << 6 : s << 5;
-      const int offset = kChunks > 8 ? (s & 1) * 32 + (s >> 3) * 256 : 0;
-      c = go(read<i32x4>((first ^ turn) + offset + u * 32 * kRowBytes), reg[s], c);
+      // chunk 2 s + half, of which the swizzle turns the lowest three or four bits
+      const int offset = (s >> 3) * 256 + u * 32 * kRowBytes;
+      c = go(read<i32x4>((first ^ (s & 7) << 5) + offset), reg[s], c);
+    }
+  }
+
+  // How many fragments the handwritten stretches read ahead.
+  static constexpr int kLead = 6;
+  // Fragment s of rows 0 .. 31 of a tile.
+  static __device__ __forceinline__ i32x4 chunk(int first, int s) {
+    return read<i32x4>((first ^ (s & 7) << 5) + (s >> 3) * 256);
+  }
+  // along() of rows 0 .. 31 in a fixed order (16-bit types); `meanwhile` has kSteps
+  // parts, done between the matrix instructions.
+  template <class F>
+  static __device__ __forceinline__ void along_while(f32x16 &x, const lds_char *tile, const i32x4 (&reg)[kSteps],
+                                                     const Lane &at, F meanwhile) {
+    constexpr int kAhead = kSteps < kLead ? kSteps : kLead;
+    const int first = here((int)(uintptr_t)tile + at.row);
+    i32x4 f[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) f[i] = chunk(first, i);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      x = go(f[i % kAhead], reg[i], x);
+      __builtin_amdgcn_sched_barrier(0);
+      if (i + kAhead < kSteps) f[i % kAhead] = chunk(first, i + kAhead);
+      meanwhile(i);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
@@ -292,27 +349,50 @@ struct Core {
     const int first = here((int)(uintptr_t)tile + at.column);
     if constexpr (FMT != kF32) {
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        const int lo = (first ^ b << 6) + x * 16 * kRowBytes;
-        const s16x4 y = transposed((lds_s16x4 *)(uintptr_t)(uint32_t)lo);
-        const s16x4 z = transposed((lds_s16x4 *)(uintptr_t)(uint32_t)(lo + 8 * kRowBytes));
-        c[b] = go(__builtin_bit_cast(i32x4, __builtin_shufflevector(y, z, 0, 1, 2, 3, 4, 5, 6, 7)), p.w[0], c[b]);
-      }
+      for (int b = 0; b < kBlocks; ++b) c[b] = go(column(first, x, b), p.w[0], c[b]);
     } else {
-      // row 8 (e / 4) + 4 half + e % 4: of its swizzle, bits 2 and 3 are e's
+      // row 16 x + 8 (e / 4) + e % 4, and 4 half more
 #pragma unroll
       for (int e = 0; e < 8; ++e)
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
-          const float f = read<float>((first ^ (e & 1) << 6) + (x * 16 + 8 * (e >> 2) + (e & 3)) * kRowBytes +
-                                      (b ^ ((e >> 1) & 1)) * 128);
+          const int row = x * 16 + 8 * (e >> 2) + (e & 3), turn = swizzle(row);
+          const float f = read<float>((first ^ (turn & 7) << 4) + row * kRowBytes + (b ^ turn >> 3) * 128);
           c[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(f, __int_as_float(p.w[e >> 2][e & 3]), c[b], 0, 0, 0);
         }
     }
   }
+  // Fragment b of those rows (16-bit types).
+  static __device__ __forceinline__ i32x4 column(int first, int x, int b) {
+    const int lo = (first ^ b << 6 ^ swizzle(x * 16) << 4) + x * 16 * kRowBytes;
+    const int hi = (first ^ b << 6 ^ swizzle(x * 16 + 8) << 4) + (x * 16 + 8) * kRowBytes;
+    const s16x4 y = transposed((lds_s16x4 *)(uintptr_t)(uint32_t)lo);
+    const s16x4 z = transposed((lds_s16x4 *)(uintptr_t)(uint32_t)hi);
+    return __builtin_bit_cast(i32x4, __builtin_shufflevector(y, z, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  // across() of rows 0 .. 31 under weights p, in a fixed order.
+  static __device__ __forceinline__ void across_rows(f32x16 (&c)[kBlocks], const lds_char *tile, const f32x16 &p,
+                                                       const Lane &at) {
+    constexpr int kAll = 2 * kBlocks, kAhead = kAll < kLead ? kAll : kLead;
+    const int first = here((int)(uintptr_t)tile + at.column);
+    const Weights weights[2] = {pack(p, 0), pack(p, 8)};
+    i32x4 f[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) f[i] = column(first, i / kBlocks, i % kBlocks);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kAll; ++i) {
+      c[i % kBlocks] = go(f[i % kAhead], weights[i / kBlocks].w[0], c[i % kBlocks]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (i + kAhead < kAll) {
+        f[i % kAhead] = column(first, (i + kAhead) / kBlocks, (i + kAhead) % kBlocks);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+
   // ds_read_b64_tr_b16: of each 16 lanes' 4 rows of 16 values (a row is four
-  // lanes' 8 bytes), lane t receives column t.  The restrict pointer tells the
-  // compiler that the read does not wait for loads to LDS in flight.
+  // lanes' 8 bytes), lane t receives column t.
   static __device__ __forceinline__ s16x4 transposed(lds_s16x4 *__restrict p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
   }
@@ -341,13 +421,15 @@ struct Loader {
     row0 = wave * kRowsEach + lane / C::kChunks;
     chunk0 = (lane % C::kChunks) ^ C::swizzle(row0);
   }
-  // The i-th load's row, and its byte in the row or kOutside.  The rows between
+  // The i-th load's row, and its byte in the row or kOutside (whose bit stays when
+  // it is added to a place below 2^31).  The rows between
   // two loads are a power of two that row0 stays below, so their swizzles add up.
   __device__ __forceinline__ int row_of(int i) const { return row0 + i * NW * kRowsEach; }
   __device__ __forceinline__ uint32_t byte_of(int i) const {
     const int c = chunk0 ^ C::swizzle(i * NW * kRowsEach);
     return c * C::kPer < dim ? (uint32_t)c * 16u : kOutside;
   }
+  static __device__ __forceinline__ uint32_t outside(bool v) { return v ? kOutside : 0u; }
   __device__ __forceinline__ void issue(const char *from, uint32_t off, lds_char *lds, int i) const {
     const __amdgpu_buffer_rsrc_t rsrc =
         __builtin_amdgcn_make_buffer_rsrc((void *)from, 0, (int)kOutside, 0x00020000);
@@ -359,8 +441,8 @@ struct Loader {
     const char *const from = x.base + (long long)first * x.row;
 #pragma unroll
     for (int i = 0; i < kIssues; ++i) {
-      const uint32_t r = (uint32_t)row_of(i), c = byte_of(i);
-      issue(from, first + (int)r < rows && c != kOutside ? r * x.row + c : kOutside, lds, i);
+      const uint32_t r = (uint32_t)row_of(i);
+      issue(from, (r * x.row + byte_of(i)) | outside(first + (int)r >= rows), lds, i);
     }
   }
   // The same, of two tensors.
@@ -369,13 +451,23 @@ struct Loader {
     const char *const from_y = y.base + (long long)first * y.row;
 #pragma unroll
     for (int i = 0; i < kIssues; ++i) {
-      const uint32_t r = (uint32_t)row_of(i), c = byte_of(i);
-      const bool in = first + (int)r < rows && c != kOutside;
-      issue(from_x, in ? r * x.row + c : kOutside, lds, i);
-      issue(from_y, in ? r * y.row + c : kOutside, lds + kBytes, i);
+      const uint32_t r = (uint32_t)row_of(i), c = byte_of(i), out = outside(first + (int)r >= rows);
+      issue(from_x, (r * x.row + c) | out, lds, i);
+      issue(from_y, (r * y.row + c) | out, lds + kBytes, i);
     }
   }
-  // The same of a group's rows.
+  // The same of a group's rows, of one tensor and of two.
+  __device__ __forceinline__ void grouped(const Source &x, int first, int rows, const FastDiv &group,
+                                          lds_char *lds) const {
+    const int token0 = (int)fdiv((uint32_t)first, group);
+    const char *const from = x.base + (long long)token0 * x.row;
+#pragma unroll
+    for (int i = 0; i < kIssues; ++i) {
+      const int r = first + row_of(i);
+      const uint32_t token = fdiv((uint32_t)r, group), g = (uint32_t)r - token * group.d;
+      issue(from, ((token - token0) * x.row + g * x.head + byte_of(i)) | outside(r >= rows), lds, i);
+    }
+  }
   __device__ __forceinline__ void grouped(const Source &x, const Source &y, int first, int rows,
                                           const FastDiv &group, lds_char *lds) const {
     const int token0 = (int)fdiv((uint32_t)first, group);
@@ -385,9 +477,9 @@ struct Loader {
     for (int i = 0; i < kIssues; ++i) {
       const int r = first + row_of(i);
       const uint32_t c = byte_of(i), token = fdiv((uint32_t)r, group), g = (uint32_t)r - token * group.d;
-      const bool in = r < rows && c != kOutside;
-      issue(from_x, in ? (token - token0) * x.row + g * x.head + c : kOutside, lds, i);
-      issue(from_y, in ? (token - token0) * y.row + g * y.head + c : kOutside, lds + kBytes, i);
+      const uint32_t out = outside(r >= rows);
+      issue(from_x, ((token - token0) * x.row + g * x.head + c) | out, lds, i);
+      issue(from_y, ((token - token0) * y.row + g * y.head + c) | out, lds + kBytes, i);
     }
   }
 };

@@ -67,8 +67,7 @@ __global__ __launch_bounds__(256) void k_starts(Args a, FastDiv heads, long long
   const long long tokens = total / heads.d;
   if (lane == 0) {
     const long long to = (kv * tokens + token) * a.group.d + g;
-    a.start_dp[to] = -s;
-    a.start_s[to] = start_of<FMT>(a.lse[to], a.scale2);
+    *(float2 *)(a.starts + 2 * to) = make_float2(start_of<FMT>(a.lse[to], a.scale2), -s);
   }
 }
 
@@ -173,10 +172,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
     const long long i =
         (head * tokens + (a.q_offsets ? 0 : (long long)at.seq * a.q_rows) + at.q0) * group + row;
     start_s = start_of<FMT>(a.lse[i], a.scale2);
-    if (half == 0) {
-      a.start_s[i] = start_s;
-      a.start_dp[i] = start_dp;
-    }
+    if (half == 0) *(float2 *)(a.starts + 2 * i) = make_float2(start_s, start_dp);
   }
   f32x16 sums[C::kBlocks];
 #pragma unroll
@@ -206,6 +202,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
       fill(dp, start_dp);
       C::along(s, sk, u, q, lanes);
       C::along(dp, sv, u, dy, lanes);
+      if constexpr (FMT != kF32) interleave<6, 2 * C::kSteps, 1, 2 * C::kSteps>();
       const int key0 = t * kKeys + u * 32;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
@@ -221,6 +218,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
       }
       scaled.hold(s, sums);
       across32<C>(sums, sk, u, s, lanes);
+      if constexpr (FMT != kF32) interleave<8, 4 * C::kBlocks, 2, 2 * C::kBlocks>();
     }
   }
   if (!there) return;
@@ -228,6 +226,24 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
                         a.dq.p + (first_of(a.dq, at, at.q0 + token, head * group) + in_group * a.dq.head) * C::kSize,
                         a.dim, half, a.scale * scaled.out());
 #endif
+}
+
+// Sums of a key to dk (which = 0) or dv, or to the parts' sums:
+// [part][dk, dv][key head][key][dim].
+template <class C, int FMT>
+__device__ __forceinline__ void store_keys(const Args &a, const Place &at, const Mat &to, int which, int head,
+                                           int key, const f32x16 (&c)[C::kBlocks], int half, float by) {
+  const long long where = at.k0 + key;
+  if (a.splits > 1) {
+    const long long all = (a.q_offsets ? 1LL : a.batch) * a.k_rows;
+    const long long mine = (a.q_offsets ? 0 : (long long)at.seq * a.k_rows) + where;
+    using P = Core<kF32, C::kBlocks * 32>;
+    store_columns<P, kF32>(
+        c, (char *)(a.part_k + (((2LL * blockIdx.y + which) * a.kv_heads + head) * all + mine) * a.dim), a.dim, half,
+        by);
+    return;
+  }
+  store_columns<C, FMT>(c, to.p + (at.seq * to.batch + where * to.row + head * to.head) * C::kSize, a.dim, half, by);
 }
 
 // dk and dv: 128 keys to a workgroup, 32 to a wave; the waves share tiles of
@@ -280,20 +296,24 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_kv(Args a
   scaled.init();
   const Source from_q(a.q, first_of(a.q, at, at.q0, head * group), C::kSize);
   const Source from_dy(a.dy, first_of(a.dy, at, at.q0, head * group), C::kSize);
-  L loader;
-  loader.init(a.dim, wave, lane);
   const long long tokens = a.q_offsets ? a.q_rows : (long long)a.batch * a.q_rows;
   const long long first =
       (head * tokens + (a.q_offsets ? 0 : (long long)at.seq * a.q_rows) + at.q0) * group;
+  // What only this and the ends need of a lane's number is worked out each time: with
+  // two waves on a SIMD there is no register to hold it, and what is fetched back
+  // from scratch memory waits for all loads in flight.
   auto load = [&](int t, lds_char *stage) {
+    const int lane = lane_again();
+    L loader;
+    loader.init(a.dim, wave, lane);
     loader.grouped(from_q, from_dy, t * kRows, rows, a.group, stage);
-    const float *src = wave == 0 ? a.start_s : a.start_dp;  // one wave each
     const __amdgpu_buffer_rsrc_t rsrc =
-        __builtin_amdgcn_make_buffer_rsrc((void *)(src + first + t * kRows), 0, kRows * 4, 0x00020000);
+        __builtin_amdgcn_make_buffer_rsrc((void *)(a.starts + 2 * (first + t * kRows)), 0, kRows * 8, 0x00020000);
+    // one wave each
     if (wave < 2)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rsrc, (lds_void *)(stage + 2 * L::kBytes + wave * (kRows * 4)), 4,
-          t * kRows + lane < rows ? lane * 4 : (int)kOutside, 0, 0, 0);
+          (lane * 8 + wave * 4) | (int)L::outside(t * kRows + lane >= rows), 0, 0, 0);
   };
   if (begin < end) load(begin, smem);
   for (int t = begin; t < end; ++t) {
@@ -322,6 +342,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_kv(Args a
         dp[r] = ds;
       }
       if (r0 < plain || r0 + 32 > rows) {
+        const int lane = lane_again(), half = lane >> 5, key = key0 + wave * 32 + (lane & 31);
         const int first = here(first_row(key) - r0 - 4 * half), last = here(rows - r0 - 4 * half);
 #pragma unroll
         for (int r = 0; r < 16; ++r)
@@ -332,24 +353,11 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_kv(Args a
       across32<C>(dk, sq, u, dp, lanes);
     }
   }
-  if (key >= at.stored) return;
-  const float by_k = there ? a.scale * scaled.out() : 0.f;
-  const float by_v = there ? (FMT == kF16 ? ldexpf(1.f, -kShift) : 1.f) : 0.f;
-  const long long where = at.k0 + key;
-  if (a.splits > 1) {
-    // [part][dk, dv][key head][key][dim]
-    const long long all = (a.q_offsets ? 1LL : a.batch) * a.k_rows;
-    const long long mine = (a.q_offsets ? 0 : (long long)at.seq * a.k_rows) + where;
-    float *const to = a.part_k + ((2LL * blockIdx.y * a.kv_heads + head) * all + mine) * a.dim;
-    using P = Core<kF32, DP>;
-    store_columns<P, kF32>(dk, (char *)to, a.dim, half, by_k);
-    store_columns<P, kF32>(dv, (char *)(to + a.kv_heads * all * a.dim), a.dim, half, by_v);
-    return;
-  }
-  store_columns<C, FMT>(dk, a.dk.p + (at.seq * a.dk.batch + where * a.dk.row + head * a.dk.head) * C::kSize,
-                        a.dim, half, by_k);
-  store_columns<C, FMT>(dv, a.dv.p + (at.seq * a.dv.batch + where * a.dv.row + head * a.dv.head) * C::kSize,
-                        a.dim, half, by_v);
+  const int lane_now = lane_again(), half_now = lane_now >> 5, key_now = key0 + wave * 32 + (lane_now & 31);
+  if (key_now >= at.stored) return;
+  const bool is_key = key_now < at.nk;
+  store_keys<C, FMT>(a, at, a.dk, 0, head, key_now, dk, half_now, is_key ? a.scale * scaled.out() : 0.f);
+  store_keys<C, FMT>(a, at, a.dv, 1, head, key_now, dv, half_now, is_key ? (FMT == kF16 ? ldexpf(1.f, -kShift) : 1.f) : 0.f);
 #endif
 }
 

@@ -11,7 +11,10 @@ namespace attend {
 namespace {
 
 // The running softmax of a lane's query, in units of log2, and the sums of
-// values under its maximum.
+// values under it.  `most` follows the maximum only when that has grown by more
+// than kSlack: weights of up to 2^8 are as good as those up to 1, in sums of fp32
+// and in fp16's range, and nearly all tiles are spared a pass over the sums.
+constexpr float kSlack = 8.f;
 template <class C>
 struct Query {
   f32x16 out[C::kBlocks];
@@ -23,7 +26,7 @@ struct Query {
 #pragma unroll
     for (int b = 0; b < C::kBlocks; ++b) clear(out[b]);
   }
-  // Scores of 32 N keys to weights, in place; everything so far to their maximum.
+  // Scores of 32 N keys to weights, in place.
   template <int N>
   __device__ __forceinline__ void weigh(f32x16 (&s)[N], float scale2) {
     float m = s[0][0];
@@ -31,15 +34,18 @@ struct Query {
     for (int u = 0; u < N; ++u)
 #pragma unroll
       for (int r = 0; r < 16; ++r) m = fmaxf(m, s[u][r]);
-    m = fmaxf(most, fmaxf(m, other_half(m)) * scale2);
-    const float from = m == -INFINITY ? 0.f : m;  // nothing seen yet
-    const float down = exp2_(most - from);
-    most = m;
-    sum *= down;
+    m = fmaxf(m, other_half(m)) * scale2;
+    if (__any(m > most + kSlack)) {
+      // a lane that has seen nothing yet has no sums
+      const float up = fmaxf(most, m), down = up == -INFINITY ? 1.f : exp2_(most - up);
+      most = up;
+      sum *= down;
 #pragma unroll
-    for (int b = 0; b < C::kBlocks; ++b)
+      for (int b = 0; b < C::kBlocks; ++b)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) out[b][r] *= down;
+        for (int r = 0; r < 16; ++r) out[b][r] *= down;
+    }
+    const float from = most == -INFINITY ? 0.f : most;  // nothing seen yet
 #pragma unroll
     for (int u = 0; u < N; ++u)
 #pragma unroll
@@ -151,6 +157,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_forward(Args a) {
       clear(s[u]);
       C::along(s[u], sk, u, q, lanes);
     }
+    if constexpr (FMT != kF32) interleave<6, 2 * C::kSteps, 1, 2 * C::kSteps>();
     if ((t + 1) * kKeys > plain) {
       const int seen = here(row.seen - t * kKeys - 4 * half);
 #pragma unroll
@@ -158,6 +165,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_forward(Args a) {
     }
     query.template weigh<2>(s, a.scale2);
     query.template take<2>(sv, s, lanes);
+    if constexpr (FMT != kF32) interleave<8, 8 * C::kBlocks, 2, 4 * C::kBlocks>();
   }
   const float sum = query.sum + other_half(query.sum);
   if (!row.there) return;

@@ -283,8 +283,7 @@ int pdr_attention_backward(const pdr_attention *p, void *workspace, size_t works
   if (rc != PDR_OK) return rc;
   const hipStream_t st = (hipStream_t)stream;
   Args a = args_of(*p);
-  a.start_s = (float *)workspace;
-  a.start_dp = (float *)((char *)workspace + row_values(*p));
+  a.starts = (float *)workspace;
   a.part_k = (float *)((char *)workspace + 2 * row_values(*p));
   hipError_t e = hipSuccess;
   if (!p->dq) {
