@@ -11,12 +11,27 @@ dimension is packed (anything else is copied first).
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
 from .dense import _call, _check, _differentiated, _ld, _rows
 from .splat import _FMT
+
+
+
+def _once(backward):
+    """once_differentiable, without its gradient mode's switch where that is off already
+    (it takes some microseconds of autograd's thread)."""
+    checked = once_differentiable(backward)
+
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        return (checked if torch.is_grad_enabled() else backward)(ctx, *grads)
+    return run
+
 
 # ---------------------------------------------------------------- attention
 
@@ -39,44 +54,43 @@ def _heads(t: torch.Tensor) -> torch.Tensor:
     return t
 
 
-def _place(a, name: str, t: torch.Tensor):
-    """The fields of a tensor [batch, tokens, heads, D] or [tokens, heads, D]."""
+def _place(t):
+    """(pointer, row, head, batch) of [batch, tokens, heads, D] or [tokens, heads, D]."""
+    if t is None:
+        return None, 0, 0, 0
     strides = t.stride()
-    setattr(a, name, t.data_ptr())
-    setattr(a, name + "_row", strides[-3])
-    setattr(a, name + "_head", strides[-2])
-    setattr(a, name + "_batch", strides[0] if t.dim() == 4 else 0)
+    if len(strides) == 4:
+        return t.data_ptr(), strides[1], strides[2], strides[0]
+    return t.data_ptr(), strides[0], strides[1], 0
 
 
-def _attention_args(q, k, v, causal, scale, offsets, key_offsets, key_lengths):
-    a = _lib.pdr_attention()
-    a.fmt, a.causal, a.scale = _FMT[q.dtype], causal, scale
-    a.heads, a.kv_heads, a.dim = q.shape[-2], k.shape[-2], q.shape[-1]
-    a.q_rows, a.k_rows = q.shape[-3], k.shape[-3]
-    if offsets is None:
-        a.batch = q.shape[0]
-        if key_lengths is not None:
-            a.key_lengths = key_lengths.data_ptr()
-    else:
-        a.batch = offsets.shape[0] - 1
-        a.q_offsets, a.k_offsets = offsets.data_ptr(), key_offsets.data_ptr()
-    _place(a, "q", q)
-    _place(a, "k", k)
-    _place(a, "v", v)
-    return a
+def _attention_args(q, k, v, o, lse, meta, index, dy=None, dq=None, dk=None, dv=None):
+    """pdr_attention of tensors that _heads has seen; index: (offsets, key_offsets, key_lengths)."""
+    offsets, key_offsets, key_lengths = index
+    batch = q.shape[0] if offsets is None else offsets.shape[0] - 1
+    causal, scale = meta
+    # in the struct's order
+    return _lib.pdr_attention(
+        _FMT[q.dtype], causal, batch, q.shape[-2], k.shape[-2], q.shape[-1], q.shape[-3], k.shape[-3],
+        None if offsets is None else offsets.data_ptr(),
+        None if offsets is None else key_offsets.data_ptr(),
+        None if key_lengths is None else key_lengths.data_ptr(), scale,
+        *_place(q), *_place(k), *_place(v), *_place(o), None if lse is None else lse.data_ptr(),
+        *_place(dy), *_place(dq), *_place(dk), *_place(dv))
 
 
-def _attention_forward(q, k, v, causal, scale, offsets, key_offsets, key_lengths, keep):
+def _packed(t):
+    """Room for a result of t's shape."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _attention_forward(q, k, v, meta, index, keep):
     """(o, lse) of tensors that _heads has seen; lse only with `keep`."""
-    a = _attention_args(q, k, v, causal, scale, offsets, key_offsets, key_lengths)
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _place(a, "o", o)
-    lse = None
+    o, lse = _packed(q), None
     if keep:
-        lse = torch.empty((a.kv_heads, q.shape[:-2].numel(), a.heads // a.kv_heads),
+        lse = torch.empty((k.shape[-2], q.shape[:-2].numel(), q.shape[-2] // k.shape[-2]),
                           dtype=torch.float32, device=q.device)
-        a.lse = lse.data_ptr()
-    _call("pdr_attention_forward", a, q.device)
+    _call("pdr_attention_forward", _attention_args(q, k, v, o, lse, meta, index), q.device)
     return o, lse
 
 
@@ -89,36 +103,26 @@ class Attention(torch.autograd.Function):
     row's log of the sum of exponentials for the backward."""
 
     @staticmethod
-    def forward(ctx, q, k, v, causal, scale, offsets, key_offsets, key_lengths):
+    def forward(ctx, q, k, v, meta, *index):
         d = q.shape[-1]
         q, k, v = _heads(q), _heads(k), _heads(v)
-        o, lse = _attention_forward(q, k, v, causal, scale, offsets, key_offsets, key_lengths, True)
-        ctx.save_for_backward(q, k, v, o, lse, offsets, key_offsets, key_lengths)
-        ctx.meta = (causal, scale, d)
+        o, lse = _attention_forward(q, k, v, meta, index, True)
+        ctx.save_for_backward(q, k, v, o, lse, *index)
+        ctx.meta = (meta, d)
         return _to_dim(o, d)
 
     @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, dy):
-        q, k, v, o, lse, offsets, key_offsets, key_lengths = ctx.saved_tensors
-        causal, scale, d = ctx.meta
-        a = _attention_args(q, k, v, causal, scale, offsets, key_offsets, key_lengths)
-        dy = _heads(dy)
-        _place(a, "o", o)
-        _place(a, "dy", dy)
-        a.lse = lse.data_ptr()
-        dq = dk = dv = None
-        if ctx.needs_input_grad[0]:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            _place(a, "dq", dq)
-        if ctx.needs_input_grad[1] or ctx.needs_input_grad[2]:
-            dk, dv = (torch.empty(k.shape, dtype=k.dtype, device=k.device) for _ in range(2))
-            _place(a, "dk", dk)
-            _place(a, "dv", dv)
-        _call("pdr_attention_backward", a, q.device)
+        q, k, v, o, lse, *index = ctx.saved_tensors
+        meta, d = ctx.meta
         need = ctx.needs_input_grad
+        dq = _packed(q) if need[0] else None
+        dk, dv = (_packed(k), _packed(v)) if need[1] or need[2] else (None, None)
+        dy = _heads(dy)
+        _call("pdr_attention_backward", _attention_args(q, k, v, o, lse, meta, index, dy, dq, dk, dv), q.device)
         return (*(_to_dim(g, d) if n else None for g, n in zip((dq, dk, dv), need)),
-                None, None, None, None, None)
+                None, None, None, None)
 
 
 def _check_index(name: str, t, like, length=None):
@@ -178,36 +182,27 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
             raise ValueError("offsets must have a value more than there are sequences")
         key_offsets = (offsets if key_offsets is None
                        else _check_index("key_offsets", key_offsets, q, offsets.shape[0]))
-    rest = (bool(causal), scale, offsets, key_offsets, key_lengths)
+    meta, index = (bool(causal), scale), (offsets, key_offsets, key_lengths)
     if _differentiated(q, k, v):
-        return Attention.apply(q, k, v, *rest)
-    return _to_dim(_attention_forward(_heads(q), _heads(k), _heads(v), *rest, False)[0], d)
+        return Attention.apply(q, k, v, meta, *index)
+    return _to_dim(_attention_forward(_heads(q), _heads(k), _heads(v), meta, index, False)[0], d)
 
 
 # --------------------------------------------------------------- layer norm
 
-def _norm_args(x, weight, eps):
-    a = _lib.pdr_layer_norm()
-    a.fmt, a.eps = _FMT[x.dtype], eps
-    a.rows, a.cols = x.shape
-    a.x, a.ldx = x.data_ptr(), _ld(x)
-    if weight is not None:
-        a.weight = weight.data_ptr()
-    return a
+def _pointer(t):
+    return None if t is None else t.data_ptr()
 
 
 def _norm_forward(x, weight, bias, eps, keep):
     """(y, stats); stats only with `keep`."""
-    a = _norm_args(x, weight, eps)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    a.y, a.ldy = y.data_ptr(), max(a.cols, 1)
-    if bias is not None:
-        a.bias = bias.data_ptr()
-    stats = None
+    rows, cols = x.shape
+    y, stats = _packed(x), None
     if keep:
-        stats = torch.empty((a.rows, 2), dtype=torch.float32, device=x.device)
-        a.stats = stats.data_ptr()
-    _call("pdr_layer_norm_forward", a, x.device)
+        stats = torch.empty((rows, 2), dtype=torch.float32, device=x.device)
+    _call("pdr_layer_norm_forward",
+          _lib.pdr_layer_norm(_FMT[x.dtype], rows, cols, eps, x.data_ptr(), _ld(x), _pointer(weight), _pointer(bias),
+                              y.data_ptr(), cols or 1, _pointer(stats)), x.device)
     return y, stats
 
 
@@ -222,25 +217,19 @@ class LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, dy):
         x, weight, stats = ctx.saved_tensors
-        a = _norm_args(x, weight, ctx.eps)
-        rows = _rows(dy)
-        a.dy, a.lddy = rows.data_ptr(), _ld(rows)
-        a.stats = stats.data_ptr()
         need = ctx.needs_input_grad
-        dx = dw = db = None
-        if need[0]:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            a.dx, a.lddx = dx.data_ptr(), max(a.cols, 1)
-        if need[1]:
-            dw = torch.empty((a.cols,), dtype=x.dtype, device=x.device)
-            a.dweight = dw.data_ptr()
-        if need[2]:
-            db = torch.empty((a.cols,), dtype=x.dtype, device=x.device)
-            a.dbias = db.data_ptr()
-        _call("pdr_layer_norm_backward", a, x.device)
+        rows, cols = x.shape
+        dy = _rows(dy)
+        dx = _packed(x) if need[0] else None
+        dw = _packed(weight) if need[1] else None
+        db = torch.empty((cols,), dtype=x.dtype, device=x.device) if need[2] else None
+        _call("pdr_layer_norm_backward",
+              _lib.pdr_layer_norm(_FMT[x.dtype], rows, cols, ctx.eps, x.data_ptr(), _ld(x), _pointer(weight), None,
+                                  None, 0, stats.data_ptr(), dy.data_ptr(), _ld(dy), _pointer(dx), cols or 1,
+                                  _pointer(dw), _pointer(db)), x.device)
         return dx, dw, db, None
 
 
@@ -272,19 +261,13 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
 # ------------------------------------------------------------------ dropout
 
 def _dropout(x, residual, p, seed, offset):
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    a = _lib.pdr_dropout_args()
-    a.fmt, a.p, a.offset = _FMT[x.dtype], p, offset
-    a.rows, a.cols = x.shape
-    if isinstance(seed, torch.Tensor):
-        a.seed_at = seed.data_ptr()
-    else:
-        a.seed = seed
-    a.x, a.ldx = x.data_ptr(), _ld(x)
-    a.y, a.ldy = y.data_ptr(), max(a.cols, 1)
-    if residual is not None:
-        a.res, a.ldr = residual.data_ptr(), _ld(residual)
-    _call("pdr_dropout", a, x.device)
+    y = _packed(x)
+    rows, cols = x.shape
+    whole = not isinstance(seed, torch.Tensor)
+    _call("pdr_dropout",
+          _lib.pdr_dropout_args(_FMT[x.dtype], rows, cols, p, seed if whole else 0, offset,
+                                None if whole else seed.data_ptr(), x.data_ptr(), _ld(x), _pointer(residual),
+                                0 if residual is None else _ld(residual), y.data_ptr(), cols or 1), x.device)
     return y
 
 
@@ -302,7 +285,7 @@ class Dropout(torch.autograd.Function):
         return _dropout(x, residual, p, seed, offset)
 
     @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, dy):
         seed = ctx.saved_tensors[0] if ctx.seed is None else ctx.seed
         p, offset = ctx.meta

@@ -190,6 +190,9 @@ __device__ __forceinline__ void interleave() {
   }
 }
 
+// Row of a result's register r in this half.
+__device__ __forceinline__ int row_in(int r, int half) { return 8 * (r >> 2) + 4 * half + (r & 3); }
+
 template <int FMT, int DP>  // DP: values a row has in LDS and registers (dim, rounded up)
 struct Core {
   static constexpr int kSize = FMT == kF32 ? 4 : 2;
@@ -294,33 +297,6 @@ struct Core {
     }
   }
 
-  // How many fragments the handwritten stretches read ahead.
-  static constexpr int kLead = 6;
-  // Fragment s of rows 0 .. 31 of a tile.
-  static __device__ __forceinline__ i32x4 chunk(int first, int s) {
-    return read<i32x4>((first ^ (s & 7) << 5) + (s >> 3) * 256);
-  }
-  // along() of rows 0 .. 31 in a fixed order (16-bit types); `meanwhile` has kSteps
-  // parts, done between the matrix instructions.
-  template <class F>
-  static __device__ __forceinline__ void along_while(f32x16 &x, const lds_char *tile, const i32x4 (&reg)[kSteps],
-                                                     const Lane &at, F meanwhile) {
-    constexpr int kAhead = kSteps < kLead ? kSteps : kLead;
-    const int first = here((int)(uintptr_t)tile + at.row);
-    i32x4 f[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) f[i] = chunk(first, i);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      x = go(f[i % kAhead], reg[i], x);
-      __builtin_amdgcn_sched_barrier(0);
-      if (i + kAhead < kSteps) f[i % kAhead] = chunk(first, i + kAhead);
-      meanwhile(i);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-
   // Eight registers of an along() as the second operand of across().
   struct Weights {
     i32x4 w[FMT == kF32 ? 2 : 1];
@@ -351,16 +327,18 @@ struct Core {
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) c[b] = go(column(first, x, b), p.w[0], c[b]);
     } else {
-      // row 16 x + 8 (e / 4) + e % 4, and 4 half more
 #pragma unroll
       for (int e = 0; e < 8; ++e)
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-          const int row = x * 16 + 8 * (e >> 2) + (e & 3), turn = swizzle(row);
-          const float f = read<float>((first ^ (turn & 7) << 4) + row * kRowBytes + (b ^ turn >> 3) * 128);
-          c[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(f, __int_as_float(p.w[e >> 2][e & 3]), c[b], 0, 0, 0);
-        }
+        for (int b = 0; b < kBlocks; ++b)
+          c[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(value(first, x, e, b), __int_as_float(p.w[e >> 2][e & 3]), c[b], 0,
+                                                      0, 0);
     }
+  }
+  // fp32: a value of row 16 x + 8 (e / 4) + e % 4, and 4 half more, of block b.
+  static __device__ __forceinline__ float value(int first, int x, int e, int b) {
+    const int row = x * 16 + 8 * (e >> 2) + (e & 3), turn = swizzle(row);
+    return read<float>((first ^ (turn & 7) << 4) + row * kRowBytes + (b ^ turn >> 3) * 128);
   }
   // Fragment b of those rows (16-bit types).
   static __device__ __forceinline__ i32x4 column(int first, int x, int b) {
@@ -370,24 +348,77 @@ struct Core {
     const s16x4 z = transposed((lds_s16x4 *)(uintptr_t)(uint32_t)hi);
     return __builtin_bit_cast(i32x4, __builtin_shufflevector(y, z, 0, 1, 2, 3, 4, 5, 6, 7));
   }
-  // across() of rows 0 .. 31 under weights p, in a fixed order.
-  static __device__ __forceinline__ void across_rows(f32x16 (&c)[kBlocks], const lds_char *tile, const f32x16 &p,
-                                                       const Lane &at) {
-    constexpr int kAll = 2 * kBlocks, kAhead = kAll < kLead ? kAll : kLead;
+  // ---- what is not finite where a mask hides it
+  //
+  // A weight of zero does not hide an infinity or a NaN: their product is NaN.  Where
+  // a tile is masked it is looked through, and if there are any, across_careful()
+  // sums the finite values and then adds the others where they are seen.
+  static __device__ __forceinline__ bool finite(i32x4 v) {
+    uint32_t bad = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= not_finite((uint32_t)v[i]);
+    return bad == 0;
+  }
+  // The bits of a word's values that are not finite.
+  static __device__ __forceinline__ uint32_t not_finite(uint32_t v) {
+    if constexpr (FMT == kF32) return (v & 0x7f800000u) == 0x7f800000u ? ~0u : 0u;
+    constexpr uint32_t kExp = FMT == kBf16 ? 0x7f80u : 0x7c00u;
+    return ((v & kExp) == kExp ? 0xffffu : 0u) | ((v >> 16 & kExp) == kExp ? 0xffff0000u : 0u);
+  }
+  // Whether rows 32 u .. 32 u + 31 hold any (the same for all lanes).
+  static __device__ __forceinline__ bool any_not_finite(const lds_char *tile, int u, int lane) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 32 * kRowBytes / 1024; ++i)
+      bad |= !finite(read<i32x4>((int)(uintptr_t)tile + u * 32 * kRowBytes + i * 1024 + lane * 16));
+    return __any(bad);
+  }
+  // across() of rows 32 u .. 32 u + 31 under weights w; this lane's column sees rows
+  // [low, high) of them.
+  static __device__ __forceinline__ void across_careful(f32x16 (&c)[kBlocks], const lds_char *tile, int u,
+                                                        const f32x16 &w, const Lane &at, int half, int low, int high) {
     const int first = here((int)(uintptr_t)tile + at.column);
-    const Weights weights[2] = {pack(p, 0), pack(p, 8)};
-    i32x4 f[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) f[i] = column(first, i / kBlocks, i % kBlocks);
-    __builtin_amdgcn_sched_barrier(0);
+    for (int x = 0; x < 2; ++x) {
+      const Weights p = pack(w, 8 * x);
+      if constexpr (FMT != kF32) {
 #pragma unroll
-    for (int i = 0; i < kAll; ++i) {
-      c[i % kBlocks] = go(f[i % kAhead], weights[i / kBlocks].w[0], c[i % kBlocks]);
-      __builtin_amdgcn_sched_barrier(0);
-      if (i + kAhead < kAll) {
-        f[i % kAhead] = column(first, (i + kAhead) / kBlocks, (i + kAhead) % kBlocks);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int b = 0; b < kBlocks; ++b) {
+          i32x4 f = column(first, 2 * u + x, b);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] &= (int)~not_finite((uint32_t)f[i]);
+          c[b] = go(f, p.w[0], c[b]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) {
+            float f = value(first, 2 * u + x, e, b);
+            f = not_finite(__float_as_uint(f)) ? 0.f : f;
+            c[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(f, __int_as_float(p.w[e >> 2][e & 3]), c[b], 0, 0, 0);
+          }
       }
+    }
+#pragma unroll 1
+    for (int row = 0; row < 32; ++row) {
+      const int place = (int)(uintptr_t)tile + (u * 32 + row) * kRowBytes;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const int byte = (b * 32 + row_in(r, half)) * kSize;
+          const int from = place + ((byte >> 4 ^ swizzle(row)) << 4) + (byte & 15);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v;
+            if constexpr (FMT == kF32)
+              v = read<float>(from + 4 * i);
+            else
+              v = dense::to_f<FMT>((uint16_t)read<short>(from + 2 * i));
+            if (row >= low && row < high && !(fabsf(v) < INFINITY)) c[b][r + i] += v;
+          }
+        }
     }
   }
 
@@ -497,9 +528,6 @@ __device__ __forceinline__ void all_landed() {
 
 // The value of the lane 32 further on (or back).
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
-
-// Row of a result's register r in this half.
-__device__ __forceinline__ int row_in(int r, int half) { return 8 * (r >> 2) + 4 * half + (r & 3); }
 
 __device__ __forceinline__ float exp2_(float v) { return __builtin_amdgcn_exp2f(v); }
 

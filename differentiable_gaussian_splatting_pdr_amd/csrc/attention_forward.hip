@@ -3,6 +3,8 @@
 // A lane (with its other half) owns one query: scores come out of the matrix
 // cores with keys in registers, so a running maximum and sum need one exchange
 // between halves a tile, and the weights go back in as they are.
+#include <type_traits>
+
 #include "attention.hpp"
 
 namespace pdr {
@@ -53,6 +55,13 @@ struct Query {
         s[u][r] = exp2_(fmaf(s[u][r], scale2, -from));
         sum += s[u][r];
       }
+  }
+  // The same where masks may hide what is not finite; `seen` as of mask().
+  template <int N>
+  __device__ __forceinline__ void take_carefully(const lds_char *values, const f32x16 (&s)[N],
+                                                 const typename C::Lane &at, int half, int seen) {
+#pragma unroll
+    for (int u = 0; u < N; ++u) C::across_careful(out, values, u, s[u], at, half, 0, seen - 32 * u);
   }
   // 32 N keys' values under these weights.
   template <int N>
@@ -128,8 +137,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_forward(Args a) {
   const int row0 = at.tile << kLogWide, mine = row0 + wave * 32;
   if (at.tile < 0 || row0 >= rows) return;
   const Row row(a, at, mine + (lane & 31), rows);
-  const int keys = keys_of(a, at, row0 + 127, rows);
-  const int plain = keys_of(a, at, mine, rows);  // below this key no row of the wave needs a mask
+  const int keys = keys_of(a, at, row0 + 127, rows), plain = keys_of(a, at, row0, rows);
 
   i32x4 q[C::kSteps];
   C::fetch_row(q, row_at(a.q, at, row, head, group, C::kSize), a.dim, half, row.there);
@@ -144,7 +152,8 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_forward(Args a) {
   if (tiles > 0) {
     load.tokens(k, v, 0, at.nk, smem);
   }
-  for (int t = 0; t < tiles; ++t) {
+  // Tile t: scores, weights, sums of values.
+  auto turn = [&](int t, auto masked) {
     const lds_char *const sk = smem + (t & 1) * (2 * L::kBytes), *const sv = sk + L::kBytes;
     all_landed<0>();
     if (t + 1 < tiles) {
@@ -158,15 +167,26 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_forward(Args a) {
       C::along(s[u], sk, u, q, lanes);
     }
     if constexpr (FMT != kF32) interleave<6, 2 * C::kSteps, 1, 2 * C::kSteps>();
-    if ((t + 1) * kKeys > plain) {
-      const int seen = here(row.seen - t * kKeys - 4 * half);
+    if constexpr (decltype(masked)::value) {
+      const int seen = row.seen - t * kKeys;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) mask(s[u], u * 32, seen);
+      for (int u = 0; u < 2; ++u) mask(s[u], u * 32, seen - 4 * half);
+      query.template weigh<2>(s, a.scale2);
+      if (C::any_not_finite(sv, 0, lane) || C::any_not_finite(sv, 1, lane))
+        query.template take_carefully<2>(sv, s, lanes, half, seen);
+      else
+        query.template take<2>(sv, s, lanes);
+    } else {
+      query.template weigh<2>(s, a.scale2);
+      query.template take<2>(sv, s, lanes);
+      if constexpr (FMT != kF32) interleave<8, 8 * C::kBlocks, 2, 4 * C::kBlocks>();
     }
-    query.template weigh<2>(s, a.scale2);
-    query.template take<2>(sv, s, lanes);
-    if constexpr (FMT != kF32) interleave<8, 8 * C::kBlocks, 2, 4 * C::kBlocks>();
-  }
+  };
+  // tiles that all rows of the workgroup see, and the others
+  const int whole = plain / kKeys < tiles ? plain / kKeys : tiles;
+  int t = 0;
+  for (; t < whole; ++t) turn(t, std::false_type());
+  for (; t < tiles; ++t) turn(t, std::true_type());
   const float sum = query.sum + other_half(query.sum);
   if (!row.there) return;
   if (a.lse && half == 0)
@@ -235,9 +255,16 @@ __global__ __launch_bounds__(64 * NW, FMT == kF32 ? 1 : 2) void k_forward_few(Ar
     clear(s[0]);
 #pragma unroll
     for (int i = 0; i < C::kSteps; ++i) s[0] = C::go(keys_now[i], q[i], s[0]);
-    if ((t + 1) * kKeys > plain) mask(s[0], 0, here(row.seen - t * kKeys - 4 * half));
+    bool careful = false;
+    if ((t + 1) * kKeys > plain) {
+      mask(s[0], 0, here(row.seen - t * kKeys - 4 * half));
+      careful = C::any_not_finite(sv, 0, lane);
+    }
     query.template weigh<1>(s, a.scale2);
-    query.template take<1>(sv, s, lanes);
+    if (careful)
+      query.template take_carefully<1>(sv, s, lanes, half, row.seen - t * kKeys);
+    else
+      query.template take<1>(sv, s, lanes);
 #pragma unroll
     for (int i = 0; i < C::kSteps; ++i) keys_now[i] = keys_next[i];
   }

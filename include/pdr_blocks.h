@@ -32,7 +32,9 @@ extern "C" {
  * not 0 those with j <= i + (keys - queries), so that the last query sees every
  * key.  A query that sees no key (or only keys whose score is -infinity) gets
  * zeros and has no gradient.  What a query does not see does not reach its
- * result, whatever it holds.
+ * result, whatever it holds.  Nor does it reach gradients across sequences, or
+ * from behind a length; but within a causal sequence an infinity or NaN may make
+ * gradients not finite that it is masked from, of up to 127 tokens beside it.
  *
  * Sequences.  Without offsets there are `batch` of them, each of q_rows
  * queries and k_rows keys, *_batch elements apart; key_lengths, if not NULL,

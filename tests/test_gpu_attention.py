@@ -182,6 +182,49 @@ def test_cache(nq, causal, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("nq,nk,h", [(150, 150, 2), (3, 200, 2), (1, 90, 4), (40, 300, 1)])
+def test_not_finite_behind_the_mask(nq, nk, h, dtype):
+    """Results of queries that do not see an infinity or NaN are those without it; the others' are not finite."""
+    b, d = blocks(), 64
+    q, k, v = normal(1, 1, nq, h, d, dtype=dtype), normal(2, 1, nk, 1, d, dtype=dtype), normal(3, 1, nk, 1, d, dtype=dtype)
+    clean = b.attention(q.cuda(), k.cuda(), v.cuda(), causal=True).cpu()
+    for at in (nk - 1, nk - nq // 2 - 1, nk - nq):
+        for bad in (float("nan"), float("inf"), -float("inf")):
+            first = max(0, at - (nk - nq))   # the first query that sees it
+            w = v.clone()
+            w[0, at, 0, 5] = bad
+            y = b.attention(q.cuda(), k.cuda(), w.cuda(), causal=True).cpu()
+            assert torch.equal(y[:, :first], clean[:, :first]), (at, bad)
+            keep = [i for i in range(d) if i != 5]
+            assert torch.allclose(y[..., keep].float(), clean[..., keep].float(), rtol=2 ** -7, atol=2 ** -9)
+            got = y[0, first:, :, 5]
+            # a weight that is 0 in fp32 makes NaN of an infinity; none is here
+            assert torch.isnan(got).all() if bad != bad else (got == bad).all(), (at, bad)
+            x = k.clone()
+            x[0, at, 0, 5] = bad
+            y = b.attention(q.cuda(), x.cuda(), v.cuda(), causal=True).cpu()
+            assert torch.equal(y[:, :first], clean[:, :first]), (at, bad)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_not_finite_in_other_sequences(dtype):
+    """Neither results nor gradients of a sequence depend on what others hold."""
+    b, d, offs = blocks(), 40, torch.tensor([0, 30, 75, 140], dtype=torch.int32, device="cuda")
+    ts = [normal(i, 140, n, d, dtype=dtype) for i, n in ((1, 4), (2, 2), (3, 2), (4, 4))]
+
+    def run(ts):
+        q, k, v = (leaf(t) for t in ts[:3])
+        y = b.attention(q, k, v, causal=True, offsets=offs)
+        return [y.detach().cpu()] + [g.cpu() for g in torch.autograd.grad(y, (q, k, v), ts[3].cuda())]
+    clean = run(ts)
+    for i in range(4):
+        bad = [t.clone() for t in ts]
+        bad[i][30:75] = float("nan")
+        for got, want in zip(run(bad), clean):
+            assert torch.equal(got[:30], want[:30]) and torch.equal(got[75:], want[75:]), i
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_layouts(dtype):
     """Views: parts of one projection, heads before tokens, rows on odd places, expanded keys, packed the other way."""
     b, d = blocks(), 64
