@@ -571,6 +571,7 @@ hipError_t launch_forward(const Args &a, int fmt, hipStream_t st);
 hipError_t launch_forward_few(const Args &a, int fmt, hipStream_t st);
 hipError_t launch_starts(const Args &a, int fmt, long long tokens, int heads, hipStream_t st);
 hipError_t launch_backward_q(const Args &a, int fmt, hipStream_t st);
+hipError_t launch_backward_q_few(const Args &a, int fmt, hipStream_t st);
 hipError_t launch_backward_kv(const Args &a, int fmt, hipStream_t st);
 
 }  // namespace attend

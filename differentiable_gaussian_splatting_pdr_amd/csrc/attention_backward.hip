@@ -121,6 +121,28 @@ __device__ __forceinline__ void across32(f32x16 (&c)[C::kBlocks], const lds_char
   for (int x = 0; x < 2; ++x) C::across(c, tile, 2 * u + x, C::pack(w, 8 * x), at);
 }
 
+// A row's starts, from what its lanes hold of dy; `writes`: also for dk and dv.
+template <int FMT, int DP>
+__device__ __forceinline__ void starts_of_row(const Args &a, const Place &at, int head, int row, bool there, int token,
+                                              int in_group, int half, const i32x4 (&dy)[Core<FMT, DP>::kSteps],
+                                              bool writes, float *start_s, float *start_dp) {
+  using C = Core<FMT, DP>;
+  const int group = (int)a.group.d;
+  i32x4 o[C::kSteps];
+  C::fetch_row(o, a.o.p + (first_of(a.o, at, at.q0 + token, head * group) + in_group * a.o.head) * C::kSize, a.dim,
+               half, there);
+  float d = 0.f;
+#pragma unroll
+  for (int i = 0; i < C::kSteps; ++i) d = dot<FMT>(o[i], dy[i], d);
+  *start_dp = -(d + other_half(d));
+  *start_s = 0.f;
+  if (!there) return;
+  const long long tokens = a.q_offsets ? a.q_rows : (long long)a.batch * a.q_rows;
+  const long long i = (head * tokens + (a.q_offsets ? 0 : (long long)at.seq * a.q_rows) + at.q0) * group + row;
+  *start_s = start_of<FMT>(a.lse[i], a.scale2);
+  if (half == 0 && writes) *(float2 *)(a.starts + 2 * i) = make_float2(*start_s, *start_dp);
+}
+
 // dq: 128 rows to a workgroup, 32 to a wave, as in the forward; and the rows'
 // starts.
 template <int FMT, int DP>
@@ -143,7 +165,6 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
   const int token = (int)fdiv((uint32_t)(there ? row : rows - 1), a.group);
   const int in_group = there ? row - token * group : 0;
   const int ahead = at.nk - at.nq;
-  const int seen = !a.causal ? at.nk : token + ahead + 1 < at.nk ? token + ahead + 1 : at.nk;
   int keys = at.nk;
   if (a.causal) {
     const int last = row0 + 127 < rows ? row0 + 127 : rows - 1;
@@ -158,22 +179,8 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
                a.dim, half, there);
   C::fetch_row(dy, a.dy.p + (first_of(a.dy, at, at.q0 + token, head * group) + in_group * a.dy.head) * C::kSize,
                a.dim, half, there);
-  float start_s = 0.f, start_dp = 0.f;
-  {
-    i32x4 o[C::kSteps];
-    C::fetch_row(o, a.o.p + (first_of(a.o, at, at.q0 + token, head * group) + in_group * a.o.head) * C::kSize,
-                 a.dim, half, there);
-#pragma unroll
-    for (int i = 0; i < C::kSteps; ++i) start_dp = dot<FMT>(o[i], dy[i], start_dp);
-    start_dp = -(start_dp + other_half(start_dp));
-  }
-  if (there) {
-    const long long tokens = a.q_offsets ? a.q_rows : (long long)a.batch * a.q_rows;
-    const long long i =
-        (head * tokens + (a.q_offsets ? 0 : (long long)at.seq * a.q_rows) + at.q0) * group + row;
-    start_s = start_of<FMT>(a.lse[i], a.scale2);
-    if (half == 0) *(float2 *)(a.starts + 2 * i) = make_float2(start_s, start_dp);
-  }
+  float start_s, start_dp;
+  starts_of_row<FMT, DP>(a, at, head, row, there, token, in_group, half, dy, true, &start_s, &start_dp);
   f32x16 sums[C::kBlocks];
 #pragma unroll
   for (int b = 0; b < C::kBlocks; ++b) clear(sums[b]);
@@ -182,18 +189,22 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
   Scaled<C, FMT> scaled;
   scaled.init();
   const Source k(a.k, first_of(a.k, at, at.k0, head), C::kSize), v(a.v, first_of(a.v, at, at.k0, head), C::kSize);
-  L load;
-  load.init(a.dim, wave, lane);
+  // a lane's place in the loads is worked out each time, as in k_backward_kv
+  auto load = [&](int t, lds_char *to) {
+    L loader;
+    loader.init(a.dim, wave, lane_again());
+    loader.tokens(k, v, t * kKeys, at.nk, to);
+  };
   const int tiles = (keys + kKeys - 1) / kKeys;
   if (tiles > 0) {
-    load.tokens(k, v, 0, at.nk, smem);
+    load(0, smem);
   }
   for (int t = 0; t < tiles; ++t) {
     const lds_char *const sk = smem + (t & 1) * (2 * L::kBytes), *const sv = sk + L::kBytes;
     all_landed<0>();
     if (t + 1 < tiles) {
       lds_char *const next = smem + ((t + 1) & 1) * (2 * L::kBytes);
-      load.tokens(k, v, (t + 1) * kKeys, at.nk, next);
+      load(t + 1, next);
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -211,7 +222,10 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
         s[r] = ds;
       }
       if (key0 + 32 > plain) {
-        const int last = here(seen - key0 - 4 * half);
+        const int lane = lane_again(), r = row0 + wave * 32 + (lane & 31);
+        const int token = (int)fdiv((uint32_t)(r < rows ? r : rows - 1), a.group);
+        const int seen = !a.causal ? at.nk : token + ahead + 1 < at.nk ? token + ahead + 1 : at.nk;
+        const int last = here(seen - key0 - 4 * (lane >> 5));
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           if (row_in(r, 0) >= last) s[r] = 0.f;
@@ -221,10 +235,11 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
       if constexpr (FMT != kF32) interleave<8, 4 * C::kBlocks, 2, 2 * C::kBlocks>();
     }
   }
-  if (!there) return;
-  store_columns<C, FMT>(sums,
-                        a.dq.p + (first_of(a.dq, at, at.q0 + token, head * group) + in_group * a.dq.head) * C::kSize,
-                        a.dim, half, a.scale * scaled.out());
+  const int lane_now = lane_again(), row_now = row0 + wave * 32 + (lane_now & 31);
+  if (row_now >= rows) return;
+  const int n = (int)fdiv((uint32_t)row_now, a.group), g = row_now - n * group;
+  store_columns<C, FMT>(sums, a.dq.p + (first_of(a.dq, at, at.q0 + n, head * group) + g * a.dq.head) * C::kSize, a.dim,
+                        lane_now >> 5, a.scale * scaled.out());
 #endif
 }
 
@@ -244,6 +259,112 @@ __device__ __forceinline__ void store_keys(const Args &a, const Place &at, const
     return;
   }
   store_columns<C, FMT>(c, to.p + (at.seq * to.batch + where * to.row + head * to.head) * C::kSize, a.dim, half, by);
+}
+
+// dq where 128 rows to a workgroup would leave compute units without one: 32 rows,
+// whose waves take parts of the keys each, in LDS of their own.
+template <int FMT, int DP, int NW>
+__global__ __launch_bounds__(64 * NW) void k_backward_q_few(Args a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  using C = Core<FMT, DP>;
+  constexpr int kKeys = 32;
+  using L = Loader<C, kKeys, 1>;
+  constexpr int kRing = 4 * L::kBytes;  // two tiles of keys and values
+  __shared__ __align__(1024) char shared[NW * kRing];
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int unit = (int)fdiv(blockIdx.x, a.heads), head = blockIdx.x - unit * a.kv_heads;
+  const Place at = place<kLogFew, false>(a, a.causal ? a.q_tiles - 1 - unit : unit);
+  const int group = (int)a.group.d, rows = at.nq * group;
+  const int row0 = at.tile << kLogFew;
+  if (at.tile < 0 || row0 >= rows) return;
+  const int row = row0 + (lane & 31);
+  const bool there = row < rows;
+  const int token = (int)fdiv((uint32_t)(there ? row : rows - 1), a.group);
+  const int in_group = there ? row - token * group : 0;
+  const int ahead = at.nk - at.nq;
+  const int seen = !a.causal ? at.nk : token + ahead + 1 < at.nk ? token + ahead + 1 : at.nk;
+  int keys = at.nk, plain = at.nk;
+  if (a.causal) {
+    const int last = row0 + 31 < rows ? row0 + 31 : rows - 1;
+    keys = (int)fdiv((uint32_t)last, a.group) + ahead + 1;
+    plain = (int)fdiv((uint32_t)row0, a.group) + ahead + 1;
+    if (keys < 0) keys = 0;
+  }
+
+  i32x4 q[C::kSteps], dy[C::kSteps];
+  C::fetch_row(q, a.q.p + (first_of(a.q, at, at.q0 + token, head * group) + in_group * a.q.head) * C::kSize,
+               a.dim, half, there);
+  C::fetch_row(dy, a.dy.p + (first_of(a.dy, at, at.q0 + token, head * group) + in_group * a.dy.head) * C::kSize,
+               a.dim, half, there);
+  float start_s, start_dp;
+  starts_of_row<FMT, DP>(a, at, head, row, there, token, in_group, half, dy, wave == 0, &start_s, &start_dp);
+  f32x16 sums[C::kBlocks];
+#pragma unroll
+  for (int b = 0; b < C::kBlocks; ++b) clear(sums[b]);
+  typename C::Lane lanes;
+  lanes.init(lane);
+  Scaled<C, FMT> scaled;
+  scaled.init();
+  const Source k(a.k, first_of(a.k, at, at.k0, head), C::kSize), v(a.v, first_of(a.v, at, at.k0, head), C::kSize);
+  L load;
+  load.init(a.dim, 0, lane);
+  lds_char *const ring = (lds_char *)shared + wave * kRing;
+  const int all = (keys + kKeys - 1) / kKeys, each = (all + NW - 1) / NW;
+  const int begin = wave * each < all ? wave * each : all;
+  const int end = begin + each < all ? begin + each : all;
+  if (begin < end) load.tokens(k, v, begin * kKeys, at.nk, ring);
+  for (int t = begin; t < end; ++t) {
+    const lds_char *const sk = ring + ((t - begin) & 1) * (2 * L::kBytes), *const sv = sk + L::kBytes;
+    landed<0>();  // this tile; and the last one's reads are done
+    if (t + 1 < end) load.tokens(k, v, (t + 1) * kKeys, at.nk, ring + ((t + 1 - begin) & 1) * (2 * L::kBytes));
+    f32x16 s, dp;
+    fill(s, FMT == kF32 ? 0.f : start_s);
+    fill(dp, start_dp);
+    C::along(s, sk, 0, q, lanes);
+    C::along(dp, sv, 0, dy, lanes);
+    if constexpr (FMT != kF32) interleave<6, 2 * C::kSteps, 1, 2 * C::kSteps>();
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      float p = s[r], ds = dp[r];
+      weigh<FMT>(p, ds, start_s, a.scale2);
+      s[r] = ds;
+    }
+    if ((t + 1) * kKeys > plain) {
+      const int last = here(seen - t * kKeys - 4 * half);
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (row_in(r, 0) >= last) s[r] = 0.f;
+    }
+    scaled.hold(s, sums);
+    across32<C>(sums, sk, 0, s, lanes);
+  }
+  // the waves' sums, where their keys were
+  __syncthreads();
+  const float by = a.scale * scaled.out();
+#pragma unroll
+  for (int b = 0; b < C::kBlocks; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4)
+      *(float4 *)(shared + wave * kRing + (lane & 31) * (DP * 4) + (((b * 32 + row_in(r, half)) / 4 ^ (lane & 7)) * 16)) =
+          make_float4(sums[b][r] * by, sums[b][r + 1] * by, sums[b][r + 2] * by, sums[b][r + 3] * by);
+  __syncthreads();
+  for (int x = threadIdx.x; x < 32 * (DP / 4); x += 64 * NW) {
+    const int i = x / (DP / 4), d = x % (DP / 4) * 4;
+    if (row0 + i >= rows || d >= a.dim) continue;
+    float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float4 o = *(const float4 *)(shared + w * kRing + i * (DP * 4) + ((d / 4 ^ (i & 7)) * 16));
+      c[0] += o.x;
+      c[1] += o.y;
+      c[2] += o.z;
+      c[3] += o.w;
+    }
+    const int n = (int)fdiv((uint32_t)(row0 + i), a.group), g = row0 + i - n * group;
+    store4<FMT>(a.dq.p + (first_of(a.dq, at, at.q0 + n, head * group) + g * a.dq.head + d) * C::kSize, c);
+  }
+#endif
 }
 
 // dk and dv: 128 keys to a workgroup, 32 to a wave; the waves share tiles of
@@ -397,6 +518,15 @@ void go_q(const Args &a, hipStream_t st) {
     hipLaunchKernelGGL((k_backward_q<FMT, 128>), grid, dim3(256), 0, st, a);
 }
 template <int FMT>
+void go_q_few(const Args &a, hipStream_t st) {
+  const dim3 grid((unsigned)a.q_tiles * a.kv_heads);
+  constexpr int kWaves = FMT == kF32 ? 2 : 4;  // what leaves LDS for two workgroups, or one at 128
+  if (a.dim <= 64)
+    hipLaunchKernelGGL((k_backward_q_few<FMT, 64, kWaves>), grid, dim3(64 * kWaves), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_backward_q_few<FMT, 128, kWaves>), grid, dim3(64 * kWaves), 0, st, a);
+}
+template <int FMT>
 void go_kv(const Args &a, hipStream_t st) {
   const dim3 grid((unsigned)a.k_tiles * a.kv_heads, (unsigned)a.splits);
   if (a.dim <= 64)
@@ -434,6 +564,17 @@ hipError_t launch_backward_q(const Args &a, int fmt, hipStream_t st) {
     go_q<kF16>(a, st);
   else
     go_q<kF32>(a, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_backward_q_few(const Args &a, int fmt, hipStream_t st) {
+  if (!a.q_tiles || !a.kv_heads) return hipSuccess;
+  if (fmt == kBf16)
+    go_q_few<kBf16>(a, st);
+  else if (fmt == kF16)
+    go_q_few<kF16>(a, st);
+  else
+    go_q_few<kF32>(a, st);
   return hipGetLastError();
 }
 

@@ -202,7 +202,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_forward(Args a) {
 // so that only values take up LDS and two workgroups' loads are in flight on a
 // compute unit.
 template <int FMT, int DP, int NW>
-__global__ __launch_bounds__(64 * NW, FMT == kF32 ? 1 : 2) void k_forward_few(Args a) {
+__global__ __launch_bounds__(64 * NW, FMT == kF32 && DP > 64 ? 1 : 2) void k_forward_few(Args a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using C = Core<FMT, DP>;
   constexpr int kKeys = 32;

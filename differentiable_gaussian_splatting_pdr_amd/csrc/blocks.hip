@@ -112,10 +112,43 @@ int tiles_of(const pdr_attention &p, long long tokens, long long each, int log) 
   return (int)(((tokens * each + (1 << log) - 1) >> log) * p.batch);
 }
 
-constexpr long long kFewBelow = 256;   // workgroups of 128 rows
-constexpr long long kFewUnits = 2048;  // workgroups of 32 rows to aim for
-constexpr long long kFewKeys = 256;    // keys of a workgroup, at least
-constexpr long long kAlone = 1024;     // keys that one workgroup takes without a join
+constexpr long long kFewUnits = 512;       // workgroups of 32 rows to aim for: two to a compute unit,
+constexpr long long kUnequalUnits = 2048;  // and of sequences of different lengths (a cache of 16 sequences up
+                                           // to 32768 keys: 4 parts 298 us, 16 parts 272)
+constexpr long long kFewKeys = 256;        // keys of a workgroup, at least
+constexpr long long kAlone = 1024;         // keys that one workgroup takes without a join
+
+// Sizes of the average sequence.
+struct Sizes {
+  long long seqs, rows, keys;  // rows: queries and heads of a key head
+  long long wide;              // workgroups of 128 rows
+  explicit Sizes(const pdr_attention &p) {
+    seqs = p.batch > 0 ? p.batch : 1;
+    rows = (p.q_offsets ? (p.q_rows + seqs - 1) / seqs : p.q_rows) * (p.heads / p.kv_heads);
+    keys = p.q_offsets ? (p.k_rows + seqs - 1) / seqs : p.k_rows;
+    wide = (rows + 127) / 128 * seqs * p.kv_heads;
+  }
+};
+
+// Whether 32 rows go to a workgroup whose waves share the keys, instead of 128 whose
+// waves share tiles of keys: where a sequence has no more, and where the larger
+// workgroups are fewer than the compute units.  The gradient's smaller ones pay for
+// a start of their own only along many keys; where fp32 workgroups of 64 values a
+// head see different numbers of keys, one to a compute unit waits for the longest.
+// Larger against smaller, forward / forward's and all gradients' time, us:
+//   bf16 2 x 512, 8 heads of 128      (64 workgroups)   19 /  52     15 /  76
+//   bf16 8192, 2 heads of 128        (128)             154 / 340    116 / 256
+//   fp32 4 x 1024, 8 heads of 64     (256, causal)      88 / 244     67 / 211
+//   the same, not causal             (256)              87 / 304     98 / 323
+//   fp32 4 x 1024, 8 heads of 128    (256, causal)     146 / 414    135 / 477
+bool takes_few(const pdr_attention &p, bool gradient) {
+  const Sizes n(p);
+  const bool uneven = p.fmt == kF32 && p.causal && p.dim <= 64 && n.wide < 512;
+  if (n.rows > 32 && !uneven && (n.wide >= 256 || (gradient && p.fmt != kF32 && n.keys < 2048))) return false;
+  // a launch has fewer than 2^32 threads
+  const long long each = p.heads / p.kv_heads;
+  return (p.q_offsets ? (p.q_rows * each >> 5) + n.seqs + 2 : (n.rows + 31) / 32 * n.seqs) * p.kv_heads < 1 << 22;
+}
 
 struct Plan {
   bool few;
@@ -123,25 +156,20 @@ struct Plan {
   size_t part_o, part_ml;  // bytes
 };
 
-// Few queries, or too few workgroups of many: 32 rows to a workgroup whose waves
-// take different keys, and several workgroups over the keys until the card has
-// work.
+// Few queries: several workgroups over the keys until the card has work.
 Plan plan_of(const pdr_attention &p) {
-  const long long group = p.heads / p.kv_heads;
-  const long long seqs = p.batch > 0 ? p.batch : 1;
-  const long long rows = p.q_offsets ? (p.q_rows * group + seqs - 1) / seqs : p.q_rows * group;
-  const long long keys = p.q_offsets ? (p.k_rows + seqs - 1) / seqs : p.k_rows;
-  const long long units = (rows + 31) / 32 * seqs * p.kv_heads;
-  Plan plan = {rows <= 32 || (rows + 127) / 128 * seqs * p.kv_heads < kFewBelow, 4, 1, 0, 0};
-  // a launch has fewer than 2^32 threads
-  if ((p.q_offsets ? (p.q_rows * group >> 5) + seqs + 2 : units) * p.kv_heads >= 1 << 22) plan.few = false;
-  if (!plan.few || !rows) return plan;
-  if (keys <= kAlone) {
-    if (!(p.fmt == kF32 && p.dim > 64)) plan.waves = 8;
+  const Sizes n(p);
+  const long long units = (n.rows + 31) / 32 * n.seqs * p.kv_heads;
+  Plan plan = {takes_few(p, false), 4, 1, 0, 0};
+  if (!plan.few || !n.rows) return plan;
+  if (n.keys <= kAlone) {
+    // eight waves where that leaves one workgroup to a compute unit; their LDS holds no fp32 rows of 128
+    if (units < 512 && !(p.fmt == kF32 && p.dim > 64)) plan.waves = 8;
     return plan;
   }
-  long long splits = (kFewUnits + units - 1) / units;
-  const long long most = (keys + kFewKeys - 1) / kFewKeys;
+  const long long aim = p.q_offsets || p.key_lengths ? kUnequalUnits : kFewUnits;
+  long long splits = (aim + units - 1) / units;
+  const long long most = (n.keys + kFewKeys - 1) / kFewKeys;
   if (splits > most) splits = most;
   plan.splits = (int)(splits < 1 ? 1 : splits);
   if (plan.splits > 1) {
@@ -158,13 +186,11 @@ constexpr long long kKeyUnits = 512;  // workgroups of 128 keys to aim for
 constexpr long long kKeyRows = 256;   // rows of a part, at least
 int key_splits(const pdr_attention &p, size_t *bytes) {
   *bytes = 0;
-  const long long seqs = p.batch > 0 ? p.batch : 1;
-  const long long rows = (p.q_offsets ? (p.q_rows + seqs - 1) / seqs : p.q_rows) * (p.heads / p.kv_heads);
-  const long long keys = p.q_offsets ? (p.k_rows + seqs - 1) / seqs : p.k_rows;
-  const long long units = (keys + 127) / 128 * seqs * p.kv_heads;
+  const Sizes n(p);
+  const long long units = (n.keys + 127) / 128 * n.seqs * p.kv_heads;
   if (!p.dk || !units) return 1;
   long long splits = (kKeyUnits + units - 1) / units;
-  if (splits > rows / kKeyRows) splits = rows / kKeyRows;
+  if (splits > n.rows / kKeyRows) splits = n.rows / kKeyRows;
   if (splits <= 1) return 1;
   *bytes = round256((size_t)(p.q_offsets ? 1 : p.batch) * p.k_rows * p.kv_heads * p.dim * splits * 8);
   return (int)splits;
@@ -289,8 +315,9 @@ int pdr_attention_backward(const pdr_attention *p, void *workspace, size_t works
   if (!p->dq) {
     e = attend::launch_starts(a, p->fmt, tokens_of(*p), (int)p->heads, st);
   } else if (tokens_of(*p)) {
-    a.q_tiles = tiles_of(*p, p->q_rows, p->heads / p->kv_heads, attend::kLogWide);
-    e = attend::launch_backward_q(a, p->fmt, st);
+    const bool few = takes_few(*p, true);
+    a.q_tiles = tiles_of(*p, p->q_rows, p->heads / p->kv_heads, few ? attend::kLogFew : attend::kLogWide);
+    e = few ? attend::launch_backward_q_few(a, p->fmt, st) : attend::launch_backward_q(a, p->fmt, st);
   }
   if (e == hipSuccess && p->dk) {
     size_t parts;
