@@ -435,7 +435,15 @@ struct Source {
   const char *base;    // first token of the sequence, this head
   uint32_t row, head;  // bytes
   __device__ __forceinline__ Source(const Mat &m, long long first, int size)
-      : base(m.p + first * size), row((uint32_t)(m.row * size)), head((uint32_t)(m.head * size)) {}
+      : base(scalar(m.p + first * size)), row((uint32_t)(m.row * size)), head((uint32_t)(m.head * size)) {}
+  // All lanes have the same place, which the compiler does not see in every kernel:
+  // it then puts a loop over lanes around each load.
+  static __device__ __forceinline__ const char *scalar(const char *p) {
+    const uint64_t v = (uint64_t)(uintptr_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (const char *)(uintptr_t)((uint64_t)hi << 32 | lo);
+  }
 };
 template <class C, int ROWS, int NW>
 struct Loader {
@@ -569,7 +577,7 @@ constexpr int kLogWide = 7;  // 128 rows, or keys, to a workgroup
 constexpr int kLogFew = 5;   // 32
 hipError_t launch_forward(const Args &a, int fmt, hipStream_t st);
 hipError_t launch_forward_few(const Args &a, int fmt, hipStream_t st);
-hipError_t launch_starts(const Args &a, int fmt, long long tokens, int heads, hipStream_t st);
+// Without dq they make the rows' starts alone.
 hipError_t launch_backward_q(const Args &a, int fmt, hipStream_t st);
 hipError_t launch_backward_q_few(const Args &a, int fmt, hipStream_t st);
 hipError_t launch_backward_kv(const Args &a, int fmt, hipStream_t st);

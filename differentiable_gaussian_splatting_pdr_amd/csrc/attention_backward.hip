@@ -42,35 +42,6 @@ __device__ __forceinline__ float dot(i32x4 x, i32x4 y, float s) {
   return s;
 }
 
-// The starts of each row, where no dq is wanted (its kernel makes them on the
-// way): 16 lanes to a row, 16 bytes each at a time.
-template <int FMT>
-__global__ __launch_bounds__(256) void k_starts(Args a, FastDiv heads, long long total) {
-  constexpr int kSize = FMT == kF32 ? 4 : 2, kPer = 16 / kSize;
-  const long long at = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const int lane = threadIdx.x & 15;
-  if (at >= total) return;
-  const uint32_t token = fdiv((uint32_t)at, heads), head = (uint32_t)at - token * heads.d;
-  long long seq = 0, i = token;
-  if (!a.q_offsets) {
-    seq = token / (uint32_t)a.q_rows;
-    i = token - seq * a.q_rows;
-  }
-  const char *o = a.o.p + (seq * a.o.batch + i * a.o.row + head * a.o.head) * kSize;
-  const char *dy = a.dy.p + (seq * a.dy.batch + i * a.dy.row + head * a.dy.head) * kSize;
-  float s = 0.f;
-  for (int d = lane * kPer; d < a.dim; d += 16 * kPer)
-    s = dot<FMT>(*(const i32x4 *)(o + d * kSize), *(const i32x4 *)(dy + d * kSize), s);
-#pragma unroll
-  for (int w = 8; w > 0; w >>= 1) s += __shfl_xor(s, w);
-  const uint32_t kv = fdiv(head, a.group), g = head - kv * a.group.d;
-  const long long tokens = total / heads.d;
-  if (lane == 0) {
-    const long long to = (kv * tokens + token) * a.group.d + g;
-    *(float2 *)(a.starts + 2 * to) = make_float2(start_of<FMT>(a.lse[to], a.scale2), -s);
-  }
-}
-
 // A tile's weights from its scores, and their gradients, in place.  `start`: of the
 // scores in fp32.
 template <int FMT>
@@ -98,14 +69,14 @@ struct Scaled {
         // leave room for four times as much
         int to = most - 2 < -120 ? -120 : most - 2;
         if (most >= e) to = e;
-        const float by = ldexpf(1.f, to - e < -250 ? -250 : to - e);
+        const float by = __builtin_amdgcn_ldexpf(1.f, to - e);
 #pragma unroll
         for (int b = 0; b < C::kBlocks; ++b)
 #pragma unroll
           for (int r = 0; r < 16; ++r) sums[b][r] *= by;
         e = to;
       }
-      const float by = ldexpf(1.f, e);
+      const float by = __builtin_amdgcn_ldexpf(1.f, e);
 #pragma unroll
       for (int r = 0; r < 16; ++r) ds[r] *= by;
     }
@@ -143,8 +114,28 @@ __device__ __forceinline__ void starts_of_row(const Args &a, const Place &at, in
   if (half == 0 && writes) *(float2 *)(a.starts + 2 * i) = make_float2(*start_s, *start_dp);
 }
 
+// delta = dy . o takes over the rounding of o and, in it, of the forward's weights.
+// Since p sums to 1, what ds adds up to with such a delta is by how much it is off:
+//   sum p (dp - delta') = delta - delta'.
+// A row of n keys loses to that about 1 / n of what rounding its ds costs, so that it
+// shows where n is small: queries that see up to kExact keys find the sum in a pass over them
+// first.  16 bits, causal, 777 queries: errors of dq 1.60 times those of rounding
+// the result, and 1.45 with this; 1.41 is the rounding of ds.
+constexpr int kExact = 256;
+
+// The row's start with the sum of ds added, there and for dk and dv.
+template <int FMT>
+__device__ __forceinline__ void mend_start(const Args &a, const Place &at, int head, int row, int rows, float off,
+                                           bool writes, float *start_dp) {
+  *start_dp -= FMT == kF16 ? ldexpf(off, -kShift) : off;
+  if (!writes || row >= rows) return;
+  const long long tokens = a.q_offsets ? a.q_rows : (long long)a.batch * a.q_rows;
+  const long long first = (head * tokens + (a.q_offsets ? 0 : (long long)at.seq * a.q_rows) + at.q0) * a.group.d;
+  a.starts[2 * (first + row) + 1] = *start_dp;
+}
+
 // dq: 128 rows to a workgroup, 32 to a wave, as in the forward; and the rows'
-// starts.
+// starts, which is all there is to do where dq is not wanted.
 template <int FMT, int DP>
 __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -175,12 +166,12 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
   const int plain = !a.causal ? at.nk : (int)fdiv((uint32_t)first_row, a.group) + ahead + 1;
 
   i32x4 q[C::kSteps], dy[C::kSteps];
-  C::fetch_row(q, a.q.p + (first_of(a.q, at, at.q0 + token, head * group) + in_group * a.q.head) * C::kSize,
-               a.dim, half, there);
   C::fetch_row(dy, a.dy.p + (first_of(a.dy, at, at.q0 + token, head * group) + in_group * a.dy.head) * C::kSize,
                a.dim, half, there);
   float start_s, start_dp;
   starts_of_row<FMT, DP>(a, at, head, row, there, token, in_group, half, dy, true, &start_s, &start_dp);
+  C::fetch_row(q, a.q.p + (first_of(a.q, at, at.q0 + token, head * group) + in_group * a.q.head) * C::kSize,
+               a.dim, half, there);
   f32x16 sums[C::kBlocks];
 #pragma unroll
   for (int b = 0; b < C::kBlocks; ++b) clear(sums[b]);
@@ -195,41 +186,65 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
     loader.init(a.dim, wave, lane_again());
     loader.tokens(k, v, t * kKeys, at.nk, to);
   };
+  // ds of 32 keys, in s
+  auto gradients = [&](f32x16 &s, const lds_char *sk, const lds_char *sv, int t, int u) {
+    f32x16 dp;
+    fill(s, FMT == kF32 ? 0.f : start_s);
+    fill(dp, start_dp);
+    C::along(s, sk, u, q, lanes);
+    C::along(dp, sv, u, dy, lanes);
+    if constexpr (FMT != kF32) interleave<6, 2 * C::kSteps, 1, 2 * C::kSteps>();
+    const int key0 = t * kKeys + u * 32;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      float p = s[r], ds = dp[r];
+      weigh<FMT>(p, ds, start_s, a.scale2);
+      s[r] = ds;
+    }
+    if (key0 + 32 > plain) {
+      const int lane = lane_again(), r = row0 + wave * 32 + (lane & 31);
+      const int token = (int)fdiv((uint32_t)(r < rows ? r : rows - 1), a.group);
+      const int seen = !a.causal ? at.nk : token + ahead + 1 < at.nk ? token + ahead + 1 : at.nk;
+      const int last = here(seen - key0 - 4 * (lane >> 5));
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (row_in(r, 0) >= last) s[r] = 0.f;
+    }
+  };
   const int tiles = (keys + kKeys - 1) / kKeys;
-  if (tiles > 0) {
+  // Tile t has come, and the next is on its way.
+  auto turn = [&](int t) {
+    all_landed<0>();
+    if (t + 1 < tiles) load(t + 1, smem + ((t + 1) & 1) * (2 * L::kBytes));
+    return smem + (t & 1) * (2 * L::kBytes);
+  };
+  const bool exact = FMT != kF32 && tiles > 0 && keys <= kExact;
+  if (!exact && !a.dq.p) return;
+  if (tiles > 0) load(0, smem);
+  if (exact) {
+    float off = 0.f;
+    for (int t = 0; t < tiles; ++t) {
+      const lds_char *const sk = turn(t), *const sv = sk + L::kBytes;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        f32x16 s;
+        gradients(s, sk, sv, t, u);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) off += s[r];
+      }
+    }
+    const int lane = lane_again();
+    mend_start<FMT>(a, at, head, row0 + wave * 32 + (lane & 31), rows, off + other_half(off), lane < 32, &start_dp);
+    if (!a.dq.p) return;
+    __syncthreads();
     load(0, smem);
   }
   for (int t = 0; t < tiles; ++t) {
-    const lds_char *const sk = smem + (t & 1) * (2 * L::kBytes), *const sv = sk + L::kBytes;
-    all_landed<0>();
-    if (t + 1 < tiles) {
-      lds_char *const next = smem + ((t + 1) & 1) * (2 * L::kBytes);
-      load(t + 1, next);
-    }
+    const lds_char *const sk = turn(t), *const sv = sk + L::kBytes;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      f32x16 s, dp;
-      fill(s, FMT == kF32 ? 0.f : start_s);
-      fill(dp, start_dp);
-      C::along(s, sk, u, q, lanes);
-      C::along(dp, sv, u, dy, lanes);
-      if constexpr (FMT != kF32) interleave<6, 2 * C::kSteps, 1, 2 * C::kSteps>();
-      const int key0 = t * kKeys + u * 32;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        float p = s[r], ds = dp[r];
-        weigh<FMT>(p, ds, start_s, a.scale2);
-        s[r] = ds;
-      }
-      if (key0 + 32 > plain) {
-        const int lane = lane_again(), r = row0 + wave * 32 + (lane & 31);
-        const int token = (int)fdiv((uint32_t)(r < rows ? r : rows - 1), a.group);
-        const int seen = !a.causal ? at.nk : token + ahead + 1 < at.nk ? token + ahead + 1 : at.nk;
-        const int last = here(seen - key0 - 4 * (lane >> 5));
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (row_in(r, 0) >= last) s[r] = 0.f;
-      }
+      f32x16 s;
+      gradients(s, sk, sv, t, u);
       scaled.hold(s, sums);
       across32<C>(sums, sk, u, s, lanes);
       if constexpr (FMT != kF32) interleave<8, 4 * C::kBlocks, 2, 2 * C::kBlocks>();
@@ -293,12 +308,12 @@ __global__ __launch_bounds__(64 * NW) void k_backward_q_few(Args a) {
   }
 
   i32x4 q[C::kSteps], dy[C::kSteps];
-  C::fetch_row(q, a.q.p + (first_of(a.q, at, at.q0 + token, head * group) + in_group * a.q.head) * C::kSize,
-               a.dim, half, there);
   C::fetch_row(dy, a.dy.p + (first_of(a.dy, at, at.q0 + token, head * group) + in_group * a.dy.head) * C::kSize,
                a.dim, half, there);
   float start_s, start_dp;
   starts_of_row<FMT, DP>(a, at, head, row, there, token, in_group, half, dy, wave == 0, &start_s, &start_dp);
+  C::fetch_row(q, a.q.p + (first_of(a.q, at, at.q0 + token, head * group) + in_group * a.q.head) * C::kSize,
+               a.dim, half, there);
   f32x16 sums[C::kBlocks];
 #pragma unroll
   for (int b = 0; b < C::kBlocks; ++b) clear(sums[b]);
@@ -313,16 +328,13 @@ __global__ __launch_bounds__(64 * NW) void k_backward_q_few(Args a) {
   const int all = (keys + kKeys - 1) / kKeys, each = (all + NW - 1) / NW;
   const int begin = wave * each < all ? wave * each : all;
   const int end = begin + each < all ? begin + each : all;
-  if (begin < end) load.tokens(k, v, begin * kKeys, at.nk, ring);
-  for (int t = begin; t < end; ++t) {
-    const lds_char *const sk = ring + ((t - begin) & 1) * (2 * L::kBytes), *const sv = sk + L::kBytes;
-    landed<0>();  // this tile; and the last one's reads are done
-    if (t + 1 < end) load.tokens(k, v, (t + 1) * kKeys, at.nk, ring + ((t + 1 - begin) & 1) * (2 * L::kBytes));
-    f32x16 s, dp;
+  // ds of tile t, in s
+  auto gradients = [&](f32x16 &s, const lds_char *sk, int t) {
+    f32x16 dp;
     fill(s, FMT == kF32 ? 0.f : start_s);
     fill(dp, start_dp);
     C::along(s, sk, 0, q, lanes);
-    C::along(dp, sv, 0, dy, lanes);
+    C::along(dp, sk + L::kBytes, 0, dy, lanes);
     if constexpr (FMT != kF32) interleave<6, 2 * C::kSteps, 1, 2 * C::kSteps>();
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
@@ -336,6 +348,41 @@ __global__ __launch_bounds__(64 * NW) void k_backward_q_few(Args a) {
       for (int r = 0; r < 16; ++r)
         if (row_in(r, 0) >= last) s[r] = 0.f;
     }
+  };
+  // Tile t has come, the last one's reads are done, and the next is on its way.
+  auto turn = [&](int t) {
+    landed<0>();
+    if (t + 1 < end) load.tokens(k, v, (t + 1) * kKeys, at.nk, ring + ((t + 1 - begin) & 1) * (2 * L::kBytes));
+    return ring + ((t - begin) & 1) * (2 * L::kBytes);
+  };
+  const bool exact = FMT != kF32 && keys <= kExact;
+  if (!exact && !a.dq.p) return;
+  if (begin < end) load.tokens(k, v, begin * kKeys, at.nk, ring);
+  if (exact) {
+    float off = 0.f;
+    for (int t = begin; t < end; ++t) {
+      f32x16 s;
+      gradients(s, turn(t), t);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) off += s[r];
+    }
+    off += other_half(off);
+    float *const offs = (float *)shared;
+    __syncthreads();
+    if (half == 0) offs[wave * 32 + lane] = off;
+    __syncthreads();
+    off = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) off += offs[w * 32 + (lane & 31)];
+    mend_start<FMT>(a, at, head, row, rows, off, wave == 0 && half == 0, &start_dp);
+    if (!a.dq.p) return;
+    __syncthreads();
+    if (begin < end) load.tokens(k, v, begin * kKeys, at.nk, ring);
+  }
+  for (int t = begin; t < end; ++t) {
+    const lds_char *const sk = turn(t);
+    f32x16 s;
+    gradients(s, sk, t);
     scaled.hold(s, sums);
     across32<C>(sums, sk, 0, s, lanes);
   }
@@ -541,20 +588,6 @@ void go_kv(const Args &a, hipStream_t st) {
 }
 
 }  // namespace
-
-hipError_t launch_starts(const Args &a, int fmt, long long tokens, int heads, hipStream_t st) {
-  const long long total = tokens * heads;
-  if (!total) return hipSuccess;
-  const dim3 grid((unsigned)((total + 15) / 16));
-  const FastDiv div = make_fastdiv((uint32_t)heads);
-  if (fmt == kBf16)
-    hipLaunchKernelGGL(k_starts<kBf16>, grid, dim3(256), 0, st, a, div, total);
-  else if (fmt == kF16)
-    hipLaunchKernelGGL(k_starts<kF16>, grid, dim3(256), 0, st, a, div, total);
-  else
-    hipLaunchKernelGGL(k_starts<kF32>, grid, dim3(256), 0, st, a, div, total);
-  return hipGetLastError();
-}
 
 hipError_t launch_backward_q(const Args &a, int fmt, hipStream_t st) {
   if (!a.q_tiles || !a.kv_heads) return hipSuccess;

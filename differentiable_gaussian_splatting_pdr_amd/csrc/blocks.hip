@@ -312,9 +312,7 @@ int pdr_attention_backward(const pdr_attention *p, void *workspace, size_t works
   a.starts = (float *)workspace;
   a.part_k = (float *)((char *)workspace + 2 * row_values(*p));
   hipError_t e = hipSuccess;
-  if (!p->dq) {
-    e = attend::launch_starts(a, p->fmt, tokens_of(*p), (int)p->heads, st);
-  } else if (tokens_of(*p)) {
+  if (tokens_of(*p)) {
     const bool few = takes_few(*p, true);
     a.q_tiles = tiles_of(*p, p->q_rows, p->heads / p->kv_heads, few ? attend::kLogFew : attend::kLogWide);
     e = few ? attend::launch_backward_q_few(a, p->fmt, st) : attend::launch_backward_q(a, p->fmt, st);
