@@ -373,3 +373,18 @@ def test_refusals():
     wide = torch.zeros(1, 2, 1, 136, device="cuda")
     with pytest.raises(ValueError):
         b.attention(wide, wide, wide)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("n,h,hk,d", [(130, 4, 4, 64), (700, 2, 2, 72), (1, 4, 1, 128), (520, 3, 1, 128)])
+def test_gradients_are_as_near_as_their_types(n, h, hk, d, dtype):
+    # dq and dk come from ds rounded to 16 bits, and are rounded: two independent errors of one size, sqrt(2) times
+    # what rounding the 64-bit result costs.  6 % more for all else, weights and delta among it.
+    q, k, v, dy = (normal(60 + i, 2, n, m, d, dtype=dtype) for i, m in enumerate((h, hk, hk, h)))
+    want = stack([ref.attention(q[b], k[b], v[b], dy[b], True, d ** -0.5) for b in range(2)])
+    ts = [leaf(t) for t in (q, k, v)]
+    got = torch.autograd.grad(blocks().attention(*ts, causal=True), ts, dy.cuda())
+    for name, t in zip(("dq", "dk"), got):
+        value = want[name][0]
+        rounding = (value.to(dtype).double() - value).norm()
+        assert (t.cpu().double() - value).norm() <= 1.06 * 2 ** 0.5 * rounding + 2.0 ** -40, name
