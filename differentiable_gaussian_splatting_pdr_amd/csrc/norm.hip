@@ -70,6 +70,44 @@ struct Row {
   }
 };
 
+// A row on its way: as it is in memory, so that the next row's loads are in flight
+// while this one is worked on (16-byte accesses; others are loaded when opened).
+template <int FMT, int LANES, int CH, bool VEC>
+struct Ahead {
+  static constexpr int kPieces = FMT == kF32 ? 2 : 1, kSize = FMT == kF32 ? 4 : 2;
+  uint4 raw[VEC ? CH * kPieces : 1];
+  const void *p;
+  long long at;
+  __device__ __forceinline__ void load(const void *p_, long long at_, int cols, int l) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        const int c = column<LANES, CH, VEC>(j, 0, l);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          raw[j * kPieces + i] = c < cols ? *(const uint4 *)((const char *)p_ + (at_ + c) * kSize + i * 16)
+                                          : make_uint4(0, 0, 0, 0);
+      }
+    } else {
+      p = p_;
+      at = at_;
+    }
+  }
+  __device__ __forceinline__ void open(Row<FMT, LANES, CH, VEC> &row, int cols, int l) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < CH * 8; ++i) {
+        const uint4 w = raw[i * kSize / 16];
+        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+        const uint32_t word = words[i * kSize / 4 % 4];
+        row.v[i] = FMT == kF32 ? __uint_as_float(word) : dense::to_f<FMT>((uint16_t)(word >> (i % 2 * 16)));
+      }
+    } else {
+      row.load(p, at, cols, l);
+    }
+  }
+};
+
 // Sums of N values over the LANES lanes of a row, for all of them.  `red` has
 // room for two calls: each uses the half that the one before did not.
 template <int LANES, int N>
@@ -154,14 +192,22 @@ __global__ __launch_bounds__(kThreads) void k_norm_backward(Norm a) {
   dw.fill(0.f);
   db.fill(0.f);
   const long long step = (long long)gridDim.x * kRows;
-  for (long long first = (long long)blockIdx.x * kRows; first < a.rows; first += step) {
-    const long long r = first + threadIdx.x / LANES;
-    const bool there = r < a.rows;
-    if (LANES <= 64 && !there) break;
+  // (a row of several waves is a workgroup's: all of them go round as often)
+  long long r = (long long)blockIdx.x * kRows + threadIdx.x / LANES;
+  Ahead<FMT, LANES, CH, VEC> next_x, next_g;
+  float2 next_st = make_float2(0.f, 0.f);
+  auto fetch = [&](long long row) {
+    next_x.load(a.x, row * a.ldx, a.cols, l);
+    next_g.load(a.dy, row * a.lddy, a.cols, l);
+    next_st = *(const float2 *)(a.stats + 2 * row);
+  };
+  if (r < a.rows) fetch(r);
+  for (; r < a.rows; r += step) {
     R x, g;
-    x.load(a.x, r * a.ldx, a.cols, l);
-    g.load(a.dy, r * a.lddy, a.cols, l);
-    const float2 st = *(const float2 *)(a.stats + 2 * r);
+    next_x.open(x, a.cols, l);
+    next_g.open(g, a.cols, l);
+    const float2 st = next_st;
+    if (r + step < a.rows) fetch(r + step);
     float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < CH * 8; ++i) {
