@@ -219,17 +219,19 @@ class LayerNorm(torch.autograd.Function):
     @staticmethod
     @_once
     def backward(ctx, dy):
+        # autograd's thread takes several times as long for a line as the caller's: few of them
         x, weight, stats = ctx.saved_tensors
-        need = ctx.needs_input_grad
+        need_x, need_w, need_b, _ = ctx.needs_input_grad
         rows, cols = x.shape
         dy = _rows(dy)
-        dx = _packed(x) if need[0] else None
-        dw = _packed(weight) if need[1] else None
-        db = torch.empty((cols,), dtype=x.dtype, device=x.device) if need[2] else None
+        dx = torch.empty_like(x) if need_x else None
+        dw = torch.empty_like(weight) if need_w else None
+        db = x.new_empty(cols) if need_b else None
         _call("pdr_layer_norm_backward",
-              _lib.pdr_layer_norm(_FMT[x.dtype], rows, cols, ctx.eps, x.data_ptr(), _ld(x), _pointer(weight), None,
-                                  None, 0, stats.data_ptr(), dy.data_ptr(), _ld(dy), _pointer(dx), cols or 1,
-                                  _pointer(dw), _pointer(db)), x.device)
+              _lib.pdr_layer_norm(_FMT[x.dtype], rows, cols, ctx.eps, x.data_ptr(), _ld(x),
+                                  None if weight is None else weight.data_ptr(), None, None, 0, stats.data_ptr(),
+                                  dy.data_ptr(), _ld(dy), dx.data_ptr() if need_x else None, cols or 1,
+                                  dw.data_ptr() if need_w else None, db.data_ptr() if need_b else None), x.device)
         return dx, dw, db, None
 
 

@@ -22,6 +22,7 @@ from .splat import _FMT
 
 # the current stream's handle, without the stream object around it
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice   # torch.cuda.current_device once a tensor is on a device
 
 _ACTS = {"none": _lib.PDR_ACT_NONE, "relu": _lib.PDR_ACT_RELU, "silu": _lib.PDR_ACT_SILU,
          "gelu": _lib.PDR_ACT_GELU}
@@ -56,8 +57,8 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
     """t as [rows, columns] with packed columns; a view where its strides allow."""
     if t.dim() != 2:
         t = t.reshape(t.shape[:-1].numel(), t.shape[-1])
-    if t.numel() and (t.stride(1) != 1 and t.shape[1] > 1
-                      or not t.shape[1] <= t.stride(0) <= _MAX_LD):
+    if not t.is_contiguous() and t.numel() and (t.stride(1) != 1 and t.shape[1] > 1
+                                                or not t.shape[1] <= t.stride(0) <= _MAX_LD):
         t = t.contiguous()
     return t
 
@@ -77,7 +78,7 @@ _CALLS = {}
 
 def _call(name: str, args, device):
     """Run an entry point in a workspace of its size, on the current stream."""
-    if torch.cuda.current_device() != device.index:
+    if _current_device() != device.index:
         with torch.cuda.device(device):
             return _call(name, args, device)
     if name not in _CALLS:
