@@ -175,18 +175,17 @@ __device__ __forceinline__ int lane_again() {
 }
 
 // The order that a stretch of products is to run in: AHEAD reads of LDS first, then
-// to each of MFMAS matrix instructions EACH more reads, until there are READS, and
-// VALU other instructions.  Left alone, the compiler reads a fragment, waits for it
-// and uses it, one after another.
-template <int AHEAD, int READS, int EACH, int MFMAS, int VALU = 0>
+// GROUPS times MFMAS matrix instructions and EACH more reads, until there are READS.
+// Left alone, the compiler reads a fragment, waits for it and uses it, one after
+// another.
+template <int AHEAD, int READS, int EACH, int GROUPS, int MFMAS>
 __device__ __forceinline__ void interleave() {
-  constexpr int kMfma = 0x8, kRead = 0x100, kValu = 0x2;
+  constexpr int kMfma = 0x8, kRead = 0x100;
   __builtin_amdgcn_sched_group_barrier(kRead, AHEAD, 0);
 #pragma unroll
-  for (int i = 0; i < MFMAS; ++i) {
-    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+  for (int i = 0; i < GROUPS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kMfma, MFMAS, 0);
     if (AHEAD + i * EACH < READS) __builtin_amdgcn_sched_group_barrier(kRead, EACH, 0);
-    if (VALU > 0) __builtin_amdgcn_sched_group_barrier(kValu, VALU, 0);
   }
 }
 
@@ -347,6 +346,21 @@ struct Core {
     const s16x4 y = transposed((lds_s16x4 *)(uintptr_t)(uint32_t)lo);
     const s16x4 z = transposed((lds_s16x4 *)(uintptr_t)(uint32_t)hi);
     return __builtin_bit_cast(i32x4, __builtin_shufflevector(y, z, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  // The order of N calls of along(), after OTHER reads, and of across() over 32 N rows.
+  template <int N, int OTHER = 0>
+  static __device__ __forceinline__ void pace_along() {
+    if constexpr (FMT == kF32)
+      interleave<OTHER + 3, OTHER + N * kSteps, 1, N * kSteps, 4>();
+    else
+      interleave<OTHER + 6, OTHER + N * kSteps, 1, N * kSteps, 1>();
+  }
+  template <int N>
+  static __device__ __forceinline__ void pace_across() {
+    if constexpr (FMT == kF32)  // two values of each lane to a read
+      interleave<4, N * 8 * kBlocks, 1, N * 8 * kBlocks, 2>();
+    else
+      interleave<8, N * 4 * kBlocks, 2, N * 2 * kBlocks, 1>();
   }
   // ---- what is not finite where a mask hides it
   //

@@ -193,7 +193,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
     fill(dp, start_dp);
     C::along(s, sk, u, q, lanes);
     C::along(dp, sv, u, dy, lanes);
-    if constexpr (FMT != kF32) interleave<6, 2 * C::kSteps, 1, 2 * C::kSteps>();
+    C::template pace_along<2>();
     const int key0 = t * kKeys + u * 32;
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
       gradients(s, sk, sv, t, u);
       scaled.hold(s, sums);
       across32<C>(sums, sk, u, s, lanes);
-      if constexpr (FMT != kF32) interleave<8, 4 * C::kBlocks, 2, 2 * C::kBlocks>();
+      C::template pace_across<1>();
     }
   }
   const int lane_now = lane_again(), row_now = row0 + wave * 32 + (lane_now & 31);
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(64 * NW) void k_backward_q_few(Args a) {
     fill(dp, start_dp);
     C::along(s, sk, 0, q, lanes);
     C::along(dp, sk + L::kBytes, 0, dy, lanes);
-    if constexpr (FMT != kF32) interleave<6, 2 * C::kSteps, 1, 2 * C::kSteps>();
+    C::template pace_along<2>();
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       float p = s[r], ds = dp[r];
@@ -385,6 +385,7 @@ __global__ __launch_bounds__(64 * NW) void k_backward_q_few(Args a) {
     gradients(s, sk, t);
     scaled.hold(s, sums);
     across32<C>(sums, sk, 0, s, lanes);
+    C::template pace_across<1>();
   }
   // the waves' sums, where their keys were
   __syncthreads();
@@ -501,6 +502,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_kv(Args a
       }
       C::along(s, sq, u, k, lanes);
       C::along(dp, sy, u, v, lanes);
+      if constexpr (FMT == kF32) C::template pace_along<2, 8>();
       const int r0 = t * kRows + u * 32;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
@@ -519,6 +521,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_kv(Args a
       across32<C>(dv, sy, u, s, lanes);
       scaled.hold(dp, dk);
       across32<C>(dk, sq, u, dp, lanes);
+      if constexpr (FMT == kF32) C::template pace_across<2>();
     }
   }
   const int lane_now = lane_again(), half_now = lane_now >> 5, key_now = key0 + wave * 32 + (lane_now & 31);

@@ -166,7 +166,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_forward(Args a) {
       clear(s[u]);
       C::along(s[u], sk, u, q, lanes);
     }
-    if constexpr (FMT != kF32) interleave<6, 2 * C::kSteps, 1, 2 * C::kSteps>();
+    C::template pace_along<2>();
     if constexpr (decltype(masked)::value) {
       const int seen = row.seen - t * kKeys;
 #pragma unroll
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_forward(Args a) {
     } else {
       query.template weigh<2>(s, a.scale2);
       query.template take<2>(sv, s, lanes);
-      if constexpr (FMT != kF32) interleave<8, 8 * C::kBlocks, 2, 4 * C::kBlocks>();
+      C::template pace_across<2>();
     }
   };
   // tiles that all rows of the workgroup see, and the others
@@ -236,11 +236,15 @@ __global__ __launch_bounds__(64 * NW, FMT == kF32 && DP > 64 ? 1 : 2) void k_for
   const int begin = part * each < all ? part * each : all;
   const int end = begin + each < all ? begin + each : all;
   i32x4 keys_now[C::kSteps], keys_next[C::kSteps], q[C::kSteps];
+  C::fetch_row(q, row_at(a.q, at, row, head, group, C::kSize), a.dim, half, row.there);
   if (begin < end) {
     C::fetch_rows(keys_now, k, begin * kKeys, at.nk, a.dim, lane);
     load.tokens(v, begin * kKeys, at.nk, ring);
   }
-  C::fetch_row(q, row_at(a.q, at, row, head, group, C::kSize), a.dim, half, row.there);
+  // The compiler waits for these here; left to the loop, it would wait in each turn for
+  // all that is in flight, the next tile included.
+#pragma unroll
+  for (int i = 0; i < C::kSteps; ++i) asm volatile("" : "+v"(q[i]), "+v"(keys_now[i]));
   for (int t = begin; t < end; ++t) {
     const lds_char *const sv = ring + ((t - begin) & 1) * L::kBytes;
     if (t + 1 < end) {
@@ -261,10 +265,12 @@ __global__ __launch_bounds__(64 * NW, FMT == kF32 && DP > 64 ? 1 : 2) void k_for
       careful = C::any_not_finite(sv, 0, lane);
     }
     query.template weigh<1>(s, a.scale2);
-    if (careful)
+    if (careful) {
       query.template take_carefully<1>(sv, s, lanes, half, row.seen - t * kKeys);
-    else
+    } else {
       query.template take<1>(sv, s, lanes);
+      C::template pace_across<1>();
+    }
 #pragma unroll
     for (int i = 0; i < C::kSteps; ++i) keys_now[i] = keys_next[i];
   }
