@@ -35,7 +35,6 @@ using dense::kBf16;
 using dense::kF16;
 using dense::kF32;
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -387,10 +386,10 @@ struct Core {
       bad |= !finite(read<i32x4>((int)(uintptr_t)tile + u * 32 * kRowBytes + i * 1024 + lane * 16));
     return __any(bad);
   }
-  // across() of rows 32 u .. 32 u + 31 under weights w; this lane's column sees rows
-  // [low, high) of them.
+  // across() of rows 32 u .. 32 u + 31 under weights w; this lane's column sees the
+  // first `seen` of them.
   static __device__ __forceinline__ void across_careful(f32x16 (&c)[kBlocks], const lds_char *tile, int u,
-                                                        const f32x16 &w, const Lane &at, int half, int low, int high) {
+                                                        const f32x16 &w, const Lane &at, int half, int seen) {
     const int first = here((int)(uintptr_t)tile + at.column);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -430,7 +429,7 @@ struct Core {
               v = read<float>(from + 4 * i);
             else
               v = dense::to_f<FMT>((uint16_t)read<short>(from + 2 * i));
-            if (row >= low && row < high && !(fabsf(v) < INFINITY)) c[b][r + i] += v;
+            if (row < seen && !(fabsf(v) < INFINITY)) c[b][r + i] += v;
           }
         }
     }
@@ -509,18 +508,7 @@ struct Loader {
       issue(from_y, (r * y.row + c) | out, lds + kBytes, i);
     }
   }
-  // The same of a group's rows, of one tensor and of two.
-  __device__ __forceinline__ void grouped(const Source &x, int first, int rows, const FastDiv &group,
-                                          lds_char *lds) const {
-    const int token0 = (int)fdiv((uint32_t)first, group);
-    const char *const from = x.base + (long long)token0 * x.row;
-#pragma unroll
-    for (int i = 0; i < kIssues; ++i) {
-      const int r = first + row_of(i);
-      const uint32_t token = fdiv((uint32_t)r, group), g = (uint32_t)r - token * group.d;
-      issue(from, ((token - token0) * x.row + g * x.head + byte_of(i)) | outside(r >= rows), lds, i);
-    }
-  }
+  // The same of a group's rows.
   __device__ __forceinline__ void grouped(const Source &x, const Source &y, int first, int rows,
                                           const FastDiv &group, lds_char *lds) const {
     const int token0 = (int)fdiv((uint32_t)first, group);

@@ -131,20 +131,21 @@ struct Sizes {
 };
 
 // Whether 32 rows go to a workgroup whose waves share the keys, instead of 128 whose
-// waves share tiles of keys: where a sequence has no more, and where the larger
-// workgroups are fewer than the compute units.  The gradient's smaller ones pay for
-// a start of their own only along many keys; where fp32 workgroups of 64 values a
-// head see different numbers of keys, one to a compute unit waits for the longest.
-// Larger against smaller, forward / forward's and all gradients' time, us:
-//   bf16 2 x 512, 8 heads of 128      (64 workgroups)   19 /  52     15 /  76
-//   bf16 8192, 2 heads of 128        (128)             154 / 340    116 / 256
-//   fp32 4 x 1024, 8 heads of 64     (256, causal)      88 / 244     67 / 211
-//   the same, not causal             (256)              87 / 304     98 / 323
-//   fp32 4 x 1024, 8 heads of 128    (256, causal)     146 / 414    135 / 477
-bool takes_few(const pdr_attention &p, bool gradient) {
+// waves share tiles of keys: where a sequence has no more, where the larger workgroups
+// are fewer than the compute units, and where fp32 workgroups of 64 values a head see
+// different numbers of keys, as one to a compute unit waits for the longest.
+// Larger against smaller, forward / all gradients, us:
+//   bf16 2 x 512, 8 heads of 128      (64 workgroups)   18 /  49     13 /  47
+//   bf16 4 x 1024, 4 heads of 128    (128)              27 /  73     24 /  68
+//   bf16 8192, 2 heads of 128        (128)             159 / 302    125 / 216
+//   fp32 4 x 1024, 8 heads of 64     (256, causal)      80 / 216     58 / 179
+//   the same, not causal             (256)              79 / 277     89 / 290
+//   fp32 4 x 1024, 8 heads of 128    (256, causal)     146 / 395    132 / 438
+//   fp32 8 x 1024, 8 heads of 64     (512, causal)     110 / 305    102 / 319
+bool takes_few(const pdr_attention &p) {
   const Sizes n(p);
   const bool uneven = p.fmt == kF32 && p.causal && p.dim <= 64 && n.wide < 512;
-  if (n.rows > 32 && !uneven && (n.wide >= 256 || (gradient && p.fmt != kF32 && n.keys < 2048))) return false;
+  if (n.rows > 32 && !uneven && n.wide >= 256) return false;
   // a launch has fewer than 2^32 threads
   const long long each = p.heads / p.kv_heads;
   return (p.q_offsets ? (p.q_rows * each >> 5) + n.seqs + 2 : (n.rows + 31) / 32 * n.seqs) * p.kv_heads < 1 << 22;
@@ -160,7 +161,7 @@ struct Plan {
 Plan plan_of(const pdr_attention &p) {
   const Sizes n(p);
   const long long units = (n.rows + 31) / 32 * n.seqs * p.kv_heads;
-  Plan plan = {takes_few(p, false), 4, 1, 0, 0};
+  Plan plan = {takes_few(p), 4, 1, 0, 0};
   if (!plan.few || !n.rows) return plan;
   if (n.keys <= kAlone) {
     // eight waves where that leaves one workgroup to a compute unit; their LDS holds no fp32 rows of 128
@@ -313,7 +314,7 @@ int pdr_attention_backward(const pdr_attention *p, void *workspace, size_t works
   a.part_k = (float *)((char *)workspace + 2 * row_values(*p));
   hipError_t e = hipSuccess;
   if (tokens_of(*p)) {
-    const bool few = takes_few(*p, true);
+    const bool few = takes_few(*p);
     a.q_tiles = tiles_of(*p, p->q_rows, p->heads / p->kv_heads, few ? attend::kLogFew : attend::kLogWide);
     e = few ? attend::launch_backward_q_few(a, p->fmt, st) : attend::launch_backward_q(a, p->fmt, st);
   }
