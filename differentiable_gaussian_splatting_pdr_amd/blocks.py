@@ -151,7 +151,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
     Tokens outside of all sequences get zeros.
     causal: a query sees the keys up to its own, the last query being at the last
     key: j <= i + (keys - queries).  A query that sees no key gets zeros.
-    scale: positive; D ** -0.5 by default.  D is at most 128.
+    scale: in [2^-64, 2^64]; D ** -0.5 by default.  D is at most 128.
     """
     _check("q", q)
     _check("k", k, q.dtype, q.device)
@@ -167,8 +167,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
     if kv_heads < 1 or heads < 1 or heads % kv_heads:
         raise ValueError("q's heads must be a multiple of k's: %d, %d" % (heads, kv_heads))
     scale = d ** -0.5 if scale is None else float(scale)
-    if not 0 < scale < float("inf"):
-        raise ValueError("scale must be positive and finite")
+    if not 2.0 ** -64 <= scale <= 2.0 ** 64:
+        raise ValueError("scale must be in [2^-64, 2^64]")
     if offsets is None:
         if key_offsets is not None:
             raise ValueError("key_offsets needs offsets")

@@ -47,7 +47,8 @@ int check_attention(const pdr_attention *p, bool backward) {
   if (p->kv_heads < 1 || p->kv_heads > 65536 || p->heads < 1 || p->heads > 65536 || p->heads % p->kv_heads)
     return PDR_ERR_INVALID_ARG;
   if (p->dim < 1 || p->dim > 128 || p->dim % (16 / fmt_bytes(p->fmt))) return PDR_ERR_INVALID_ARG;
-  if (!(p->scale > 0.f) || !(p->scale < INFINITY)) return PDR_ERR_INVALID_ARG;
+  // the backward's sums start from lse / scale, which has to be finite
+  if (!(p->scale >= 0x1p-64f) || !(p->scale <= 0x1p64f)) return PDR_ERR_INVALID_ARG;
   const bool packed = p->q_offsets != nullptr;
   if (packed != (p->k_offsets != nullptr) || (packed && p->key_lengths)) return PDR_ERR_INVALID_ARG;
   if (!aligned(p->q_offsets, 4) || !aligned(p->k_offsets, 4) || !aligned(p->key_lengths, 4) || !aligned(p->lse, 4))
@@ -182,9 +183,11 @@ Plan plan_of(const pdr_attention &p) {
 }
 
 // Parts that the rows are cut into for dk and dv, until the card has work; the
-// bytes of their sums.
+// bytes of their sums.  With 256 rows a part instead of 128, fp16 packed sequences of up
+// to 777 take 74 us instead of 49 (all else within 5 %), with 64 bf16 2 x 512 43
+// instead of 35; with 1024 workgroups fp32 4 x 1024 143 instead of 118.
 constexpr long long kKeyUnits = 512;  // workgroups of 128 keys to aim for
-constexpr long long kKeyRows = 256;   // rows of a part, at least
+constexpr long long kKeyRows = 128;   // rows of a part, at least
 int key_splits(const pdr_attention &p, size_t *bytes) {
   *bytes = 0;
   const Sizes n(p);

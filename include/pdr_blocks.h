@@ -61,7 +61,7 @@ typedef struct {
     long long q_rows, k_rows;
     const int *q_offsets, *k_offsets;  /* both or none */
     const int *key_lengths;            /* only without offsets */
-    float scale;                       /* finite, > 0 */
+    float scale;                       /* in [2^-64, 2^64] */
     const void *q; long long q_row, q_head, q_batch;
     const void *k; long long k_row, k_head, k_batch;
     const void *v; long long v_row, v_head, v_batch;

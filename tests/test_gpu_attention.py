@@ -394,3 +394,18 @@ def test_gradients_are_as_near_as_their_types(n, h, hk, d, dtype):
         value = want[name][0]
         rounding = (value.to(dtype).double() - value).norm()
         assert (t.cpu().double() - value).norm() <= 1.06 * 2 ** 0.5 * rounding + left[name], name
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("scale,spread", [(2.0 ** -64, 1.0), (2.0 ** 64, 2.0 ** -32)])
+def test_largest_and_smallest_scales(scale, spread, dtype):
+    # (fp16 does not hold such inputs and gradients)
+    run_batch(1, 150, 150, 2, 1, 64, dtype, True, scale=scale, spread=spread, seed=10)
+    run_batch(1, 3, 600, 2, 1, 64, dtype, False, scale=scale, spread=spread, seed=11)
+
+
+def test_scales_out_of_range_are_refused():
+    q = torch.zeros(1, 2, 1, 8, device="cuda")
+    for scale in (2.0 ** -65, 2.0 ** 65):
+        with pytest.raises(ValueError):
+            blocks().attention(q, q, q, scale=scale)
