@@ -47,9 +47,9 @@ def _heads(t: torch.Tensor) -> torch.Tensor:
     d, strides = t.shape[-1], t.stride()
     if d % per:
         return torch.nn.functional.pad(t, (0, -d % per))
-    if t.numel() and (strides[-1] != 1 or any(s % per for s in strides[:-1]) or t.data_ptr() % 16
-                      or strides[-3] > _MAX_ROW or strides[-2] > _MAX_HEAD
-                      or strides[-2] * (t.shape[-2] - 1) > _MAX_HEADS):
+    batch, row, head = strides[0], strides[-3], strides[-2]
+    if ((strides[-1] != 1 or (batch | row | head) % per or t.data_ptr() % 16 or row > _MAX_ROW or head > _MAX_HEAD
+         or head * (t.shape[-2] - 1) > _MAX_HEADS) and t.numel()):
         return t.clone(memory_format=torch.contiguous_format)
     return t
 
@@ -64,19 +64,21 @@ def _place(t):
     return t.data_ptr(), strides[0], strides[1], 0
 
 
-def _attention_args(q, k, v, o, lse, meta, index, dy=None, dq=None, dk=None, dv=None):
-    """pdr_attention of tensors that _heads has seen; index: (offsets, key_offsets, key_lengths)."""
+def _attention_args(q, k, v, o, lse, meta, index, *gradients):
+    """pdr_attention of tensors that _heads has seen; index: (offsets, key_offsets, key_lengths);
+    gradients: dy, dq, dk and dv, or none."""
     offsets, key_offsets, key_lengths = index
     batch = q.shape[0] if offsets is None else offsets.shape[0] - 1
     causal, scale = meta
-    # in the struct's order
+    heads, d = q.shape[-2:]
+    # in the struct's order; what is left out is 0
     return _lib.pdr_attention(
-        _FMT[q.dtype], causal, batch, q.shape[-2], k.shape[-2], q.shape[-1], q.shape[-3], k.shape[-3],
+        _FMT[q.dtype], causal, batch, heads, k.shape[-2], d, q.shape[-3], k.shape[-3],
         None if offsets is None else offsets.data_ptr(),
         None if offsets is None else key_offsets.data_ptr(),
         None if key_lengths is None else key_lengths.data_ptr(), scale,
         *_place(q), *_place(k), *_place(v), *_place(o), None if lse is None else lse.data_ptr(),
-        *_place(dy), *_place(dq), *_place(dk), *_place(dv))
+        *(x for t in gradients for x in _place(t)))
 
 
 def _packed(t):
@@ -144,7 +146,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
     Sequences of one length: q [B, Sq, Hq, D], k and v [B, Sk, Hk, D]; Hq is a
     multiple of Hk, and query head h reads key head h // (Hq // Hk).
     key_lengths (int32 [B], on the device): how many of its Sk keys each sequence
-    has, as for a cache that is being filled.
+    has, as for a cache that is being filled.  The queries are its last ones: where
+    queries are padded too, pack the sequences instead.
     Packed sequences: q [T, Hq, D], k and v [Tk, Hk, D] with offsets (int32
     [n + 1], on the device, not descending): sequence b has the queries
     offsets[b] .. offsets[b + 1] - 1, and the same keys or those of key_offsets.

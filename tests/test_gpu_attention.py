@@ -409,3 +409,36 @@ def test_scales_out_of_range_are_refused():
     for scale in (2.0 ** -65, 2.0 ** 65):
         with pytest.raises(ValueError):
             blocks().attention(q, q, q, scale=scale)
+
+
+def test_one_tensor_for_all_and_shared_batches():
+    # q, k and v one tensor, whose gradient is the sum; keys that all sequences share (no stride between them)
+    b = blocks()
+    x, dy = normal(1, 2, 70, 3, 64), normal(2, 2, 70, 3, 64)
+    want = stack([ref.attention(x[i], x[i], x[i], dy[i], True, 0.125) for i in range(2)])
+    t = leaf(x)
+    (g,) = torch.autograd.grad(b.attention(t, t, t, causal=True), t, dy.cuda())
+    value = sum(want[n][0] for n in ("dq", "dk", "dv"))
+    bound = sum(want[n][1] for n in ("dq", "dk", "dv")) + 2 * 2.0 ** -24 * value.abs()   # and two sums in fp32
+    ref.within(g, (value, bound), "one tensor")
+    k = normal(3, 1, 70, 3, 64)
+    want = stack([ref.attention(x[i], k[0], k[0], None, False, 0.125) for i in range(2)])
+    shared = k.cuda().expand(2, 70, 3, 64)
+    ref.within(b.attention(x.cuda(), shared, shared), want["y"], "shared keys")
+
+
+def test_lengths_and_offsets_beyond_the_tokens():
+    # taken to the tokens' ends
+    b = blocks()
+    q, k = normal(1, 3, 4, 2, 64, dtype=BF).cuda(), normal(2, 3, 50, 2, 64, dtype=BF).cuda()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    assert torch.equal(b.attention(q, k, k, causal=True, key_lengths=i32(-3, 51, 2 ** 31 - 1)),
+                       b.attention(q, k, k, causal=True, key_lengths=i32(0, 50, 50)))
+    x = normal(3, 64, 2, 64, dtype=BF).cuda()
+    for bad, good in (((-5, 40, 1000), (0, 40, 64)), ((64, 2 ** 31 - 1), (64, 64)), ((-2 ** 31, -1, 3), (0, 0, 3))):
+        t, u = x.clone().requires_grad_(), x.clone().requires_grad_()
+        y, z = b.attention(t, t, t, offsets=i32(*bad)), b.attention(u, u, u, offsets=i32(*good))
+        assert torch.equal(y, z)
+        y.sum().backward()
+        z.sum().backward()
+        assert torch.equal(t.grad, u.grad)
