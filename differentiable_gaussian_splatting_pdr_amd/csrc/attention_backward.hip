@@ -280,7 +280,7 @@ __device__ __forceinline__ void store_keys(const Args &a, const Place &at, const
 
 // dq where 128 rows to a workgroup would leave compute units without one: 32 rows,
 // whose waves take parts of the keys each, in LDS of their own (fp32 4 x 1024, 8 heads
-// of 64, causal: 82 us, 127 with the larger ones).
+// of 64, causal: 82 us, about 120 with the larger ones).
 template <int FMT, int DP, int NW>
 __global__ __launch_bounds__(64 * NW) void k_backward_q_few(Args a) {
 #if defined(__HIP_DEVICE_COMPILE__)
