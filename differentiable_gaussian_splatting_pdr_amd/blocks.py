@@ -241,7 +241,7 @@ class LayerNorm(torch.autograd.Function):
 def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
                bias: torch.Tensor | None = None, eps: float = 1e-5) -> torch.Tensor:
     """(x - mean) / sqrt(var + eps) * weight + bias over the last dimension of x
-    [..., N]; weight and bias [N], or None for one and zero.
+    [..., N]; weight and bias [N], or None for one and zero.  N is at most 2^30.
 
     The squares of centred values are summed in fp32 and have to be in its range.
     """

@@ -212,7 +212,8 @@ bool good_rows(const void *p, long long ld, long long rows, long long cols, int 
 }
 
 int check_norm(const pdr_layer_norm *p, bool backward) {
-  if (!p || !good_fmt(p->fmt) || !good_len(p->rows) || !good_len(p->cols)) return PDR_ERR_INVALID_ARG;
+  if (!p || !good_fmt(p->fmt) || !good_len(p->rows) || p->cols < 0 || p->cols > norm::kMaxCols)
+    return PDR_ERR_INVALID_ARG;
   if (!(p->eps >= 0.f) || !(p->eps < INFINITY)) return PDR_ERR_INVALID_ARG;
   if (!good_rows(p->x, p->ldx, p->rows, p->cols, p->fmt) || !good_ptr(p->weight, p->fmt) ||
       !good_ptr(p->bias, p->fmt) || !aligned(p->stats, 8))

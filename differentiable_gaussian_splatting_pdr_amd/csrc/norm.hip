@@ -252,7 +252,8 @@ __global__ __launch_bounds__(kThreads) void k_norm_backward(Norm a) {
 }
 
 // Rows too long for registers: a workgroup goes over one row several times, from
-// the caches.
+// the caches.  Columns are counted in 32 bits: rows end at kMaxCols, so that a step
+// behind the end does not leave them.
 __global__ __launch_bounds__(kThreads) void k_norm_long(Norm a) {
   __shared__ float red[2][4][3];
   int turn = 0;
@@ -327,9 +328,9 @@ __global__ __launch_bounds__(kThreads) void k_norm_long_backward(Norm a) {
 
 // Sums of dy xh and dy over a block of rows: a column to a thread.
 __global__ __launch_bounds__(kThreads) void k_norm_columns(Norm a, int rows_each) {
-  const int c = blockIdx.y * kThreads + threadIdx.x;
+  const int c = blockIdx.x * kThreads + threadIdx.x;
   if (c >= a.cols) return;
-  const long long r0 = (long long)blockIdx.x * rows_each;
+  const long long r0 = (long long)blockIdx.y * rows_each;
   const long long r1 = r0 + rows_each < a.rows ? r0 + rows_each : a.rows;
   float dw = 0.f, db = 0.f;
 #pragma unroll 4
@@ -339,29 +340,34 @@ __global__ __launch_bounds__(kThreads) void k_norm_columns(Norm a, int rows_each
     dw = fmaf(g, (dense::load1(a.x, a.fmt, r * a.ldx + c) - st.x) * st.y, dw);
     db += g;
   }
-  a.part[(long long)blockIdx.x * a.cols + c] = dw;
-  a.part[((long long)gridDim.x + blockIdx.x) * a.cols + c] = db;
+  a.part[(long long)blockIdx.y * a.cols + c] = dw;
+  a.part[((long long)gridDim.y + blockIdx.y) * a.cols + c] = db;
 }
 
-// dweight and dbias: the sums of the blocks' sums; 32 columns to a workgroup.
+// dweight and dbias: the sums of the blocks' sums; 32 columns to a workgroup, and the
+// next 32 of as many workgroups as there are.
 __global__ __launch_bounds__(kThreads) void k_norm_join(Norm a, int blocks) {
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), ty = threadIdx.x >> 5, which = blockIdx.y;
+  const int ty = threadIdx.x >> 5, which = blockIdx.y;
   void *const out = which ? a.dbias : a.dweight;
   if (!out) return;
   const float *const part = a.part + (long long)which * blocks * a.cols;
-  float s = 0.f;
-  if (c < a.cols) {
-#pragma unroll 8
-    for (int i = ty; i < blocks; i += 8) s += part[(long long)i * a.cols + c];
-  }
   __shared__ float red[8][32];
-  red[ty][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (ty == 0 && c < a.cols) {
-    float t = 0.f;
+  for (int first = blockIdx.x * 32; first < a.cols; first += gridDim.x * 32) {
+    const int c = first + (threadIdx.x & 31);
+    float s = 0.f;
+    if (c < a.cols) {
+#pragma unroll 8
+      for (int i = ty; i < blocks; i += 8) s += part[(long long)i * a.cols + c];
+    }
+    __syncthreads();
+    red[ty][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (ty == 0 && c < a.cols) {
+      float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += red[i][threadIdx.x];
-    dense::store1(out, a.fmt, c, t);
+      for (int i = 0; i < 8; ++i) t += red[i][threadIdx.x];
+      dense::store1(out, a.fmt, c, t);
+    }
   }
 }
 
@@ -438,7 +444,7 @@ hipError_t launch_norm_backward(const Norm &a, hipStream_t st) {
     if (a.dx)
       hipLaunchKernelGGL(k_norm_long_backward, dim3(workgroups(a.rows, 4096)), dim3(kThreads), 0, st, a);
     if (a.part)
-      hipLaunchKernelGGL(k_norm_columns, dim3((unsigned)blocks, (unsigned)((a.cols + kThreads - 1) / kThreads)),
+      hipLaunchKernelGGL(k_norm_columns, dim3((unsigned)((a.cols + kThreads - 1) / kThreads), (unsigned)blocks),
                          dim3(kThreads), 0, st, a, (int)((a.rows + blocks - 1) / blocks));
   } else if (a.rows) {
     by_format(a, [&](auto fmt) {
@@ -452,7 +458,8 @@ hipError_t launch_norm_backward(const Norm &a, hipStream_t st) {
     });
   }
   if (a.dweight || a.dbias)
-    hipLaunchKernelGGL(k_norm_join, dim3((unsigned)((a.cols + 31) / 32), 2), dim3(kThreads), 0, st, a, blocks);
+    // (a launch has fewer than 2^32 threads)
+    hipLaunchKernelGGL(k_norm_join, dim3(workgroups((a.cols + 31) / 32, 1 << 20), 2), dim3(kThreads), 0, st, a, blocks);
   return hipGetLastError();
 }
 

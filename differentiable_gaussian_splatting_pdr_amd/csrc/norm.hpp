@@ -12,6 +12,8 @@
 namespace pdr {
 namespace norm {
 
+constexpr long long kMaxCols = 1 << 30;
+
 struct Norm {
   const void *x, *weight, *bias, *dy;
   void *y, *dx, *dweight, *dbias;

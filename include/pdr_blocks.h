@@ -91,8 +91,8 @@ int pdr_attention_backward(const pdr_attention *p, void *workspace, size_t works
  *   y = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(var + eps)
  * with the variance over cols.  weight and bias [cols] or NULL (one and zero).
  * stats, if not NULL, receives (mean, rstd) of each row for the backward, fp32
- * [rows][2].  Rows are ld* elements apart; any alignment.  Lengths are below
- * 2^31 - 256. */
+ * [rows][2].  Rows are ld* elements apart; any alignment.  There are fewer than
+ * 2^31 - 256 rows, of at most 2^30 values. */
 typedef struct {
     int fmt;
     long long rows, cols;
