@@ -193,6 +193,7 @@ __device__ __forceinline__ int row_in(int r, int half) { return 8 * (r >> 2) + 4
 
 template <int FMT, int DP>  // DP: values a row has in LDS and registers (dim, rounded up)
 struct Core {
+  static constexpr int kFmt = FMT;
   static constexpr int kSize = FMT == kF32 ? 4 : 2;
   static constexpr int kPer = 16 / kSize;             // values of a 16-byte chunk
   static constexpr int kChunks = DP / kPer;           // of a row

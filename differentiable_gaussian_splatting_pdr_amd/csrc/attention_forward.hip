@@ -15,8 +15,16 @@ namespace {
 // The running softmax of a lane's query, in units of log2, and the sums of
 // values under it.  `most` follows the maximum only when that has grown by more
 // than kSlack: weights of up to 2^8 are as good as those up to 1, in sums of fp32
-// and in fp16's range, and nearly all tiles are spared a pass over the sums.
-constexpr float kSlack = 8.f;
+// and in the operands' range, and nearly all tiles are spared a pass over the sums.
+// fp16 weights enter the products times 2^12, so that the smallest are kept to 2^-37 of
+// the largest and not to 2^-25, which many keys' sum would show (65536 keys, all but
+// one of them 2^-24.5 of it: 0.0027 came out as 0.0039); what is left of the range, to
+// 2^16, is for a slack of 3 (with 2^14 and 1 there are more passes over the sums: 8 x 4096,
+// 16 heads of 128, 640 us instead of 614).
+template <int FMT>
+constexpr float kUp = FMT == kF16 ? 12.f : 0.f;  // log2 of that
+template <int FMT>
+constexpr float kSlack = FMT == kF16 ? 3.f : 8.f;
 template <class C>
 struct Query {
   f32x16 out[C::kBlocks];
@@ -37,7 +45,7 @@ struct Query {
 #pragma unroll
       for (int r = 0; r < 16; ++r) m = fmaxf(m, s[u][r]);
     m = fmaxf(m, other_half(m)) * scale2;
-    if (__any(m > most + kSlack)) {
+    if (__any(m > most + kSlack<C::kFmt>)) {
       // a lane that has seen nothing yet has no sums
       const float up = fmaxf(most, m), down = up == -INFINITY ? 1.f : exp2_(most - up);
       most = up;
@@ -47,7 +55,7 @@ struct Query {
 #pragma unroll
         for (int r = 0; r < 16; ++r) out[b][r] *= down;
     }
-    const float from = most == -INFINITY ? 0.f : most;  // nothing seen yet
+    const float from = most == -INFINITY ? 0.f : most - kUp<C::kFmt>;  // nothing seen yet
     // a tile's sum first: beside a key that takes most of the weight each of many small
     // ones would be rounded at its magnitude (65536 keys: 1.4e-3 of the sum)
     float tile = 0.f;
@@ -80,8 +88,9 @@ struct Query {
 __device__ __forceinline__ float weight_of(float most, float sum) {
   return most == -INFINITY && sum == 0.f ? 0.f : 1.f / sum;
 }
+template <int FMT>
 __device__ __forceinline__ float lse_of(float most, float sum) {
-  return most == -INFINITY && sum == 0.f ? INFINITY : most + __log2f(sum);
+  return most == -INFINITY && sum == 0.f ? INFINITY : most + (__log2f(sum) - kUp<FMT>);
 }
 
 // Scores of keys that the lane's query does not see; `seen` counts from the tile's
@@ -200,7 +209,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_forward(Args a) {
   const float sum = query.sum + other_half(query.sum);
   if (!row.there) return;
   if (a.lse && half == 0)
-    a.lse[rows_before(a, at, head) + mine + (lane & 31)] = lse_of(query.most, sum);
+    a.lse[rows_before(a, at, head) + mine + (lane & 31)] = lse_of<FMT>(query.most, sum);
   store_columns<C, FMT>(query.out, row_at(a.o, at, row, head, group, C::kSize), a.dim, half,
                         weight_of(query.most, sum));
 #endif
@@ -332,7 +341,7 @@ __global__ __launch_bounds__(64 * NW, FMT == kF32 && DP > 64 ? 1 : 2) void k_for
       for (int j = 0; j < 4; ++j) v[j] *= by;
       const Row r(a, at, row0 + i, rows);
       store4<FMT>(row_at(a.o, at, r, head, group, C::kSize) + d * C::kSize, v);
-      if (a.lse && d == 0) a.lse[before + i] = lse_of(most, total);
+      if (a.lse && d == 0) a.lse[before + i] = lse_of<FMT>(most, total);
     }
   }
 #endif
@@ -366,7 +375,7 @@ __global__ __launch_bounds__(256) void k_join(Args a, FastDiv quads, FastDiv row
   const float by = weight_of(most, total);
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] *= by;
-  if (a.lse && d == 0) a.lse[i] = lse_of(most, total);
+  if (a.lse && d == 0) a.lse[i] = lse_of<FMT>(most, total);
   // row i is head g of token n, for a key head
   const uint32_t head = fdiv(i, rows_each), in = i - head * rows_each.d;
   const uint32_t token = fdiv(in, a.group), g = in - token * a.group.d;

@@ -81,7 +81,8 @@ int pdr_attention_forward(const pdr_attention *p, void *workspace, size_t worksp
 /* delta_i = dy_i . o_i, ds_ij = p_ij (dy_i . v_j - delta_i), dq_i = scale sum_j ds_ij k_j,
  * dk_j = scale sum_i ds_ij q_i, dv_j = sum_i p_ij dy_i; sums over i are over
  * all heads that read the key's.  p and ds are rounded to fmt where they enter
- * the products (in fp16 under powers of two that keep them in its range). */
+ * the products, as p is in the forward (in fp16 under powers of two that keep them
+ * in its range: p to 2^-37 of a row's largest in the forward, to 2^-40 here). */
 long long pdr_attention_backward_workspace_bytes(const pdr_attention *p);
 int pdr_attention_backward(const pdr_attention *p, void *workspace, size_t workspace_bytes,
                            void *stream);

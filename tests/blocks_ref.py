@@ -39,12 +39,13 @@ def within(got, ref, what):
         what, share[at], at, got[at], value[at], bound[at])
 
 
-def attention(q, k, v, dy, causal, scale):
+def attention(q, k, v, dy, causal, scale, step=2.0 ** -25):
     """One sequence: q, dy [nq, H, D], k, v [nk, Hk, D] -> {"y", "dq", "dk", "dv"} of
-    (value, bound); the gradients only with dy."""
+    (value, bound); the gradients only with dy.  `step`: what a weight in fp16 may be off
+    by below its range, of the largest (2^-37 where weights are held near the range's end)."""
     dt = q.dtype
     u = 0.0 if dt == torch.float32 else U[dt] * (1 + 2.0 ** -7)
-    low = 2.0 ** -25 if dt == torch.float16 else TINY
+    low = step if dt == torch.float16 else TINY
     nq, h, d = q.shape
     nk, hk = k.shape[:2]
     g = h // hk

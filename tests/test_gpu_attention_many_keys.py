@@ -44,3 +44,16 @@ def test_sum_of_many_small_weights(queries, heads, at, gap, dtype):
     y, small = one_large_key(queries, heads, at, gap, dtype)
     want = 1 / (1 + small)
     assert ((y[..., 0] - want).abs() <= want * (1.1 * 2.0 ** -15 + 2.0 ** -17 + torch.finfo(dtype).eps / 2)).all()
+
+
+@GAPS
+@PLACES
+@CALLS
+def test_values_of_many_small_weights_in_fp16(queries, heads, at, gap):
+    # The others' share is small / (1 + small).  Their weights are all alike, so it is off by one weight's and its own
+    # rounding to fp16 (2^-11 each), what the above says of the sum, the products' sum (N / 16 steps follow one
+    # another, of 2^-25 each), and by N times half a weight's smallest step, which is 2^-37 of the largest.
+    y, small = one_large_key(queries, heads, at, gap, torch.float16)
+    want = small / (1 + small)
+    bound = want * (2 * 2.0 ** -11 + 1.1 * 2.0 ** -15 + 2.0 ** -17 + 2.0 ** -13) + N * 2.0 ** -37
+    assert ((y[..., 1] - want).abs() <= bound).all()
