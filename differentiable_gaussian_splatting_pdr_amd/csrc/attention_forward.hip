@@ -45,9 +45,10 @@ struct Query {
 #pragma unroll
       for (int r = 0; r < 16; ++r) m = fmaxf(m, s[u][r]);
     m = fmaxf(m, other_half(m)) * scale2;
-    if (__any(m > most + kSlack<C::kFmt>)) {
-      // a lane that has seen nothing yet has no sums
-      const float up = fmaxf(most, m), down = up == -INFINITY ? 1.f : exp2_(most - up);
+    const bool grows = m > most + kSlack<C::kFmt>;
+    if (__any(grows)) {
+      // another query's maximum changes nothing here; a lane that has seen nothing yet has no sums
+      const float up = grows ? m : most, down = up == -INFINITY ? 1.f : exp2_(most - up);
       most = up;
       sum *= down;
 #pragma unroll
