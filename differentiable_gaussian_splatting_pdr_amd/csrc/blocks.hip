@@ -228,9 +228,13 @@ norm::Norm norm_of(const pdr_layer_norm &p, bool backward) {
   return a;
 }
 
-long long norm_backward_bytes(const pdr_layer_norm &p) {
+// Bytes of the blocks' sums, and of what there is of each row for dweight.
+size_t norm_parts(const pdr_layer_norm &p) {
   if ((!p.dweight && !p.dbias) || !p.rows || !p.cols) return 0;
-  return 2LL * norm::norm_blocks(p.rows, p.cols) * p.cols * 4;
+  return 2 * (size_t)norm::norm_blocks(p.rows, p.cols) * p.cols * 4;
+}
+size_t norm_offsets(const pdr_layer_norm &p) {
+  return p.dweight && p.cols ? 4 * (size_t)norm::norm_offsets(p.rows, p.cols) : 0;
 }
 
 int check_dropout(const pdr_dropout_args *p) {
@@ -308,7 +312,7 @@ int pdr_layer_norm_forward(const pdr_layer_norm *p, void *, size_t, void *stream
 }
 long long pdr_layer_norm_backward_workspace_bytes(const pdr_layer_norm *p) {
   const int rc = check_norm(p, true);
-  return rc != PDR_OK ? rc : norm_backward_bytes(*p);
+  return rc != PDR_OK ? rc : (long long)(norm_parts(*p) + norm_offsets(*p));
 }
 int pdr_layer_norm_backward(const pdr_layer_norm *p, void *workspace, size_t workspace_bytes, void *stream) {
   const long long need = pdr_layer_norm_backward_workspace_bytes(p);
@@ -317,6 +321,7 @@ int pdr_layer_norm_backward(const pdr_layer_norm *p, void *workspace, size_t wor
   if (rc != PDR_OK) return rc;
   norm::Norm a = norm_of(*p, true);
   a.part = need ? (float *)workspace : nullptr;
+  a.offs = norm_offsets(*p) ? (float *)((char *)workspace + norm_parts(*p)) : nullptr;
   return status(norm::launch_norm_backward(a, (hipStream_t)stream));
 }
 

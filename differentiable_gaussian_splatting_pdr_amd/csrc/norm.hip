@@ -293,13 +293,14 @@ __global__ __launch_bounds__(kThreads) void k_norm_long(Norm a) {
   }
 }
 
+// dx, if it is wanted, and each row's offset for the columns' sums.
 __global__ __launch_bounds__(kThreads) void k_norm_long_backward(Norm a) {
   __shared__ float red[2][4][3];
   int turn = 0;
   for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const float2 st = *(const float2 *)(a.stats + 2 * r);
     float s[3] = {0.f, 0.f, 0.f};
-    for (int pass = 0; pass < 2; ++pass) {
+    for (int pass = 0; pass < (a.dx ? 2 : 1); ++pass) {
       const float off = s[2] * a.by_cols, m = s[0] * a.by_cols, mx = fmaf(-off, m, s[1] * a.by_cols);
       for (int c = threadIdx.x * 8; c < a.cols; c += kThreads * 8) {
         float x[8], g[8], w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
@@ -323,10 +324,13 @@ __global__ __launch_bounds__(kThreads) void k_norm_long_backward(Norm a) {
       }
       if (pass == 0) row_sum<256, 3>(s, red, turn);
     }
+    if (a.offs && threadIdx.x == 0) a.offs[r] = s[2] * a.by_cols;
   }
 }
 
-// Sums of dy xh and dy over a block of rows: a column to a thread.
+// Sums of dy xh and dy over a block of rows: a column to a thread.  xh is without what
+// the mean's rounding left in it, as elsewhere: with it, rows 1e4 deviations from zero
+// would all be off to one side (2000 rows: dweight by 0.4 of 64).
 __global__ __launch_bounds__(kThreads) void k_norm_columns(Norm a, int rows_each) {
   const int c = blockIdx.x * kThreads + threadIdx.x;
   if (c >= a.cols) return;
@@ -337,7 +341,8 @@ __global__ __launch_bounds__(kThreads) void k_norm_columns(Norm a, int rows_each
   for (long long r = r0; r < r1; ++r) {
     const float2 st = *(const float2 *)(a.stats + 2 * r);
     const float g = dense::load1(a.dy, a.fmt, r * a.lddy + c);
-    dw = fmaf(g, (dense::load1(a.x, a.fmt, r * a.ldx + c) - st.x) * st.y, dw);
+    const float xh = (dense::load1(a.x, a.fmt, r * a.ldx + c) - st.x) * st.y;
+    dw = fmaf(g, xh - (a.offs ? a.offs[r] : 0.f), dw);
     db += g;
   }
   a.part[(long long)blockIdx.y * a.cols + c] = dw;
@@ -437,11 +442,13 @@ int norm_blocks(long long rows, long long cols) {
   return (int)workgroups((rows + per - 1) / per, 512);
 }
 
+long long norm_offsets(long long rows, long long cols) { return cols > kLongRow ? rows : 0; }
+
 hipError_t launch_norm_backward(const Norm &a, hipStream_t st) {
   if (!a.cols) return hipSuccess;
   const int blocks = a.rows ? norm_blocks(a.rows, a.cols) : 0;
   if (a.rows && a.cols > kLongRow) {
-    if (a.dx)
+    if (a.dx || a.offs)
       hipLaunchKernelGGL(k_norm_long_backward, dim3(workgroups(a.rows, 4096)), dim3(kThreads), 0, st, a);
     if (a.part)
       hipLaunchKernelGGL(k_norm_columns, dim3((unsigned)((a.cols + kThreads - 1) / kThreads), (unsigned)blocks),

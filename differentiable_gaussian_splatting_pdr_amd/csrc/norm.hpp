@@ -19,6 +19,7 @@ struct Norm {
   void *y, *dx, *dweight, *dbias;
   float *stats;
   float *part;  // [2][blocks][cols]: sums of dy xh, then of dy; null: not wanted
+  float *offs;  // [norm_offsets]: what the mean's rounding left in xh; null: not wanted
   long long rows, ldx, ldy, lddy, lddx;
   int cols, fmt;
   int vec;      // everything begins on 16 bytes in whole groups of 8
@@ -27,6 +28,7 @@ struct Norm {
 hipError_t launch_norm(const Norm &a, hipStream_t st);
 hipError_t launch_norm_backward(const Norm &a, hipStream_t st);
 int norm_blocks(long long rows, long long cols);
+long long norm_offsets(long long rows, long long cols);  // a value each, for dweight
 
 struct Drop {
   const void *x, *res;

@@ -35,3 +35,32 @@ def test_more_columns_than_workgroups_join_at_once():
         want = (gw - gw.mean(1, keepdim=True)) / x.double().std(1, keepdim=True, unbiased=False)
         # (xh mean(gw xh) is below 6 * 8 / sqrt(n) + 2^-7 * 0.8 * 0.8 * 6; the sums as above)
         assert ((dx - want).abs() <= 2.0 ** -7 * want.abs() + 0.06).all()
+
+
+@pytest.mark.parametrize("shift", [1e3, 1e4, -1e5])
+@pytest.mark.parametrize("only_weight", [False, True])
+@pytest.mark.parametrize("cols", [1000, 9001, 20000])
+def test_weight_gradient_far_from_zero(cols, only_weight, shift):
+    # fp32 rows whose mean is 1e3 to 1e5 deviations, under gradients of one sign: an offset that the mean's rounding
+    # leaves in each row would add up.  A thread sums ceil(n / 256) <= 79 values of a row and 8 more follow (at 1000
+    # columns 16 and 6), all sums a unit of 2^-24 off at most: the mean of xh is off by 87 2^-24 mean |xh|, 1 / deviation by
+    # half of that and 4 2^-24 of itself, and each xh by 4 2^-24 of itself.  The sum over rows has at most 2000 / 32 + 32
+    # + 8 steps one after another.
+    rows = 2000
+    g = torch.Generator("cuda").manual_seed(3)
+    x = torch.randn(rows, cols, device="cuda", generator=g) + shift
+    dy = torch.randn(rows, cols, device="cuda", generator=g) + 1.0
+    w = torch.ones(cols, device="cuda", requires_grad=True)
+    c = torch.zeros(cols, device="cuda", requires_grad=True)
+    x.requires_grad_(not only_weight)
+    dw, db = torch.autograd.grad(blocks().layer_norm(x, w, c), (w, c), dy)
+    with torch.no_grad():
+        xh = x.double()
+        xh = (xh - xh.mean(1, keepdim=True)) / ((xh - xh.mean(1, keepdim=True)).square().mean(1, keepdim=True) + 1e-5).sqrt()
+        u = 2.0 ** -24
+        want = (dy.double() * xh).sum(0)
+        off = 87 * u * xh.abs().mean(1, keepdim=True) + (44 + 8) * u * xh.abs()
+        bound = (dy.abs().double() * off).sum(0) + 103 * u * (dy.double() * xh).abs().sum(0) + u * want.abs()
+        assert ((dw - want).abs() <= bound).all(), float(((dw - want).abs() / bound).max())
+        want = dy.double().sum(0)
+        assert ((db - want).abs() <= 104 * u * dy.abs().double().sum(0)).all()
