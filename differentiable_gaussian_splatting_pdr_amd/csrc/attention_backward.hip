@@ -535,9 +535,16 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_kv(Args a
   }
   const int lane_now = lane_again(), half_now = lane_now >> 5, key_now = key0 + wave * 32 + (lane_now & 31);
   if (key_now >= at.stored) return;
-  const bool is_key = key_now < at.nk;
-  store_keys<C, FMT>(a, at, a.dk, 0, head, key_now, dk, half_now, is_key ? a.scale * scaled.out() : 0.f);
-  store_keys<C, FMT>(a, at, a.dv, 1, head, key_now, dv, half_now, is_key ? (FMT == kF16 ? ldexpf(1.f, -kShift) : 1.f) : 0.f);
+  if (key_now >= at.nk) {
+    // no key: zeros, where a row's infinity or NaN has made NaN of weights of zero
+#pragma unroll
+    for (int b = 0; b < C::kBlocks; ++b) {
+      clear(dk[b]);
+      clear(dv[b]);
+    }
+  }
+  store_keys<C, FMT>(a, at, a.dk, 0, head, key_now, dk, half_now, a.scale * scaled.out());
+  store_keys<C, FMT>(a, at, a.dv, 1, head, key_now, dv, half_now, FMT == kF16 ? ldexpf(1.f, -kShift) : 1.f);
 #endif
 }
 
