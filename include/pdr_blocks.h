@@ -34,7 +34,8 @@ extern "C" {
  * zeros and has no gradient.  What a query does not see does not reach its
  * result, whatever it holds.  Nor does it reach gradients across sequences, or
  * from behind a length; but within a causal sequence an infinity or NaN may make
- * gradients not finite that it is masked from, of up to 127 tokens beside it.
+ * gradients not finite that it is masked from, of up to 190 tokens beside it (the
+ * rows of a workgroup, 128, and of a tile, 64, without themselves).
  *
  * Sequences.  Without offsets there are `batch` of them, each of q_rows
  * queries and k_rows keys, *_batch elements apart; key_lengths, if not NULL,

@@ -35,3 +35,32 @@ def test_keys_behind_a_length_have_no_gradient(queries, d, causal, dtype):
         assert not dk[b, n:].any() and not dv[b, n:].any()
         if n:
             assert not torch.isfinite(dv[b, :n]).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("heads", [1, 256])   # 32 and 128 rows to a workgroup
+@pytest.mark.parametrize("more", [0, 1, 100])   # keys, than queries
+def test_how_far_masked_values_reach_in_gradients(more, heads, dtype):
+    # a key at j makes gradients not finite of queries whose last key is not below j - 190; a query, those of keys up to
+    # 190 behind its last one: the 127 other rows of a workgroup of 128, and 63 of a tile of 64
+    n, d, reach = 450, 64, 190
+    q, k, v, dy = (normal(i, 1, m, heads, d, dtype=dtype) for i, m in enumerate((n, n + more, n + more, n)))
+
+    def gradients(*ts):
+        ts = [t.detach().requires_grad_() for t in ts]
+        return torch.autograd.grad(attention(*ts, causal=True), ts, dy)
+
+    clean = gradients(q, k, v)
+    for at in (0, 191, 193, 255, 320, n - 1):
+        x = k.clone()
+        x[0, at + more, 0, 3] = float("nan")
+        far = max(0, at - reach)   # the first query, whose last key is query + more, that it may reach
+        got = gradients(q, x, v)
+        assert torch.equal(got[0][:, :far], clean[0][:, :far])
+        assert torch.isnan(got[0][0, at:, 0]).all()
+        x = q.clone()
+        x[0, at, 0, 3] = float("nan")
+        got = gradients(x, k, v)
+        for i in (1, 2):
+            assert torch.equal(got[i][:, at + more + reach + 1:], clean[i][:, at + more + reach + 1:])
+            assert torch.isnan(got[i][0, :at + more + 1, 0]).all()
