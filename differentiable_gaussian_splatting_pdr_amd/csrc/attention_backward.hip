@@ -42,6 +42,15 @@ __device__ __forceinline__ float dot(i32x4 x, i32x4 y, float s) {
   return s;
 }
 
+// A row whose scores are all -infinity (its lse is +infinity) has no gradient, where
+// ds of zero would make NaN of a key's infinity.
+template <class C>
+__device__ __forceinline__ void clear_empty(f32x16 (&sums)[C::kBlocks], float start_s) {
+  if (start_s != -INFINITY) return;
+#pragma unroll
+  for (int b = 0; b < C::kBlocks; ++b) clear(sums[b]);
+}
+
 // A tile's weights from its scores, and their gradients, in place.  `start`: of the
 // scores in fp32.
 template <int FMT>
@@ -255,6 +264,7 @@ __global__ __launch_bounds__(256, FMT == kF32 ? 1 : 2) void k_backward_q(Args a)
   const int lane_now = lane_again(), row_now = row0 + wave * 32 + (lane_now & 31);
   if (row_now >= rows) return;
   const int n = (int)fdiv((uint32_t)row_now, a.group), g = row_now - n * group;
+  clear_empty<C>(sums, start_s);
   store_columns<C, FMT>(sums, a.dq.p + (first_of(a.dq, at, at.q0 + n, head * group) + g * a.dq.head) * C::kSize, a.dim,
                         lane_now >> 5, a.scale * scaled.out());
 #endif
@@ -390,6 +400,7 @@ __global__ __launch_bounds__(64 * NW) void k_backward_q_few(Args a) {
     across32<C>(sums, sk, 0, s, lanes);
     C::template pace_across<1>();
   }
+  clear_empty<C>(sums, start_s);
   // the waves' sums, where their keys were
   __syncthreads();
   const float by = a.scale * scaled.out();

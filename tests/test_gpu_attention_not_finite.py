@@ -64,3 +64,16 @@ def test_how_far_masked_values_reach_in_gradients(more, heads, dtype):
         for i in (1, 2):
             assert torch.equal(got[i][:, at + more + reach + 1:], clean[i][:, at + more + reach + 1:])
             assert torch.isnan(got[i][0, :at + more + 1, 0]).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("heads", [2, 256])   # 32 and 128 rows to a workgroup
+@pytest.mark.parametrize("causal", [False, True])
+def test_scores_that_are_all_minus_infinity(causal, heads, dtype):
+    # such queries get zeros, and there is no gradient from them
+    n, d = 150, 64
+    q, k, v, dy = (normal(i, 1, n, heads, d, dtype=dtype) for i in range(4))
+    q[..., 7], k[..., 7] = 1.0, -float("inf")
+    ts = [t.requires_grad_() for t in (q, k, v)]
+    y = attention(*ts, causal=causal)
+    assert not any(t.any() for t in (y, *torch.autograd.grad(y, ts, dy)))
