@@ -27,8 +27,12 @@ struct Sizes {
 //   bf16 2 x 512, 8 heads of 128      (64 workgroups)   18 /  49     13 /  47
 //   bf16 4 x 1024, 4 heads of 128    (128)              27 /  73     24 /  68
 //   bf16 8192, 2 heads of 128        (128)             159 / 302    125 / 216
-//   fp32 4 x 1024, 8 heads of 64     (256, causal)      80 / 216     58 / 179
+//   fp32 4 x 1024, 8 heads of 64     (256, causal)      84 / 217     63 / 179
 //   the same, not causal             (256)              79 / 277     89 / 290
+//   fp32 6 x 512, 16 heads of 64     (384, causal)      62 / 184     54 / 185
+//   fp32 2 x 2048, 12 heads of 64    (384, causal)     196 / 498    133 / 494
+//   fp32 3 x 777, 20 heads of 40     (420, causal)      87 / 241     64 / 230
+//   fp32 4096, 15 heads of 32        (480, causal)     399 / 1026   287 / 1041
 //   fp32 4 x 1024, 8 heads of 128    (256, causal)     146 / 395    132 / 438
 //   fp32 8 x 1024, 8 heads of 64     (512, causal)     110 / 305    102 / 319
 inline bool takes_few(const pdr_attention &p) {

@@ -153,9 +153,16 @@ Plan plan_of(const pdr_attention &p) {
 }
 
 // Parts that the rows are cut into for dk and dv, until the card has work; the
-// bytes of their sums.  With 256 rows a part instead of 128, fp16 packed sequences of up
-// to 777 take 74 us instead of 49 (all else within 5 %), with 64 bf16 2 x 512 43
-// instead of 35; with 1024 workgroups fp32 4 x 1024 143 instead of 118.
+// bytes of their sums.  All gradients, us, with parts of at least 64, 128 and 256 rows, and
+// of 128 with 1024 workgroups to aim for:
+//   fp16 7 packed, up to 777, 6 heads of 72, 2 of keys    48   59   80   58
+//   bf16 2 x 512, 8 heads of 128                          47   40   43   40
+//   bf16 2048, 4 heads of 64                              46   46   46   55
+//   fp16 4 x 300, 4 heads of 64                           24   23   23   23
+//   fp32 4 x 1024, 8 heads of 64                         179  179  179  204
+//   fp32 2 x 700, 6 heads of 128, 3 of keys, not causal  256  251  257  250
+//   bf16 8 x 1024, 12 heads of 64, not causal            109  109  110  134
+//   bf16 16384, 2 heads of 128, 1 of keys                765  765  765  738
 constexpr long long kKeyUnits = 512;  // workgroups of 128 keys to aim for
 constexpr long long kKeyRows = 128;   // rows of a part, at least
 int key_splits(const pdr_attention &p, size_t *bytes) {
