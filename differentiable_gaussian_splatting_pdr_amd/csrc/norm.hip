@@ -293,14 +293,14 @@ __global__ __launch_bounds__(kThreads) void k_norm_long(Norm a) {
   }
 }
 
-// dx, if it is wanted, and each row's offset for the columns' sums.
+// dx, and each row's offset for the columns' sums.
 __global__ __launch_bounds__(kThreads) void k_norm_long_backward(Norm a) {
   __shared__ float red[2][4][3];
   int turn = 0;
   for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const float2 st = *(const float2 *)(a.stats + 2 * r);
     float s[3] = {0.f, 0.f, 0.f};
-    for (int pass = 0; pass < (a.dx ? 2 : 1); ++pass) {
+    for (int pass = 0; pass < 2; ++pass) {
       const float off = s[2] * a.by_cols, m = s[0] * a.by_cols, mx = fmaf(-off, m, s[1] * a.by_cols);
       for (int c = threadIdx.x * 8; c < a.cols; c += kThreads * 8) {
         float x[8], g[8], w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
@@ -325,6 +325,32 @@ __global__ __launch_bounds__(kThreads) void k_norm_long_backward(Norm a) {
       if (pass == 0) row_sum<256, 3>(s, red, turn);
     }
     if (a.offs && threadIdx.x == 0) a.offs[r] = s[2] * a.by_cols;
+  }
+}
+
+// The offsets alone, where dx is not wanted: x is read once more (4096 x 16384 bf16, of which
+// part is in the caches: 15 us of 141; the pass above without its second half takes 41).
+__global__ __launch_bounds__(kThreads) void k_norm_offsets(Norm a) {
+  __shared__ float red[2][4][3];
+  int turn = 0;
+  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const float2 st = *(const float2 *)(a.stats + 2 * r);
+    float s[1] = {0.f};
+    if (a.vec) {
+#pragma unroll 2
+      for (int c = threadIdx.x * 8; c < a.cols; c += kThreads * 8) {
+        float x[8];
+        dense::load8(a.x, a.fmt, r * a.ldx + c, 8, true, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[0] += (x[i] - st.x) * st.y;
+      }
+    } else {
+#pragma unroll 8
+      for (int c = threadIdx.x; c < a.cols; c += kThreads)
+        s[0] += (dense::load1(a.x, a.fmt, r * a.ldx + c) - st.x) * st.y;
+    }
+    row_sum<256, 1>(s, red, turn);
+    if (threadIdx.x == 0) a.offs[r] = s[0] * a.by_cols;
   }
 }
 
@@ -448,8 +474,10 @@ hipError_t launch_norm_backward(const Norm &a, hipStream_t st) {
   if (!a.cols) return hipSuccess;
   const int blocks = a.rows ? norm_blocks(a.rows, a.cols) : 0;
   if (a.rows && a.cols > kLongRow) {
-    if (a.dx || a.offs)
+    if (a.dx)
       hipLaunchKernelGGL(k_norm_long_backward, dim3(workgroups(a.rows, 4096)), dim3(kThreads), 0, st, a);
+    else if (a.offs)
+      hipLaunchKernelGGL(k_norm_offsets, dim3(workgroups(a.rows, 4096)), dim3(kThreads), 0, st, a);
     if (a.part)
       hipLaunchKernelGGL(k_norm_columns, dim3((unsigned)((a.cols + kThreads - 1) / kThreads), (unsigned)blocks),
                          dim3(kThreads), 0, st, a, (int)((a.rows + blocks - 1) / blocks));
