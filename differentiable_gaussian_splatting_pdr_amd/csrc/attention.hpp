@@ -296,7 +296,11 @@ struct Core {
     }
   }
 
-  // Eight registers of an along() as the second operand of across().
+  // Eight registers of an along() as the second operand of across().  In 16 bits they are
+  // rounded to the operands' type, which the matrix instruction asks for: an error of the
+  // size of the result's own rounding (bf16 results are 0.0023 from 64 bits, rounded once
+  // they would be 0.0017), where a product of what is lost would be the forward's third
+  // beside two.
   struct Weights {
     i32x4 w[FMT == kF32 ? 2 : 1];
   };
